@@ -13,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,7 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libosdn.so")
 DEBUG_LIB = os.path.join(PKG, "libosdn_debug.so")
-SOURCES = ["osdn_lib.cu"]
+SOURCES = ["osdn_lib.cu", "mixer_lib.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -49,10 +50,10 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True,
     lib = DEBUG_LIB if debug_bounds else LIB
     if not force and up_to_date(lib):
         return lib
-    objs = []
     build_dir = os.path.join(PKG, "_build_debug" if debug_bounds else "_build")
     os.makedirs(build_dir, exist_ok=True)
-    for src in SOURCES:
+
+    def compile_one(src):
         obj = os.path.join(build_dir, src.replace(".cu", ".o"))
         cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                "-Xcompiler", "-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC,
@@ -61,13 +62,17 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True,
             cmd += ["-DOSDN_DEBUG_BOUNDS"]
         if ptxas_verbose:
             cmd += ["-Xptxas", "-v"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError(f"nvcc failed on {src}")
-        if ptxas_verbose or not quiet:
-            sys.stderr.write(r.stderr)
-        objs.append(obj)
+        return src, obj, subprocess.run(cmd, capture_output=True, text=True)
+
+    objs = []
+    with ThreadPoolExecutor(len(SOURCES)) as pool:  # the translation units are independent
+        for src, obj, r in pool.map(compile_one, SOURCES):
+            if r.returncode != 0:
+                sys.stderr.write(r.stdout + r.stderr)
+                raise RuntimeError(f"nvcc failed on {src}")
+            if ptxas_verbose or not quiet:
+                sys.stderr.write(r.stderr)
+            objs.append(obj)
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)

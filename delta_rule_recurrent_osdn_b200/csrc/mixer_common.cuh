@@ -1,0 +1,103 @@
+// mixer_common.cuh -- helpers shared by the layer operators around the token mixer (short
+// convolution, selective scan, block norm): vectors of io elements, SiLU, softplus, and the
+// sequence that holds a row of a packed batch.
+#pragma once
+
+#include <math_constants.h>
+
+#include "common.cuh"
+
+namespace osdn {
+
+// V consecutive io elements <-> fp32 registers, as accesses of up to 16 bytes (V * sizeof(IO)
+// bytes, at least 16 at a time where V allows it).  V == 1 makes no assumption on alignment.
+template <int V, typename IO> struct vec_io {
+    static_assert(V % 4 == 0, "vectors of 4 or 8 elements");
+    static __device__ __forceinline__ void load(const IO* p, float* x) {
+        if constexpr (V == 8 && sizeof(IO) == 2) {
+            const uint4 r = __ldg(reinterpret_cast<const uint4*>(p));
+            const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const float4 v = load4<IO>(p + i);
+                x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+            }
+        }
+    }
+    static __device__ __forceinline__ void store(IO* p, const float* x) {
+        if constexpr (V == 8 && sizeof(IO) == 2) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i += 4)
+                store4<IO>(p + i, make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+        }
+    }
+};
+template <typename IO> struct vec_io<1, IO> {
+    static __device__ __forceinline__ void load(const IO* p, float* x) {
+        x[0] = io_traits<IO>::to_f32(*p);
+    }
+    static __device__ __forceinline__ void store(IO* p, const float* x) {
+        *p = io_traits<IO>::from_f32(x[0]);
+    }
+};
+
+// 1 / (1 + e^-z).  e^-z overflows to inf for z < -88, where the quotient is 0 as it should be.
+__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+__device__ __forceinline__ float silu_f(float z) { return __fdividef(z, 1.f + __expf(-z)); }
+// d silu(z) / dz = s (1 + z (1 - s)), s = sigmoid(z)
+__device__ __forceinline__ float silu_grad_f(float z) {
+    const float s = sigmoid_f(z);
+    return s * fmaf(z, 1.f - s, 1.f);
+}
+
+// The token step of the scan: softplus(raw) = max(raw, 0) + log(1 + e^-|raw|) (which neither
+// overflows nor loses small steps), or raw itself.
+__device__ __forceinline__ float scan_step(float raw, int softplus) {
+    return softplus ? fmaxf(raw, 0.f) + log1pf(expf(-fabsf(raw))) : raw;
+}
+
+__device__ __forceinline__ float warp_sum_f(float x) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
+
+// The sequence that holds row `row` of the [B * T] token rows, and its token range [a, b).
+// Packed offsets are searched by bisection; the range found is checked like seq_range's, so
+// offsets that are out of order give false for the rows they do not describe (the caller skips
+// the row; the error is recorded where every sequence's offsets are checked).
+__device__ __forceinline__ bool row_sequence(const int32_t* __restrict__ cu, int N, int T,
+                                             int64_t row, int& n, int64_t& a, int64_t& b) {
+    if (cu == nullptr) {
+        n = (int)(row / T);
+        a = (int64_t)n * T;
+        b = a + T;
+        return true;
+    }
+    int lo = 0, hi = N;  // the first n with cu[n + 1] > row
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)__ldg(cu + mid + 1) > row) hi = mid; else lo = mid + 1;
+    }
+    if (lo >= N) return false;
+    n = lo;
+    a = __ldg(cu + n);
+    b = __ldg(cu + n + 1);
+    return a >= 0 && a <= row && row < b && b <= T;
+}
+
+}  // namespace osdn

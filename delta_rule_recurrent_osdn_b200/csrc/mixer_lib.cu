@@ -1,0 +1,596 @@
+// mixer_lib.cu -- libosdn: host side of the layer operators around the token mixer (short
+// convolution, selective scan, block norm), declared in include/osdn.h.
+//
+// As in osdn_lib.cu: the host code validates arguments, picks a kernel for the sizes and dtype
+// and enqueues it on the caller's stream; it never allocates and never synchronizes.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "osdn.h"
+#include "common.cuh"
+#include "host_util.cuh"
+#include "conv.cuh"
+#include "norm.cuh"
+#include "ssm_step.cuh"
+#include "ssm_scan.cuh"
+
+namespace osdn {
+
+bool take_mixer_status(int* value) {
+    const int zero = 0;
+    if (cudaMemcpyFromSymbol(value, g_device_status, sizeof(int)) != cudaSuccess) return false;
+    return *value == 0 ||
+           cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int)) == cudaSuccess;
+}
+
+namespace {
+
+struct Buf { const void* p; size_t bytes; };
+
+// Alignment of every buffer, and that no written buffer overlaps any other.
+osdn_status_t check_buffers(const Buf* in, int n_in, const Buf* out, int n_out) {
+    for (int i = 0; i < n_in; ++i)
+        if (in[i].p && !aligned16(in[i].p)) return OSDN_ERR_ALIGNMENT;
+    for (int i = 0; i < n_out; ++i)
+        if (out[i].p && !aligned16(out[i].p)) return OSDN_ERR_ALIGNMENT;
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = 0; j < n_in; ++j)
+            if (overlaps(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return OSDN_ERR_INVALID_ARG;
+        for (int j = i + 1; j < n_out; ++j)
+            if (overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return OSDN_ERR_INVALID_ARG;
+    }
+    return OSDN_OK;
+}
+
+osdn_status_t check_tokens(const int32_t* cu, int32_t num_seqs, int32_t B, int32_t T,
+                           osdn_dtype_t io, int64_t* rows, int64_t* N) {
+    if (io != OSDN_BF16 && io != OSDN_F32) return OSDN_ERR_INVALID_ARG;
+    if (B < 0 || T < 0 || num_seqs < 0) return OSDN_ERR_INVALID_ARG;
+    if (cu && B != 1) return OSDN_ERR_INVALID_ARG;
+    *rows = (int64_t)B * T;
+    *N = cu ? num_seqs : B;
+    // without a sequence there is nothing that packed rows could belong to
+    if (cu && num_seqs == 0 && T > 0) return OSDN_ERR_INVALID_ARG;
+    if (*rows >= (int64_t(1) << 31)) return OSDN_ERR_UNSUPPORTED;
+    return OSDN_OK;
+}
+
+osdn_status_t check_workspace(const void* ws, size_t have, size_t need) {
+    if (need == 0) return OSDN_OK;
+    if (!ws || have < need) return OSDN_ERR_INVALID_ARG;
+    return (reinterpret_cast<uintptr_t>(ws) & 255u) ? OSDN_ERR_ALIGNMENT : OSDN_OK;
+}
+
+// Runs f(constant V, constant W) for the vector width and filter length of a convolution.
+template <typename IO, typename F> osdn_status_t conv_dispatch(int C, int W, bool narrow, F f) {
+    // 16 bytes per access where C keeps rows that aligned, 4 elements where it keeps them 4 apart
+    const int V = C % 8 == 0 && sizeof(IO) == 2 && !narrow ? 8 : C % 4 == 0 ? 4 : 1;
+    auto width = [&](auto v) {
+        switch (W) {
+            case 2: return f(v, std::integral_constant<int, 2>{});
+            case 3: return f(v, std::integral_constant<int, 3>{});
+            default: return f(v, std::integral_constant<int, 4>{});
+        }
+    };
+    if constexpr (sizeof(IO) == 2)
+        if (V == 8) return width(std::integral_constant<int, 8>{});
+    return V == 4 ? width(std::integral_constant<int, 4>{}) : width(std::integral_constant<int, 1>{});
+}
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <typename IO>
+osdn_status_t launch_conv_fwd(const void* x, const float* weight, const float* bias,
+                              const void* state0, int silu, void* y, void* stateT,
+                              const int32_t* cu, int N, int T, int C, int W, int64_t rows,
+                              cudaStream_t stream) {
+    return conv_dispatch<IO>(C, W, false, [&](auto v, auto w) -> osdn_status_t {
+        constexpr int V = decltype(v)::value, WW = decltype(w)::value;
+        const int64_t gx = ceil_div(C, (int64_t)V * CONV_THREADS);
+        // strips of as many tokens as still leave about 1024 threads for every SM
+        int64_t strip = rows * gx * CONV_THREADS / (1024LL * sm_count()) / CONV_UNROLL * CONV_UNROLL;
+        strip = strip < CONV_UNROLL ? CONV_UNROLL : strip > 64 ? 64 : strip;
+        const int64_t least = ceil_div(rows, 32768);
+        strip = strip < least ? least : strip;
+        const int64_t strips = ceil_div(rows, strip);
+        const int64_t tail = cu || stateT ? (N < 4096 ? N : 4096) : 0;
+        if (gx > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
+        if (strips + tail == 0) return OSDN_OK;
+        conv_fwd_kernel<V, WW, IO><<<dim3((unsigned)gx, (unsigned)(strips + tail)),
+                                     dim3(CONV_THREADS), 0, stream>>>(
+            static_cast<const IO*>(x), weight, bias, static_cast<const IO*>(state0), silu,
+            static_cast<IO*>(y), static_cast<IO*>(stateT), cu, N, T, C, rows, (int)strips,
+            (int)strip);
+        return launch_status();
+    });
+}
+
+template <typename IO>
+osdn_status_t launch_conv_step(const void* x, const float* weight, const float* bias, void* state,
+                               int silu, void* y, int N, int C, int W, cudaStream_t stream) {
+    return conv_dispatch<IO>(C, W, false, [&](auto v, auto w) -> osdn_status_t {
+        constexpr int V = decltype(v)::value, WW = decltype(w)::value;
+        const int64_t gx = ceil_div(C, (int64_t)V * CONV_THREADS);
+        conv_step_kernel<V, WW, IO><<<dim3((unsigned)gx, (unsigned)(N < 32768 ? N : 32768)),
+                                      dim3(CONV_THREADS), 0, stream>>>(
+            static_cast<const IO*>(x), weight, bias, static_cast<IO*>(state), silu,
+            static_cast<IO*>(y), N, C);
+        return launch_status();
+    });
+}
+
+// How the backward pass splits the rows: strips of `strip` tokens, CONV_BWD_STRIPS of them a
+// block at a time, row_blocks blocks per group of channels.
+struct ConvBwdPlan { int64_t gx; int strip, row_blocks; };
+ConvBwdPlan conv_bwd_plan(int64_t rows, int C) {
+    ConvBwdPlan pl;
+    const int V = C % 4 == 0 ? 4 : 1;
+    const int sms = 148;  // a constant, so that the workspace's size does not need a device
+    pl.gx = ceil_div(C, 32 * V);
+    pl.strip = 64;
+    while (pl.strip > 8 && ceil_div(rows, CONV_BWD_STRIPS * pl.strip) * pl.gx < 3 * sms) pl.strip /= 2;
+    int64_t most = ceil_div(4 * sms, pl.gx);
+    int64_t rb = ceil_div(rows, CONV_BWD_STRIPS * pl.strip);
+    pl.row_blocks = (int)(rb < 1 ? 1 : rb > most ? most : rb);
+    return pl;
+}
+
+template <typename IO, typename GO>
+osdn_status_t launch_conv_bwd(const void* x, const float* weight, const float* bias,
+                              const void* state0, int silu, const void* dy, const float* dstateT,
+                              void* dx, float* dweight, float* dbias, float* dstate0, float* part,
+                              const int32_t* cu, int N, int T, int C, int W, int64_t rows,
+                              cudaStream_t stream) {
+    const ConvBwdPlan pl = conv_bwd_plan(rows, C);
+    const int64_t tail = cu || dstate0 ? ceil_div(N < 4096 ? N : 4096, CONV_BWD_STRIPS) : 0;
+    const osdn_status_t st = conv_dispatch<IO>(C, W, true, [&](auto v, auto w) -> osdn_status_t {
+        constexpr int V = decltype(v)::value, WW = decltype(w)::value;
+        if constexpr (V <= 4) {
+            conv_bwd_kernel<V, WW, IO, GO>
+                <<<dim3((unsigned)pl.gx, (unsigned)(pl.row_blocks + tail)),
+                   dim3(32, CONV_BWD_STRIPS), 0, stream>>>(
+                    static_cast<const IO*>(x), weight, bias, static_cast<const IO*>(state0), silu,
+                    static_cast<const GO*>(dy), dstateT, static_cast<IO*>(dx), dstate0, part, cu, N,
+                    T, C, rows, pl.row_blocks, pl.strip);
+        }
+        return launch_status();
+    });
+    if (st != OSDN_OK) return st;
+    conv_reduce_kernel<<<dim3((unsigned)ceil_div(C, 32), (unsigned)(W + 1)),
+                         dim3(32, CONV_RED_WARPS), 0, stream>>>(part, pl.row_blocks, W, C, dweight,
+                                                                dbias);
+    return launch_status();
+}
+
+// ---------------------------------------------------------------- block norm
+// Runs f(constant VEC, constant TPR) for rows of D values: TPR threads of NORM_V values each,
+// the smallest power of two that holds a row.
+template <typename F> osdn_status_t norm_dispatch(int D, F f) {
+    const int need = (D + NORM_V - 1) / NORM_V;
+    auto vec = [&](auto tpr) {
+        return D % NORM_V == 0 ? f(std::true_type{}, tpr) : f(std::false_type{}, tpr);
+    };
+    if (need <= 8) return vec(std::integral_constant<int, 8>{});
+    if (need <= 16) return vec(std::integral_constant<int, 16>{});
+    if (need <= 32) return vec(std::integral_constant<int, 32>{});
+    if (need <= 64) return vec(std::integral_constant<int, 64>{});
+    if (need <= 128) return vec(std::integral_constant<int, 128>{});
+    if (need <= 256) return vec(std::integral_constant<int, 256>{});
+    if (need <= 512) return vec(std::integral_constant<int, 512>{});
+    return vec(std::integral_constant<int, 1024>{});
+}
+
+// Blocks of the backward pass (each leaves one partial row of dw_post and dw_next): 1024 threads
+// for every SM, or one block per set of rows.
+int64_t norm_bwd_blocks(int64_t R, int D) {
+    const int need = (D + NORM_V - 1) / NORM_V;
+    int tpr = 8;
+    while (tpr < need) tpr *= 2;
+    const int rows = tpr > 32 ? 1 : 128 / tpr, threads = tpr > 32 ? tpr : 128;
+    const int64_t most = 148LL * (1024 / threads), have = ceil_div(R, rows);
+    return have < most ? have : most;
+}
+
+// ---------------------------------------------------------------- selective scan
+template <int MODE, typename IO>
+osdn_status_t launch_ssm_scan(const SsmArgs& a, int DQ, int DV, cudaStream_t stream) {
+    const int64_t ctas = (int64_t)a.N * a.H * (DV / SSM_BV);
+    if (ctas == 0) return OSDN_OK;
+    if (ctas > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)ctas), block(SSM_THREADS);
+    if (DQ == 128 && DV == 128)
+        ssm_scan_kernel<128, 128, MODE, IO><<<grid, block, 0, stream>>>(a);
+    else if (DQ == 128)
+        ssm_scan_kernel<128, 64, MODE, IO><<<grid, block, 0, stream>>>(a);
+    else if (DV == 128)
+        ssm_scan_kernel<64, 128, MODE, IO><<<grid, block, 0, stream>>>(a);
+    else
+        ssm_scan_kernel<64, 64, MODE, IO><<<grid, block, 0, stream>>>(a);
+    return launch_status();
+}
+
+osdn_status_t check_ssm(int32_t H, int32_t G, int32_t Dk, int32_t Dv) {
+    if (H < 1 || G < 1 || H % G != 0) return OSDN_ERR_INVALID_ARG;
+    if ((Dk != 64 && Dk != 128) || (Dv != 64 && Dv != 128)) return OSDN_ERR_UNSUPPORTED;
+    return OSDN_OK;
+}
+
+// Workspace of osdn_ssm_bwd, each part rounded up to 256 bytes.
+struct SsmBwdWorkspace {
+    size_t dch, dbh, ckpt, gs, pos, rneg, vk, part, total;
+};
+SsmBwdWorkspace ssm_bwd_workspace(int64_t rows, int64_t N, int32_t H, int32_t Dk, int32_t Dv) {
+    SsmBwdWorkspace w;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += up256(bytes);
+        return at;
+    };
+    const size_t th = (size_t)rows * H, slots = (size_t)ssm_slots(rows, N, SSM_BLOCK);
+    w.dch = take(th * Dk * 4);
+    w.dbh = take(th * Dk * 4);
+    w.ckpt = take(slots * H * Dk * Dv * 4);
+    w.gs = take(slots * H * (Dk / SSM_BV) * 4);
+    w.pos = take(th * 4);
+    w.rneg = take(th * 4);
+    w.vk = take(th * 4);
+    w.part = take((size_t)3 * N * H * 8);
+    w.total = off;
+    return w;
+}
+
+template <typename IO>
+osdn_status_t launch_ssm_bwd(const void* x, const float* dt, const float* A, const void* b,
+                             const void* c, const float* D, const float* dt_bias, int softplus,
+                             const float* S0, const void* dy, const float* dST, void* dx,
+                             float* ddt, float* dA, void* db, void* dc, float* dD, float* ddt_bias,
+                             float* dS0, const int32_t* cu, int64_t N, int T, int H, int G, int Dk,
+                             int Dv, int64_t rows, uint8_t* ws, cudaStream_t stream) {
+    const SsmBwdWorkspace w = ssm_bwd_workspace(rows, N, H, Dk, Dv);
+    auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
+    SsmArgs a = {};
+    a.dt = dt; a.A = A; a.D = D; a.dt_bias = dt_bias; a.softplus = softplus;
+    a.cu = cu; a.rows = rows; a.N = (int)N; a.T = T; a.H = H; a.G = G;
+    a.ckpt = f32(w.ckpt);
+    a.gs = f32(w.gs);
+    SsmArgs dcp = a, dxp = a, dbp = a;
+    dcp.q = dy; dcp.k = x; dcp.v = b; dcp.S_in = S0; dcp.out = f32(w.dch); dcp.vk = dD ? f32(w.vk) : nullptr;
+    dxp.q = b; dxp.k = c; dxp.v = dy; dxp.S_in = dST; dxp.out = dx; dxp.S_out = dS0;
+    dbp.q = x; dbp.k = dy; dbp.v = c; dbp.S_in = dST; dbp.out = f32(w.dbh);
+    osdn_status_t st = launch_ssm_scan<SSM_DC, IO>(dcp, Dv, Dk, stream);
+    if (st == OSDN_OK) st = launch_ssm_scan<SSM_DX, IO>(dxp, Dk, Dv, stream);
+    if (st == OSDN_OK) st = launch_ssm_scan<SSM_DB, IO>(dbp, Dv, Dk, stream);
+    if (st != OSDN_OK) return st;
+    if (rows > 0) {
+        const int64_t need = ceil_div(rows * G, 8), cap = 16LL * sm_count();
+        const dim3 grid((unsigned)(need < cap ? need : cap));
+        if (Dk == 128)
+            ssm_group_kernel<128, IO><<<grid, 256, 0, stream>>>(
+                f32(w.dch), f32(w.dbh), static_cast<const IO*>(b), static_cast<const IO*>(c), dt,
+                dt_bias, softplus, static_cast<IO*>(db), static_cast<IO*>(dc), f32(w.pos),
+                f32(w.rneg), rows, H, G);
+        else
+            ssm_group_kernel<64, IO><<<grid, 256, 0, stream>>>(
+                f32(w.dch), f32(w.dbh), static_cast<const IO*>(b), static_cast<const IO*>(c), dt,
+                dt_bias, softplus, static_cast<IO*>(db), static_cast<IO*>(dc), f32(w.pos),
+                f32(w.rneg), rows, H, G);
+        st = launch_status();
+        if (st != OSDN_OK) return st;
+    }
+    double* part = reinterpret_cast<double*>(ws + w.part);
+    if (N > 0) {
+        ssm_gate_kernel<<<dim3((unsigned)(N * H)), dim3(32 * SSM_GATE_WARPS), 0, stream>>>(
+            f32(w.pos), f32(w.rneg), f32(w.gs), Dk / SSM_BV, dcp.vk, dt, A, dt_bias, softplus, ddt,
+            part, cu, (int)N, T, H, rows);
+        st = launch_status();
+        if (st != OSDN_OK) return st;
+    }
+    ssm_param_kernel<<<3, 256, 0, stream>>>(part, (int)N, H, dA, dD, ddt_bias);
+    return launch_status();
+}
+
+}  // namespace
+}  // namespace osdn
+
+using namespace osdn;
+
+extern "C" {
+
+// ---------------------------------------------------------------- short causal convolution
+osdn_status_t osdn_conv_fwd(const void* x, const float* weight, const float* bias,
+                            const void* state0, int32_t silu, void* y, void* stateT,
+                            const int32_t* cu_seqlens, int32_t num_seqs, int32_t B, int32_t T,
+                            int32_t C, int32_t W, osdn_dtype_t io, void* stream) {
+    int64_t rows, N;
+    osdn_status_t st = check_tokens(cu_seqlens, num_seqs, B, T, io, &rows, &N);
+    if (st != OSDN_OK) return st;
+    if (C < 1 || (silu != 0 && silu != 1)) return OSDN_ERR_INVALID_ARG;
+    if (W < 2 || W > 4) return OSDN_ERR_UNSUPPORTED;
+    if (!weight || (rows > 0 && (!x || !y))) return OSDN_ERR_INVALID_ARG;
+    const size_t es = io_size(io), xb = (size_t)rows * C * es, sb = (size_t)N * (W - 1) * C * es;
+    const Buf in[] = {{x, xb}, {weight, (size_t)C * W * 4}, {bias, (size_t)C * 4}, {state0, sb},
+                      {cu_seqlens, ((size_t)N + 1) * 4}};
+    const Buf out[] = {{y, xb}, {stateT, sb}};
+    st = check_buffers(in, 5, out, 2);
+    if (st != OSDN_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (io == OSDN_BF16)
+        return launch_conv_fwd<__nv_bfloat16>(x, weight, bias, state0, silu, y, stateT, cu_seqlens,
+                                              (int)N, T, C, W, rows, s);
+    return launch_conv_fwd<float>(x, weight, bias, state0, silu, y, stateT, cu_seqlens, (int)N, T, C,
+                                  W, rows, s);
+}
+
+osdn_status_t osdn_conv_step(const void* x, const float* weight, const float* bias, void* state,
+                             int32_t silu, void* y, int32_t N, int32_t C, int32_t W,
+                             osdn_dtype_t io, void* stream) {
+    if (io != OSDN_BF16 && io != OSDN_F32) return OSDN_ERR_INVALID_ARG;
+    if (N < 0 || C < 1 || (silu != 0 && silu != 1)) return OSDN_ERR_INVALID_ARG;
+    if (W < 2 || W > 4) return OSDN_ERR_UNSUPPORTED;
+    if (N == 0) return OSDN_OK;
+    if (!x || !weight || !state || !y) return OSDN_ERR_INVALID_ARG;
+    const size_t xb = (size_t)N * C * io_size(io);
+    const Buf in[] = {{x, xb}, {weight, (size_t)C * W * 4}, {bias, (size_t)C * 4}};
+    const Buf out[] = {{y, xb}, {state, xb * (W - 1)}};
+    const osdn_status_t st = check_buffers(in, 3, out, 2);
+    if (st != OSDN_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (io == OSDN_BF16)
+        return launch_conv_step<__nv_bfloat16>(x, weight, bias, state, silu, y, N, C, W, s);
+    return launch_conv_step<float>(x, weight, bias, state, silu, y, N, C, W, s);
+}
+
+size_t osdn_conv_bwd_workspace_bytes(int32_t B, int32_t T, int32_t C, int32_t W) {
+    if (B < 0 || T < 0 || C < 1 || W < 2 || W > 4) return 0;
+    return up256((size_t)conv_bwd_plan((int64_t)B * T, C).row_blocks * (W + 1) * C * 4);
+}
+
+osdn_status_t osdn_conv_bwd(const void* x, const float* weight, const float* bias,
+                            const void* state0, int32_t silu, const void* dy, osdn_dtype_t dy_io,
+                            const float* dstateT, void* dx, float* dweight, float* dbias,
+                            float* dstate0, const int32_t* cu_seqlens, int32_t num_seqs, int32_t B,
+                            int32_t T, int32_t C, int32_t W, osdn_dtype_t io, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    int64_t rows, N;
+    osdn_status_t st = check_tokens(cu_seqlens, num_seqs, B, T, io, &rows, &N);
+    if (st != OSDN_OK) return st;
+    if (C < 1 || (silu != 0 && silu != 1) || (dy_io != OSDN_F32 && dy_io != io))
+        return OSDN_ERR_INVALID_ARG;
+    if (W < 2 || W > 4) return OSDN_ERR_UNSUPPORTED;
+    if (!weight || !dweight || (rows > 0 && (!x || !dy || !dx))) return OSDN_ERR_INVALID_ARG;
+    const size_t need = osdn_conv_bwd_workspace_bytes(B, T, C, W);
+    st = check_workspace(workspace, workspace_bytes, need);
+    if (st != OSDN_OK) return st;
+    const size_t es = io_size(io), xb = (size_t)rows * C * es, sb = (size_t)N * (W - 1) * C;
+    const Buf in[] = {{x, xb}, {weight, (size_t)C * W * 4}, {bias, (size_t)C * 4}, {state0, sb * es},
+                      {dy, (size_t)rows * C * io_size(dy_io)}, {dstateT, sb * 4},
+                      {cu_seqlens, ((size_t)N + 1) * 4}};
+    const Buf out[] = {{dx, xb}, {dweight, (size_t)C * W * 4}, {dbias, (size_t)C * 4},
+                       {dstate0, sb * 4}, {workspace, need}};
+    st = check_buffers(in, 7, out, 5);
+    if (st != OSDN_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    float* part = static_cast<float*>(workspace);
+    if (io == OSDN_F32)
+        return launch_conv_bwd<float, float>(x, weight, bias, state0, silu, dy, dstateT, dx, dweight,
+                                             dbias, dstate0, part, cu_seqlens, (int)N, T, C, W, rows,
+                                             s);
+    if (dy_io == OSDN_F32)
+        return launch_conv_bwd<__nv_bfloat16, float>(x, weight, bias, state0, silu, dy, dstateT, dx,
+                                                     dweight, dbias, dstate0, part, cu_seqlens,
+                                                     (int)N, T, C, W, rows, s);
+    return launch_conv_bwd<__nv_bfloat16, __nv_bfloat16>(x, weight, bias, state0, silu, dy, dstateT,
+                                                         dx, dweight, dbias, dstate0, part,
+                                                         cu_seqlens, (int)N, T, C, W, rows, s);
+}
+
+// ---------------------------------------------------------------- selective scan
+osdn_status_t osdn_ssm_fwd(const void* x, const float* dt, const float* A, const void* b,
+                           const void* c, const float* D, const float* dt_bias, int32_t softplus,
+                           const float* S0, void* y, float* ST, const int32_t* cu_seqlens,
+                           int32_t num_seqs, int32_t B, int32_t T, int32_t H, int32_t G, int32_t Dk,
+                           int32_t Dv, osdn_dtype_t io, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    int64_t rows, N;
+    osdn_status_t st = check_tokens(cu_seqlens, num_seqs, B, T, io, &rows, &N);
+    if (st == OSDN_OK) st = check_ssm(H, G, Dk, Dv);
+    if (st != OSDN_OK) return st;
+    if (softplus != 0 && softplus != 1) return OSDN_ERR_INVALID_ARG;
+    if (!A || (rows > 0 && (!x || !dt || !b || !c || !y))) return OSDN_ERR_INVALID_ARG;
+    const size_t need = osdn_ssm_fwd_workspace_bytes(num_seqs, B, T, H, Dk, Dv, io);
+    st = check_workspace(workspace, workspace_bytes, need);
+    if (st != OSDN_OK) return st;
+    const size_t es = io_size(io), xb = (size_t)rows * H * Dv * es, gb = (size_t)rows * G * Dk * es,
+                 sb = (size_t)N * H * Dv * Dk * 4, hb = (size_t)H * 4;
+    const Buf in[] = {{x, xb}, {dt, rows * hb}, {A, hb}, {b, gb}, {c, gb}, {D, hb}, {dt_bias, hb},
+                      {S0, sb}, {cu_seqlens, ((size_t)N + 1) * 4}};
+    const Buf out[] = {{y, xb}, {ST, sb}, {need ? workspace : nullptr, need}};
+    st = check_buffers(in, 9, out, 3);
+    if (st != OSDN_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    SsmArgs a = {};
+    a.q = c; a.k = b; a.v = x; a.dt = dt; a.A = A; a.D = D; a.dt_bias = dt_bias; a.S_in = S0;
+    a.out = y; a.S_out = ST; a.cu = cu_seqlens; a.rows = rows; a.N = (int)N; a.T = T; a.H = H;
+    a.G = G; a.softplus = softplus;
+    if (io == OSDN_BF16) return launch_ssm_scan<SSM_FWD, __nv_bfloat16>(a, Dk, Dv, s);
+    return launch_ssm_scan<SSM_FWD, float>(a, Dk, Dv, s);
+}
+
+size_t osdn_ssm_fwd_workspace_bytes(int32_t, int32_t, int32_t, int32_t, int32_t, int32_t,
+                                    osdn_dtype_t) {
+    return 0;
+}
+
+osdn_status_t osdn_ssm_step(const void* x, const float* dt, const float* A, const void* b,
+                            const void* c, const float* D, const float* dt_bias, int32_t softplus,
+                            float* S, void* y, int32_t N, int32_t H, int32_t G, int32_t Dk,
+                            int32_t Dv, osdn_dtype_t io, void* stream) {
+    if (io != OSDN_BF16 && io != OSDN_F32) return OSDN_ERR_INVALID_ARG;
+    if (N < 0 || (softplus != 0 && softplus != 1)) return OSDN_ERR_INVALID_ARG;
+    osdn_status_t st = check_ssm(H, G, Dk, Dv);
+    if (st != OSDN_OK) return st;
+    const int64_t nh = (int64_t)N * H;
+    if (nh == 0) return OSDN_OK;
+    if (nh > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
+    if (!x || !dt || !A || !b || !c || !S || !y) return OSDN_ERR_INVALID_ARG;
+    const size_t es = io_size(io), xb = (size_t)nh * Dv * es, gb = (size_t)N * G * Dk * es,
+                 hb = (size_t)H * 4;
+    const Buf in[] = {{x, xb}, {dt, N * hb}, {A, hb}, {b, gb}, {c, gb}, {D, hb}, {dt_bias, hb}};
+    const Buf out[] = {{y, xb}, {S, (size_t)nh * Dv * Dk * 4}};
+    st = check_buffers(in, 7, out, 2);
+    if (st != OSDN_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto launch = [&](auto dk, auto dv, auto zero) {
+        using IO = decltype(zero);
+        constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value;
+        ssm_step_kernel<DK, DV, IO><<<dim3((unsigned)nh), dim3(DV * 4), 0, s>>>(
+            static_cast<const IO*>(x), dt, A, static_cast<const IO*>(b), static_cast<const IO*>(c), D,
+            dt_bias, softplus, S, static_cast<IO*>(y), nh, H, G);
+        return launch_status();
+    };
+    auto dims = [&](auto zero) {
+        using c64 = std::integral_constant<int, 64>;
+        using c128 = std::integral_constant<int, 128>;
+        if (Dk == 128)
+            return Dv == 128 ? launch(c128{}, c128{}, zero) : launch(c128{}, c64{}, zero);
+        return Dv == 128 ? launch(c64{}, c128{}, zero) : launch(c64{}, c64{}, zero);
+    };
+    return io == OSDN_BF16 ? dims(__nv_bfloat16{}) : dims(0.f);
+}
+
+size_t osdn_ssm_bwd_workspace_bytes(int32_t num_seqs, int32_t B, int32_t T, int32_t H, int32_t Dk,
+                                    int32_t Dv, osdn_dtype_t io) {
+    if (B < 0 || T < 0 || H < 1 || num_seqs < 0 || (Dk != 64 && Dk != 128) ||
+        (Dv != 64 && Dv != 128) || (io != OSDN_BF16 && io != OSDN_F32))
+        return 0;
+    return ssm_bwd_workspace((int64_t)B * T, num_seqs > 0 ? num_seqs : B, H, Dk, Dv).total;
+}
+
+osdn_status_t osdn_ssm_bwd(const void* x, const float* dt, const float* A, const void* b,
+                           const void* c, const float* D, const float* dt_bias, int32_t softplus,
+                           const float* S0, const void* dy, const float* dST, void* dx, float* ddt,
+                           float* dA, void* db, void* dc, float* dD, float* ddt_bias, float* dS0,
+                           const int32_t* cu_seqlens, int32_t num_seqs, int32_t B, int32_t T,
+                           int32_t H, int32_t G, int32_t Dk, int32_t Dv, osdn_dtype_t io,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+    int64_t rows, N;
+    osdn_status_t st = check_tokens(cu_seqlens, num_seqs, B, T, io, &rows, &N);
+    if (st == OSDN_OK) st = check_ssm(H, G, Dk, Dv);
+    if (st != OSDN_OK) return st;
+    if (softplus != 0 && softplus != 1) return OSDN_ERR_INVALID_ARG;
+    if (!A || !dA || (rows > 0 && (!x || !dt || !b || !c || !dy || !dx || !ddt || !db || !dc)))
+        return OSDN_ERR_INVALID_ARG;
+    const size_t need = ssm_bwd_workspace(rows, N, H, Dk, Dv).total;
+    st = check_workspace(workspace, workspace_bytes, need);
+    if (st != OSDN_OK) return st;
+    if (N * H > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
+    const size_t es = io_size(io), xb = (size_t)rows * H * Dv * es, gb = (size_t)rows * G * Dk * es,
+                 sb = (size_t)N * H * Dv * Dk * 4, hb = (size_t)H * 4;
+    const Buf in[] = {{x, xb}, {dt, rows * hb}, {A, hb}, {b, gb}, {c, gb}, {D, hb}, {dt_bias, hb},
+                      {S0, sb}, {dy, xb}, {dST, sb}, {cu_seqlens, ((size_t)N + 1) * 4}};
+    const Buf out[] = {{dx, xb}, {ddt, rows * hb}, {dA, hb}, {db, gb}, {dc, gb}, {dD, hb},
+                       {ddt_bias, hb}, {dS0, sb}, {workspace, need}};
+    st = check_buffers(in, 11, out, 9);
+    if (st != OSDN_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    if (io == OSDN_BF16)
+        return launch_ssm_bwd<__nv_bfloat16>(x, dt, A, b, c, D, dt_bias, softplus, S0, dy, dST, dx,
+                                             ddt, dA, db, dc, dD, ddt_bias, dS0, cu_seqlens, N, T, H,
+                                             G, Dk, Dv, rows, ws, s);
+    return launch_ssm_bwd<float>(x, dt, A, b, c, D, dt_bias, softplus, S0, dy, dST, dx, ddt, dA, db,
+                                 dc, dD, ddt_bias, dS0, cu_seqlens, N, T, H, G, Dk, Dv, rows, ws, s);
+}
+
+// ---------------------------------------------------------------- block norm
+osdn_status_t osdn_norm_fwd(const void* f, const void* x, const void* gate, const float* w_post,
+                            const float* w_next, int32_t gate_act, int32_t gate_first, float scale,
+                            float eps, void* x_out, void* h, int64_t R, int32_t D, osdn_dtype_t io,
+                            void* stream) {
+    if (io != OSDN_BF16 && io != OSDN_F32) return OSDN_ERR_INVALID_ARG;
+    if (R < 0 || D < 1 || (gate_act != 0 && gate_act != 1) || (gate_first != 0 && gate_first != 1))
+        return OSDN_ERR_INVALID_ARG;
+    if (D > NORM_MAX_D) return OSDN_ERR_UNSUPPORTED;
+    if (R == 0) return OSDN_OK;
+    if (!f || (w_next ? !h : h || !x_out)) return OSDN_ERR_INVALID_ARG;
+    const size_t rb = (size_t)R * D * io_size(io), wb = (size_t)D * 4;
+    const Buf in[] = {{f, rb}, {x, rb}, {gate, rb}, {w_post, wb}, {w_next, wb}};
+    const Buf out[] = {{x_out, rb}, {h, rb}};
+    const osdn_status_t st = check_buffers(in, 5, out, 2);
+    if (st != OSDN_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto go = [&](auto zero) {
+        using IO = decltype(zero);
+        return norm_dispatch(D, [&](auto vec, auto tpr) {
+            constexpr int TPR = decltype(tpr)::value;
+            constexpr int ROWS = TPR > 32 ? 1 : 128 / TPR, THREADS = TPR > 32 ? TPR : 128;
+            const int64_t need = ceil_div(R, ROWS), cap = 64LL * sm_count();
+            norm_fwd_kernel<decltype(vec)::value, TPR, IO>
+                <<<dim3((unsigned)(need < cap ? need : cap)), dim3(THREADS), 0, s>>>(
+                    static_cast<const IO*>(f), static_cast<const IO*>(x),
+                    static_cast<const IO*>(gate), w_post, w_next, gate_act, gate_first, scale, eps,
+                    static_cast<IO*>(x_out), static_cast<IO*>(h), R, D);
+            return launch_status();
+        });
+    };
+    return io == OSDN_BF16 ? go(__nv_bfloat16{}) : go(0.f);
+}
+
+size_t osdn_norm_bwd_workspace_bytes(int64_t R, int32_t D) {
+    if (R < 0 || D < 1 || D > NORM_MAX_D) return 0;
+    return up256((size_t)2 * norm_bwd_blocks(R, D) * D * 4);
+}
+
+osdn_status_t osdn_norm_bwd(const void* f, const void* x, const void* gate, const float* w_post,
+                            const float* w_next, int32_t gate_act, int32_t gate_first, float scale,
+                            float eps, const void* dx_out, const void* dh, void* df, void* dx,
+                            void* dgate, float* dw_post, float* dw_next, int64_t R, int32_t D,
+                            osdn_dtype_t io, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+    if (io != OSDN_BF16 && io != OSDN_F32) return OSDN_ERR_INVALID_ARG;
+    if (R < 0 || D < 1 || (gate_act != 0 && gate_act != 1) || (gate_first != 0 && gate_first != 1))
+        return OSDN_ERR_INVALID_ARG;
+    if (D > NORM_MAX_D) return OSDN_ERR_UNSUPPORTED;
+    if ((w_post != nullptr) != (dw_post != nullptr) || (w_next != nullptr) != (dw_next != nullptr))
+        return OSDN_ERR_INVALID_ARG;
+    if (R > 0 && (!f || !df || (!dx_out && !dh) || (w_next != nullptr) != (dh != nullptr) ||
+                  (gate != nullptr) != (dgate != nullptr) || (!x && dx)))
+        return OSDN_ERR_INVALID_ARG;
+    const size_t need = osdn_norm_bwd_workspace_bytes(R, D);
+    osdn_status_t st = check_workspace(workspace, workspace_bytes, need);
+    if (st != OSDN_OK) return st;
+    const size_t rb = (size_t)R * D * io_size(io), wb = (size_t)D * 4;
+    const Buf in[] = {{f, rb}, {x, rb}, {gate, rb}, {w_post, wb}, {w_next, wb}, {dx_out, rb}, {dh, rb}};
+    const Buf out[] = {{df, rb}, {dx, rb}, {dgate, rb}, {dw_post, wb}, {dw_next, wb},
+                       {workspace, need}};
+    st = check_buffers(in, 7, out, 6);
+    if (st != OSDN_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    float* part = static_cast<float*>(workspace);
+    const int64_t blocks = norm_bwd_blocks(R, D);
+    if (blocks > 0) {
+        auto go = [&](auto zero) {
+            using IO = decltype(zero);
+            return norm_dispatch(D, [&](auto vec, auto tpr) {
+                constexpr int TPR = decltype(tpr)::value;
+                norm_bwd_kernel<decltype(vec)::value, TPR, IO>
+                    <<<dim3((unsigned)blocks), dim3(TPR > 32 ? TPR : 128), 0, s>>>(
+                        static_cast<const IO*>(f), static_cast<const IO*>(x),
+                        static_cast<const IO*>(gate), w_post, w_next, gate_act, gate_first, scale,
+                        eps, static_cast<const IO*>(dx_out), static_cast<const IO*>(dh),
+                        static_cast<IO*>(df), static_cast<IO*>(dx), static_cast<IO*>(dgate), part, R,
+                        D);
+                return launch_status();
+            });
+        };
+        st = io == OSDN_BF16 ? go(__nv_bfloat16{}) : go(0.f);
+        if (st != OSDN_OK) return st;
+    }
+    if (!dw_post && !dw_next) return OSDN_OK;
+    norm_reduce_kernel<<<dim3((unsigned)ceil_div(D, 32), 2), dim3(32, NORM_RED_WARPS), 0, s>>>(
+        part, (int)blocks, D, dw_post, dw_next);
+    return launch_status();
+}
+
+}  // extern "C"

@@ -1,6 +1,7 @@
 // osdn_lib.cu -- libosdn: host side of the C ABI declared in include/osdn.h.
 //
-// One translation unit holds every kernel (so the device status word is a single symbol).
+// One translation unit holds the mixer's kernels, mixer_lib.cu the layer operators around it;
+// each has its own device status word, and osdn_get_device_status reads both.
 // The host code validates arguments, picks a kernel for the sizes and dtype, and enqueues it
 // on the caller's stream.  It never allocates memory and never synchronizes, except in
 // osdn_get_device_status, whose job is to synchronize.
@@ -12,6 +13,7 @@
 
 #include "osdn.h"
 #include "common.cuh"
+#include "host_util.cuh"
 #include "scan_warp.cuh"
 #include "chunk_simt.cuh"
 #include "watchdog.cuh"
@@ -24,16 +26,6 @@
 
 namespace osdn {
 namespace {
-
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
-inline size_t io_size(osdn_dtype_t io) { return io == OSDN_BF16 ? 2 : 4; }
 
 struct Dims {
     int32_t B, T, H, Dk, Dv, N;
@@ -54,16 +46,6 @@ osdn_status_t check_common(const int32_t* cu, int32_t num_seqs, int32_t B, int32
     d.Dv = Dk;
     d.N = cu ? num_seqs : B;
     return OSDN_OK;
-}
-
-inline osdn_status_t launch_status() {
-    return cudaGetLastError() == cudaSuccess ? OSDN_OK : OSDN_ERR_CUDA;
-}
-
-template <typename KernelT>
-inline bool set_smem(KernelT kernel, size_t bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)bytes) == cudaSuccess;
 }
 
 // ---------------------------------------------------------------- phase 1 dispatch
@@ -168,14 +150,6 @@ bool make_td_map(CUtensorMap* m, const void* base, int H, int64_t rows) {
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-        return 148;
-    return n;
 }
 
 // Phase 1, bf16 with 128 key channels: T_d of every chunk (prep kernel, written into the k~
@@ -620,8 +594,6 @@ struct BwdWorkspace {
     size_t kt, dall, state, fw, dq, dk, dkt, dbeta, deta, total;
 };
 
-inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-
 BwdWorkspace bwd_workspace(int64_t rows, int64_t N, int32_t H, int32_t Dk, int32_t Dv,
                            osdn_dtype_t io) {
     BwdWorkspace w;
@@ -798,7 +770,9 @@ osdn_status_t osdn_get_device_status(void* stream) {
         return OSDN_ERR_CUDA;
     if (value != 0 && cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int)) != cudaSuccess)
         return OSDN_ERR_CUDA;
-    return static_cast<osdn_status_t>(value);
+    int layer = 0;
+    if (!osdn::take_mixer_status(&layer)) return OSDN_ERR_CUDA;
+    return static_cast<osdn_status_t>(value != 0 ? value : layer);
 }
 
 osdn_status_t osdn_debug_watchdog_selftest(int64_t spin_limit, void* stream) {

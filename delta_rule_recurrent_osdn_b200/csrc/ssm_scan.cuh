@@ -1,0 +1,384 @@
+// ssm_scan.cuh -- the selective state-space scan and its gradient, token by token in fp32.
+//
+// Per (sequence, head), with step_t = softplus(dt_t + dt_bias), a_t = exp(step_t A):
+//   S_t = a_t S_{t-1} + step_t x_t b_t^T,    y_t = S_t c_t + D x_t.
+// As a map of three token streams, y = F(c, b, step x) with
+//   F(q, k, v)_i = sum_{j <= i} (prod_{j < s <= i} a_s) (q_i . k_j) v_j  + (decayed S_0) q_i,
+// and the gradient is the same map three more times:
+//   dc = F(dy, x, step b) with the transposed state (forward in time),
+//   dx = step F'(b, c, dy) + D dy,  db = step F'(x, dy, c)  with F' = F in reverse time,
+//        R_j = k_j v_j^T summed over i >= j with decay prod_{j < s <= i} a_s, carry a_j R_j.
+// For the steps: with pos_i = c_i . dc_i and neg_j = b_j . db_j (the head's own share of dc, db),
+//   d(log a_t) = sum_{i >= t} pos_i - sum_{j >= t} neg_j + <G, S>,
+// the sums running to the end of t's block of SSM_BLOCK tokens and <G, S> taken there between
+// the state S and the gradient G that reaches it from later tokens (so nothing is summed over
+// more than a block: the two sums nearly cancel over long stretches), and
+//   dstep_t = x_t . (dx_t - D dy_t) / step_t + A d(log a_t)   (the quotient is formed unscaled).
+//
+// One kernel serves all four: a CTA holds 32 rows of the state (DV channels of v) in registers,
+// 4 threads a row, each with DQ / 4 columns, and walks the tokens; tiles of q, k, v are staged in
+// shared memory, the next tile's loads in flight while one is used.  3 fp32 operations per state
+// element and token (2 packed FMA-pipe instructions per 2 elements) against 16 bytes of shared
+// memory per 8: bound by FMA issue and, for few (sequence, head) pairs, by the chain of tokens.
+#pragma once
+
+#include "mixer_common.cuh"
+
+namespace osdn {
+
+constexpr int SSM_TT = 16;        // tokens per staged tile
+constexpr int SSM_BV = 32;        // state rows per CTA
+constexpr int SSM_THREADS = 128;
+constexpr int SSM_BLOCK = 64;     // tokens between two restarts of the step gradient's sums
+
+enum { SSM_FWD = 0, SSM_DC = 1, SSM_DX = 2, SSM_DB = 3 };
+
+struct SsmArgs {
+    const void *q, *k, *v;        // io streams [rows][heads][.]
+    const float *dt, *A, *D, *dt_bias;
+    const float *S_in;            // FWD, DC: S0; DX, DB: dST; may be null
+    void* out;                    // FWD: y, DX: dx (io); DC, DB: fp32 per head [rows][H][DV]
+    float* S_out;                 // FWD: ST, DX: dS0; may be null
+    float* ckpt;                  // DC writes, DB reads: S behind each block [slot][H][DV][DQ]
+    float* gs;                    // DB: <G, S> behind each block [DV / 32][slot][H]
+    float* vk;                    // DC: dy . x per token [H][rows], or null
+    const int32_t* cu;
+    int64_t rows;
+    int N, T, H, G, softplus;
+};
+
+// Blocks of SSM_BLOCK tokens of all sequences are numbered so that sequence n's start at
+// first / SSM_BLOCK + n: no two share a number, and rows / SSM_BLOCK + N + 1 numbers suffice.
+__host__ __device__ __forceinline__ int64_t ssm_slots(int64_t rows, int64_t N, int block) {
+    return rows / block + N + 1;
+}
+
+template <int DQ, int DV, int MODE, typename IO>
+__global__ void __launch_bounds__(SSM_THREADS)
+ssm_scan_kernel(const SsmArgs p) {
+    constexpr bool REV = MODE == SSM_DX || MODE == SSM_DB;   // reverse time
+    constexpr bool TRANS = MODE == SSM_DC || MODE == SSM_DB; // state rows are key channels
+    constexpr int NF = DQ / 16;                              // float4 per thread and state row
+    constexpr int LQ = SSM_TT * DQ / 4 / SSM_THREADS;        // float4 of q (k) a thread stages
+    using tr = io_traits<IO>;
+    __shared__ float4 qs[SSM_TT][DQ / 4], ks[SSM_TT][DQ / 4];
+    __shared__ float vs[SSM_TT][SSM_BV], os[SSM_TT][SSM_BV];
+    __shared__ float as[SSM_TT], st[SSM_TT];
+    __shared__ float part[SSM_THREADS / 32];
+
+    constexpr int NSL = DV / SSM_BV;
+    const int slice = blockIdx.x % NSL;
+    const int64_t nh = blockIdx.x / NSL;
+    const int n = (int)(nh / p.H), h = (int)(nh - (int64_t)n * p.H);
+    int64_t first, count;
+    if (!seq_range(p.cu, n, p.N, p.T, first, count)) return;  // uniform over the CTA
+    const int g = h / (p.H / p.G);
+    // heads of the streams: FWD q = c, k = b, v = x; DC q = dy, k = x, v = b; DX q = b, k = c,
+    // v = dy; DB q = x, k = dy, v = c.  b and c have G heads, x and dy H.
+    const int qh = TRANS ? p.H : p.G, vh = TRANS ? p.G : p.H;
+    const int64_t qstride = (int64_t)qh * DQ, vstride = (int64_t)vh * DV;
+    const IO* q = static_cast<const IO*>(p.q) + (TRANS ? h : g) * DQ;
+    const IO* k = static_cast<const IO*>(p.k) + (TRANS ? h : g) * DQ;
+    const IO* v = static_cast<const IO*>(p.v) + (TRANS ? g : h) * DV + slice * SSM_BV;
+    const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+    const float skip = !TRANS && p.D ? p.D[h] : 0.f;
+
+    const int tid = threadIdx.x, row = tid >> 2, quarter = tid & 3;
+    const int vrow = slice * SSM_BV + row;
+    float2 S[2 * NF];
+    const int64_t sbase = nh * DV * DQ;
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+        const int col = (4 * j + quarter) * 4;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.S_in) {
+            if constexpr (TRANS) {
+                const float* e = p.S_in + sbase + vrow;  // stored [DQ][DV]
+                s = make_float4(e[(int64_t)col * DV], e[(int64_t)(col + 1) * DV],
+                                e[(int64_t)(col + 2) * DV], e[(int64_t)(col + 3) * DV]);
+            } else {
+                s = *reinterpret_cast<const float4*>(p.S_in + sbase + (int64_t)vrow * DQ + col);
+            }
+        }
+        S[2 * j] = make_float2(s.x, s.y);
+        S[2 * j + 1] = make_float2(s.z, s.w);
+    }
+
+    const int64_t ntile = (count + SSM_TT - 1) / SSM_TT;
+    float4 nq[LQ], nk[LQ];
+    float nv[4], ndt = 0.f;
+    auto tile_start = [&](int64_t i) { return (REV ? ntile - 1 - i : i) * SSM_TT; };
+    auto fetch = [&](int64_t i) {  // tile i's elements of this thread, zeros past the end
+        const int64_t t0 = tile_start(i);
+#pragma unroll
+        for (int e = 0; e < LQ; ++e) {
+            const int idx = tid + e * SSM_THREADS, t = idx / (DQ / 4), c4 = idx % (DQ / 4);
+            nq[e] = nk[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t0 + t < count) {
+                nq[e] = load4<IO>(q + (first + t0 + t) * qstride + c4 * 4);
+                nk[e] = load4<IO>(k + (first + t0 + t) * qstride + c4 * 4);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int t = (tid >> 5) + 4 * e;
+            nv[e] = t0 + t < count ? tr::to_f32(v[(first + t0 + t) * vstride + (tid & 31)]) : 0.f;
+        }
+        if (tid < SSM_TT) ndt = t0 + tid < count ? p.dt[(first + t0 + tid) * p.H + h] : 0.f;
+    };
+    if (ntile > 0) fetch(0);
+    for (int64_t i = 0; i < ntile; ++i) {
+        const int64_t t0 = tile_start(i);
+        const int len = (int)(count - t0 < SSM_TT ? count - t0 : SSM_TT);
+        __syncthreads();  // the tile before is used up
+#pragma unroll
+        for (int e = 0; e < LQ; ++e) {
+            const int idx = tid + e * SSM_THREADS;
+            qs[idx / (DQ / 4)][idx % (DQ / 4)] = nq[e];
+            ks[idx / (DQ / 4)][idx % (DQ / 4)] = nk[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vs[(tid >> 5) + 4 * e][tid & 31] = nv[e];
+        if (tid < SSM_TT) {
+            const float step = scan_step(ndt + bias, p.softplus);
+            st[tid] = step;
+            as[tid] = expf(step * A);
+        }
+        __syncthreads();
+        if (i + 1 < ntile) fetch(i + 1);
+        if constexpr (MODE == SSM_DB) {
+            // entering a block from its end: <G, S>, G = S here (the carried gradient)
+            const int64_t e = t0 + len;
+            if (e == count || e % SSM_BLOCK == 0) {
+                const int64_t slot = first / SSM_BLOCK + n + (e - 1) / SSM_BLOCK;
+                const float* cp = p.ckpt + ((slot * p.H + h) * DV + vrow) * DQ;
+                float dot = 0.f;
+#pragma unroll
+                for (int j = 0; j < NF; ++j) {
+                    const float4 c4 = *reinterpret_cast<const float4*>(cp + (4 * j + quarter) * 4);
+                    dot = fmaf(S[2 * j].x, c4.x, fmaf(S[2 * j].y, c4.y, dot));
+                    dot = fmaf(S[2 * j + 1].x, c4.z, fmaf(S[2 * j + 1].y, c4.w, dot));
+                }
+                dot = warp_sum_f(dot);
+                if ((tid & 31) == 0) part[tid >> 5] = dot;
+                __syncthreads();
+                if (tid == 0) {
+                    const int64_t slots = ssm_slots(p.rows, p.N, SSM_BLOCK);
+                    if (OSDN_IN_BOUNDS(slot, slots))
+                        p.gs[(slice * slots + slot) * p.H + h] = part[0] + part[1] + part[2] + part[3];
+                }
+                __syncthreads();
+            }
+        }
+        for (int u = 0; u < len; ++u) {
+            const int t = REV ? len - 1 - u : u;
+            const float a = as[t], step = st[t];
+            const float vraw = vs[t][row];
+            const float vv = REV ? vraw : vraw * step;
+            const float2 a2 = make_float2(a, a), v2 = make_float2(vv, vv);
+            float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < NF; ++j) {
+                const float4 k4 = ks[t][4 * j + quarter], q4 = qs[t][4 * j + quarter];
+                const float2 kl = make_float2(k4.x, k4.y), kh = make_float2(k4.z, k4.w);
+                if constexpr (REV) {  // the carried state is decayed already
+                    S[2 * j] = __ffma2_rn(v2, kl, S[2 * j]);
+                    S[2 * j + 1] = __ffma2_rn(v2, kh, S[2 * j + 1]);
+                } else {
+                    S[2 * j] = __ffma2_rn(a2, S[2 * j], __fmul2_rn(v2, kl));
+                    S[2 * j + 1] = __ffma2_rn(a2, S[2 * j + 1], __fmul2_rn(v2, kh));
+                }
+                acc0 = __ffma2_rn(S[2 * j], make_float2(q4.x, q4.y), acc0);
+                acc1 = __ffma2_rn(S[2 * j + 1], make_float2(q4.z, q4.w), acc1);
+                if constexpr (REV) {
+                    S[2 * j] = __fmul2_rn(a2, S[2 * j]);
+                    S[2 * j + 1] = __fmul2_rn(a2, S[2 * j + 1]);
+                }
+            }
+            float o = (acc0.x + acc0.y) + (acc1.x + acc1.y);
+            o += __shfl_xor_sync(0xffffffffu, o, 1);
+            o += __shfl_xor_sync(0xffffffffu, o, 2);
+            if (quarter == 0) {
+                if constexpr (MODE == SSM_DX) o *= step;
+                os[t][row] = fmaf(skip, vraw, o);
+            }
+        }
+        if constexpr (MODE == SSM_DC) {
+            const int64_t e = t0 + len;  // S behind a block
+            if (e == count || e % SSM_BLOCK == 0) {
+                const int64_t slot = first / SSM_BLOCK + n + (e - 1) / SSM_BLOCK;
+                float* cp = p.ckpt + ((slot * p.H + h) * DV + vrow) * DQ;
+                if (OSDN_IN_BOUNDS(slot, ssm_slots(p.rows, p.N, SSM_BLOCK)))
+#pragma unroll
+                    for (int j = 0; j < NF; ++j)
+                        *reinterpret_cast<float4*>(cp + (4 * j + quarter) * 4) =
+                            make_float4(S[2 * j].x, S[2 * j].y, S[2 * j + 1].x, S[2 * j + 1].y);
+            }
+            if (slice == 0 && p.vk) {  // q . k = dy . x: 8 threads a token
+                float dot = 0.f;
+#pragma unroll
+                for (int c4 = tid & 7; c4 < DQ / 4; c4 += 8) {
+                    const float4 x4 = ks[tid >> 3][c4], y4 = qs[tid >> 3][c4];
+                    dot += x4.x * y4.x + x4.y * y4.y + x4.z * y4.z + x4.w * y4.w;
+                }
+                dot += __shfl_xor_sync(0xffffffffu, dot, 1);
+                dot += __shfl_xor_sync(0xffffffffu, dot, 2);
+                dot += __shfl_xor_sync(0xffffffffu, dot, 4);
+                if ((tid & 7) == 0 && (tid >> 3) < len)
+                    p.vk[h * p.rows + first + t0 + (tid >> 3)] = dot;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int t = (tid >> 5) + 4 * e;
+            if (t < len && OSDN_IN_BOUNDS(first + t0 + t, p.rows)) {
+                const int64_t at = ((first + t0 + t) * p.H + h) * DV + slice * SSM_BV + (tid & 31);
+                if constexpr (TRANS)
+                    static_cast<float*>(p.out)[at] = os[t][tid & 31];
+                else
+                    static_cast<IO*>(p.out)[at] = tr::from_f32(os[t][tid & 31]);
+            }
+        }
+    }
+    if (!TRANS && p.S_out && OSDN_IN_BOUNDS(nh, (int64_t)p.N * p.H)) {
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            *reinterpret_cast<float4*>(p.S_out + sbase + (int64_t)vrow * DQ + (4 * j + quarter) * 4) =
+                make_float4(S[2 * j].x, S[2 * j].y, S[2 * j + 1].x, S[2 * j + 1].y);
+    }
+}
+
+// The heads' shares of dc and db summed over each group, and per head pos = c . dc and the
+// unscaled neg / step = b . db / step.  dch, dbh: [rows][H][DK] fp32, dbh before its factor step.
+// A warp per (row, group).
+template <int DK, typename IO>
+__global__ void __launch_bounds__(256)
+ssm_group_kernel(const float* __restrict__ dch, const float* __restrict__ dbh,
+                 const IO* __restrict__ b, const IO* __restrict__ c, const float* __restrict__ dt,
+                 const float* __restrict__ dt_bias, int softplus, IO* __restrict__ db,
+                 IO* __restrict__ dc, float* __restrict__ pos, float* __restrict__ rneg,
+                 int64_t rows, int H, int G) {
+    constexpr int PL = DK / 32;
+    const int lane = threadIdx.x & 31, rep = H / G;
+    const int64_t stride = (int64_t)gridDim.x * 8;
+    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < rows * G; u += stride) {
+        const int64_t row = u / G;
+        const int g = (int)(u - row * G);
+        float bb[PL], cc[PL], sb[PL], sc[PL];
+#pragma unroll
+        for (int j = 0; j < PL; j += 2) {
+            const float2 x = load2<IO>(b + u * DK + lane * PL + j);
+            const float2 y = load2<IO>(c + u * DK + lane * PL + j);
+            bb[j] = x.x; bb[j + 1] = x.y;
+            cc[j] = y.x; cc[j + 1] = y.y;
+            sb[j] = sb[j + 1] = sc[j] = sc[j + 1] = 0.f;
+        }
+        for (int r = 0; r < rep; ++r) {
+            const int h = g * rep + r;
+            const int64_t at = (row * H + h) * DK + lane * PL;
+            const float step = scan_step(dt[row * H + h] + (dt_bias ? dt_bias[h] : 0.f), softplus);
+            float dp = 0.f, dn = 0.f;
+#pragma unroll
+            for (int j = 0; j < PL; j += 2) {
+                const float2 x = *reinterpret_cast<const float2*>(dch + at + j);
+                const float2 y = *reinterpret_cast<const float2*>(dbh + at + j);
+                dp += cc[j] * x.x + cc[j + 1] * x.y;
+                dn += bb[j] * y.x + bb[j + 1] * y.y;
+                sc[j] += x.x; sc[j + 1] += x.y;
+                sb[j] = fmaf(step, y.x, sb[j]);
+                sb[j + 1] = fmaf(step, y.y, sb[j + 1]);
+            }
+            dp = warp_sum_f(dp);
+            dn = warp_sum_f(dn);
+            if (lane == 0) {
+                pos[h * rows + row] = dp;
+                rneg[h * rows + row] = dn;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < PL; j += 2) {
+            store2<IO>(db + u * DK + lane * PL + j, make_float2(sb[j], sb[j + 1]));
+            store2<IO>(dc + u * DK + lane * PL + j, make_float2(sc[j], sc[j + 1]));
+        }
+    }
+}
+
+// ddt of every token, and per (sequence, head) the sums that dA, dD and ddt_bias are made of.
+// One CTA per (sequence, head), a warp per block of tokens; part: [3][N][H].
+constexpr int SSM_GATE_WARPS = 16;
+__global__ void __launch_bounds__(32 * SSM_GATE_WARPS)
+ssm_gate_kernel(const float* __restrict__ pos, const float* __restrict__ rneg,
+                const float* __restrict__ gs, int nslice, const float* __restrict__ vk,
+                const float* __restrict__ dt, const float* __restrict__ A,
+                const float* __restrict__ dt_bias, int softplus, float* __restrict__ ddt,
+                double* __restrict__ part, const int32_t* __restrict__ cu, int N, int T, int H,
+                int64_t rows) {
+    __shared__ double red[3][SSM_GATE_WARPS];
+    const int n = blockIdx.x / H, h = blockIdx.x - n * H;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t first, count;
+    const bool ok = seq_range(cu, n, N, T, first, count);
+    double sA = 0.0, sD = 0.0, sb = 0.0;
+    const float Ah = A[h], bias = dt_bias ? dt_bias[h] : 0.f;
+    const int64_t slots = ssm_slots(rows, N, SSM_BLOCK);
+    for (int64_t t0 = (int64_t)warp * SSM_BLOCK; ok && t0 < count;
+         t0 += SSM_BLOCK * SSM_GATE_WARPS) {
+        const int64_t slot = first / SSM_BLOCK + n + t0 / SSM_BLOCK;
+        float tail = 0.f;  // <G, S> behind the block, then plus the sums of the later half
+        for (int s = 0; s < nslice; ++s) tail += gs[(s * slots + slot) * H + h];
+#pragma unroll
+        for (int half = 1; half >= 0; --half) {
+            const int64_t t = t0 + half * 32 + lane;
+            const bool live = t < count;
+            const int64_t at = h * rows + first + t;
+            const float raw = live ? dt[(first + t) * H + h] + bias : 0.f;
+            const float step = scan_step(raw, softplus);
+            const float r = live ? rneg[at] : 0.f;
+            float s = live ? pos[at] - step * r : 0.f;  // suffix sum over the half
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float o = __shfl_down_sync(0xffffffffu, s, off);
+                if (lane + off < 32) s += o;
+            }
+            const float dla = s + tail;
+            tail += __shfl_sync(0xffffffffu, s, 0);
+            if (live) {
+                float d = fmaf(Ah, dla, r);
+                if (softplus) d *= 1.f / (1.f + expf(-raw));
+                if (OSDN_IN_BOUNDS(first + t, rows)) ddt[(first + t) * H + h] = d;
+                sA += (double)(step * dla);
+                sb += (double)d;
+                if (vk) sD += (double)vk[at];
+            }
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        sA += __shfl_xor_sync(0xffffffffu, sA, off);
+        sD += __shfl_xor_sync(0xffffffffu, sD, off);
+        sb += __shfl_xor_sync(0xffffffffu, sb, off);
+    }
+    if (lane == 0) { red[0][warp] = sA; red[1][warp] = sD; red[2][warp] = sb; }
+    __syncthreads();
+    if (threadIdx.x < 3) {
+        double s = 0.0;
+        for (int w = 0; w < SSM_GATE_WARPS; ++w) s += red[threadIdx.x][w];
+        part[((int64_t)threadIdx.x * N + n) * H + h] = s;
+    }
+}
+
+// dA, dD, ddt_bias [H]: the sequences' sums in order.  blockIdx.x: which of the three.
+__global__ void __launch_bounds__(256)
+ssm_param_kernel(const double* __restrict__ part, int N, int H, float* __restrict__ dA,
+                 float* __restrict__ dD, float* __restrict__ ddt_bias) {
+    float* out = blockIdx.x == 0 ? dA : blockIdx.x == 1 ? dD : ddt_bias;
+    if (!out) return;
+    for (int h = threadIdx.x; h < H; h += blockDim.x) {
+        double s = 0.0;
+        for (int n = 0; n < N; ++n) s += part[((int64_t)blockIdx.x * N + n) * H + h];
+        out[h] = (float)s;
+    }
+}
+
+}  // namespace osdn

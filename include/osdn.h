@@ -271,6 +271,140 @@ OSDN_API osdn_status_t osdn_step(const void* q, const void* k, const void* v, co
                         int32_t N, int32_t H, int32_t Dk, int32_t Dv, osdn_dtype_t io,
                         void* stream);
 
+/* ======================================================================================
+ * Layer operators around the token mixer: the short causal convolution in front of it, the
+ * selective state-space scan beside it, the block norm behind it.  The pages describe none of
+ * them; they are defined here.  Conventions are those at the top of this header, with
+ *   - io tensors: activations (x, b, c, f, gate, ...), their gradients (rounded once to the io
+ *     dtype) and the convolution's states;  float32 in every io mode: weights, dt, scan states
+ *     and the gradients of all of these;
+ *   - num_seqs = 0 with cu_seqlens == NULL; num_seqs >= 1 with packed tokens (T > 0);
+ *   - B * T < 2^31;
+ *   - a sequence whose offsets fail the device check is skipped (what is written for its rows
+ *     is unspecified) and OSDN_ERR_DEVICE_BOUNDS recorded.
+ * Sums over tokens are made in a fixed order: the same call gives the same bits.
+ * ====================================================================================== */
+
+/*
+ * Short causal convolution, one filter of W taps per channel:
+ *   z_t[c] = bias[c] + sum_{w < W} weight[c][w] x_{t-W+1+w}[c],   y = silu ? z / (1 + e^-z) : z.
+ * The W - 1 tokens before a sequence are its initial state, oldest first (zeros without one);
+ * its final state is the last W - 1 rows of [state0; x], so calls chain exactly, also over
+ * sequences shorter than W - 1 and empty ones.
+ *   x, y    [B,T,C] io dtype (C = all channels of a token: q, k, v of [B,T,H,D] have C = H * D).
+ *   weight  [C,W] float32.   bias [C] float32, or NULL.   silu 0 or 1.
+ *   state0  [N,W-1,C] io dtype, or NULL.   stateT [N,W-1,C] io dtype, written, or NULL.
+ * W in 2..4, C >= 1 (16-byte accesses when C is a multiple of 8 (bf16) or 4 (f32)).
+ * y and stateT must not overlap anything else.
+ */
+OSDN_API osdn_status_t osdn_conv_fwd(const void* x, const float* weight, const float* bias,
+                                     const void* state0, int32_t silu, void* y, void* stateT,
+                                     const int32_t* cu_seqlens, int32_t num_seqs, int32_t B,
+                                     int32_t T, int32_t C, int32_t W, osdn_dtype_t io,
+                                     void* stream);
+
+/* One token per sequence: x, y [N,C] io dtype; state [N,W-1,C] io dtype, moved on by one token
+ * in place.  A sequence of steps equals osdn_conv_fwd bit for bit. */
+OSDN_API osdn_status_t osdn_conv_step(const void* x, const float* weight, const float* bias,
+                                      void* state, int32_t silu, void* y, int32_t N, int32_t C,
+                                      int32_t W, osdn_dtype_t io, void* stream);
+
+/*
+ * Backward pass of osdn_conv_fwd.  dy [B,T,C] in dtype dy_io: the io dtype, or OSDN_F32 (what
+ * osdn_bwd writes for q, k and v).  dstateT [N,W-1,C] float32 or NULL: dL/dstateT.
+ *   dx [B,T,C] io dtype, written.   dweight [C,W] float32, written.   dbias [C] float32 or NULL.
+ *   dstate0 [N,W-1,C] float32, written, or NULL.
+ *   workspace  osdn_conv_bwd_workspace_bytes(...) bytes, 256-byte aligned.
+ */
+OSDN_API size_t osdn_conv_bwd_workspace_bytes(int32_t B, int32_t T, int32_t C, int32_t W);
+OSDN_API osdn_status_t osdn_conv_bwd(const void* x, const float* weight, const float* bias,
+                                     const void* state0, int32_t silu, const void* dy,
+                                     osdn_dtype_t dy_io, const float* dstateT, void* dx,
+                                     float* dweight, float* dbias, float* dstate0,
+                                     const int32_t* cu_seqlens, int32_t num_seqs, int32_t B,
+                                     int32_t T, int32_t C, int32_t W, osdn_dtype_t io,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Selective state-space scan: linear attention with a decay per token and head and no erase.
+ * Per (sequence n, head h), g = h / (H / G), step_t = softplus(dt_t + dt_bias) (or dt_t +
+ * dt_bias itself when softplus == 0), a_t = exp(step_t A):
+ *   S_t = a_t S_{t-1} + step_t x_t b_t^T,     y_t = S_t c_t + D x_t.
+ *   x, y    [B,T,H,Dv] io dtype.          b, c [B,T,G,Dk] io dtype; H / G heads share a row.
+ *   dt      [B,T,H] float32.              A [H] float32 (negative for a decaying state).
+ *   D       [H] float32, or NULL for 0.   dt_bias [H] float32, or NULL for 0.
+ *   S0, ST  [N,H,Dv,Dk] float32 (as for osdn_chunk_fwd); S0 NULL for zeros, ST NULL to skip.
+ *   workspace  osdn_ssm_fwd_workspace_bytes(...) bytes, 256-byte aligned (NULL if that is 0).
+ * Dk, Dv in {64, 128}; H a multiple of G.  y and ST must not overlap anything else.
+ */
+OSDN_API size_t osdn_ssm_fwd_workspace_bytes(int32_t num_seqs, int32_t B, int32_t T, int32_t H,
+                                             int32_t Dk, int32_t Dv, osdn_dtype_t io);
+OSDN_API osdn_status_t osdn_ssm_fwd(const void* x, const float* dt, const float* A, const void* b,
+                                    const void* c, const float* D, const float* dt_bias,
+                                    int32_t softplus, const float* S0, void* y, float* ST,
+                                    const int32_t* cu_seqlens, int32_t num_seqs, int32_t B,
+                                    int32_t T, int32_t H, int32_t G, int32_t Dk, int32_t Dv,
+                                    osdn_dtype_t io, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* One token per sequence: x, y [N,H,Dv], b, c [N,G,Dk] io dtype, dt [N,H] float32; S [N,H,Dv,Dk]
+ * float32, updated in place.  A sequence of steps equals osdn_ssm_fwd up to rounding. */
+OSDN_API osdn_status_t osdn_ssm_step(const void* x, const float* dt, const float* A, const void* b,
+                                     const void* c, const float* D, const float* dt_bias,
+                                     int32_t softplus, float* S, void* y, int32_t N, int32_t H,
+                                     int32_t G, int32_t Dk, int32_t Dv, osdn_dtype_t io,
+                                     void* stream);
+
+/*
+ * Backward pass of osdn_ssm_fwd, given dy [B,T,H,Dv] io dtype and dST [N,H,Dv,Dk] float32 (NULL
+ * for 0).  Written: dx [B,T,H,Dv], db, dc [B,T,G,Dk] io dtype; ddt [B,T,H], dA [H] float32;
+ * dD, ddt_bias [H], dS0 [N,H,Dv,Dk] float32, each NULL to skip.
+ *   workspace  osdn_ssm_bwd_workspace_bytes(...) bytes, 256-byte aligned.
+ */
+OSDN_API size_t osdn_ssm_bwd_workspace_bytes(int32_t num_seqs, int32_t B, int32_t T, int32_t H,
+                                             int32_t Dk, int32_t Dv, osdn_dtype_t io);
+OSDN_API osdn_status_t osdn_ssm_bwd(const void* x, const float* dt, const float* A, const void* b,
+                                    const void* c, const float* D, const float* dt_bias,
+                                    int32_t softplus, const float* S0, const void* dy,
+                                    const float* dST, void* dx, float* ddt, float* dA, void* db,
+                                    void* dc, float* dD, float* ddt_bias, float* dS0,
+                                    const int32_t* cu_seqlens, int32_t num_seqs, int32_t B,
+                                    int32_t T, int32_t H, int32_t G, int32_t Dk, int32_t Dv,
+                                    osdn_dtype_t io, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/*
+ * Block norm: a block's output f joined to the residual stream x and to the next block's input,
+ * over R rows of D values (a mixer's output per head: R = B * T * H rows of D = Dv):
+ *   u  = rmsnorm(f) * w_post * act(gate)       (gate_first: rmsnorm(f * act(gate)) * w_post)
+ *   x_out = x + scale * u,    h = rmsnorm(x_out before rounding) * w_next,
+ * rmsnorm(v) = v / sqrt(mean(v^2) + eps).  Each part is optional: w_post NULL leaves out the
+ * first norm (and w_post), gate NULL the gate, x NULL the residual, w_next NULL the second norm.
+ *   f, x, gate, x_out, h  [R,D] io dtype.     w_post, w_next [D] float32.
+ *   gate_act  0: silu, 1: sigmoid.            gate_first 0 or 1 (no effect without gate).
+ * h is given exactly when w_next is; x_out may be NULL when h is given.  1 <= D <= 8192.
+ * x_out and h must not overlap anything else.
+ */
+OSDN_API osdn_status_t osdn_norm_fwd(const void* f, const void* x, const void* gate,
+                                     const float* w_post, const float* w_next, int32_t gate_act,
+                                     int32_t gate_first, float scale, float eps, void* x_out,
+                                     void* h, int64_t R, int32_t D, osdn_dtype_t io, void* stream);
+
+/*
+ * Backward pass of osdn_norm_fwd from its inputs, given dx_out (NULL for 0 when dh is given) and
+ * dh (exactly when w_next is given), [R,D] io dtype.  Written: df; dx when not NULL (only with
+ * x); dgate exactly with gate; dw_post, dw_next [D] float32 exactly with w_post, w_next.
+ *   workspace  osdn_norm_bwd_workspace_bytes(...) bytes, 256-byte aligned.
+ */
+OSDN_API size_t osdn_norm_bwd_workspace_bytes(int64_t R, int32_t D);
+OSDN_API osdn_status_t osdn_norm_bwd(const void* f, const void* x, const void* gate,
+                                     const float* w_post, const float* w_next, int32_t gate_act,
+                                     int32_t gate_first, float scale, float eps,
+                                     const void* dx_out, const void* dh, void* df, void* dx,
+                                     void* dgate, float* dw_post, float* dw_next, int64_t R,
+                                     int32_t D, osdn_dtype_t io, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 /*
  * Synchronizes `stream`, then returns and clears the device status word of the current
  * device: OSDN_OK, OSDN_ERR_DEVICE_TIMEOUT or OSDN_ERR_DEVICE_BOUNDS (the first error any
