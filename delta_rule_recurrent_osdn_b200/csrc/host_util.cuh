@@ -2,6 +2,8 @@
 // status, opt-in shared memory, device properties.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -38,6 +40,22 @@ inline int sm_count() {
         cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
         return 148;
     return n;
+}
+
+// cuTensorMapEncodeTiled from the driver, looked up once through the runtime (the library
+// does not link libcuda directly).
+using EncodeTiledFn = PFN_cuTensorMapEncodeTiled_v12000;
+inline EncodeTiledFn tensor_map_encoder() {
+    static EncodeTiledFn fn = []() -> EncodeTiledFn {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
 }
 
 // Reads and clears the device status word of mixer_lib.cu's kernels (each translation unit of

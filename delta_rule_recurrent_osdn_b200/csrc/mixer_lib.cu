@@ -13,6 +13,7 @@
 #include "norm.cuh"
 #include "ssm_step.cuh"
 #include "ssm_scan.cuh"
+#include "ssm_tc.cuh"
 
 namespace osdn {
 
@@ -206,6 +207,39 @@ osdn_status_t launch_ssm_scan(const SsmArgs& a, int DQ, int DV, cudaStream_t str
         ssm_scan_kernel<64, 128, MODE, IO><<<grid, block, 0, stream>>>(a);
     else
         ssm_scan_kernel<64, 64, MODE, IO><<<grid, block, 0, stream>>>(a);
+    return launch_status();
+}
+
+// 3-D bf16 view [rows][heads][D] of a token tensor; boxes of 64 channels x 1 head x 128 tokens,
+// 128-byte swizzle.
+bool make_chunk_map(CUtensorMap* m, const void* base, int D, int heads, int64_t rows) {
+    EncodeTiledFn enc = tensor_map_encoder();
+    if (!enc || rows <= 0) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)heads * D * 2};
+    cuuint32_t box[3] = {64, 1, TCS_L};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// q, k: [rows][G][DQ], v: [rows][H][nvt * 64] (q only in the forward pass).
+template <int DQ, int MODE>
+osdn_status_t launch_tc_chain(const void* q, const void* k, const void* v, TcsArgs a,
+                              cudaStream_t stream) {
+    using L = TcsSmem<DQ, MODE>;
+    const int64_t ctas = (int64_t)a.N * a.H * a.nvt;
+    if (ctas == 0) return OSDN_OK;
+    if (ctas > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
+    CUtensorMap mq, mk, mv;
+    if (!make_chunk_map(&mk, k, DQ, a.G, a.rows) || !make_chunk_map(&mv, v, a.nvt * TCS_BV, a.H, a.rows) ||
+        !make_chunk_map(&mq, q ? q : k, DQ, a.G, a.rows))
+        return OSDN_ERR_CUDA;
+    auto kern = ssm_tc_chain_kernel<DQ, MODE>;
+    if (!set_smem(kern, L::BYTES)) return OSDN_ERR_CUDA;
+    a.limit_ns = (long long)kWaitLimitNs;
+    kern<<<dim3((unsigned)ctas), dim3(L::THREADS), L::BYTES, stream>>>(mq, mk, mv, a);
     return launch_status();
 }
 
@@ -413,7 +447,17 @@ osdn_status_t osdn_ssm_fwd(const void* x, const float* dt, const float* A, const
     a.q = c; a.k = b; a.v = x; a.dt = dt; a.A = A; a.D = D; a.dt_bias = dt_bias; a.S_in = S0;
     a.out = y; a.S_out = ST; a.cu = cu_seqlens; a.rows = rows; a.N = (int)N; a.T = T; a.H = H;
     a.G = G; a.softplus = softplus;
-    if (io == OSDN_BF16) return launch_ssm_scan<SSM_FWD, __nv_bfloat16>(a, Dk, Dv, s);
+    // bf16 tokens run on the tensor cores; fp32 ones, and calls without tokens (states pass
+    // through), token by token
+    if (io == OSDN_BF16 && rows > 0) {
+        TcsArgs t = {};
+        t.dt = dt; t.A = A; t.dt_bias = dt_bias; t.D = D; t.x = static_cast<const __nv_bfloat16*>(x);
+        t.S_in = S0; t.y = static_cast<__nv_bfloat16*>(y); t.S_out = ST; t.cu = cu_seqlens;
+        t.rows = rows; t.N = (int)N; t.T = T; t.H = H; t.G = G; t.softplus = softplus;
+        t.nvt = Dv / TCS_BV;
+        return Dk == 128 ? launch_tc_chain<128, TCS_FWD>(c, b, x, t, s)
+                         : launch_tc_chain<64, TCS_FWD>(c, b, x, t, s);
+    }
     return launch_ssm_scan<SSM_FWD, float>(a, Dk, Dv, s);
 }
 

@@ -27,6 +27,20 @@
 namespace osdn {
 namespace {
 
+// Diagnostic kernel: waits on a barrier that nobody arrives at, with a bounded number of
+// non-blocking polls, so that the timeout path runs and the kernel returns.
+__global__ void watchdog_selftest_kernel(int64_t spin_limit) {
+    __shared__ __align__(8) uint64_t bar;
+    if (threadIdx.x == 0) mbar_init(&bar, 1);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        bool done = false;
+        for (int64_t i = 0; i < spin_limit && !done; ++i) done = mbar_test_parity(&bar, 0);
+        if (!done) record_status(OSDN_ERR_DEVICE_TIMEOUT);
+    }
+    __syncthreads();
+}
+
 struct Dims {
     int32_t B, T, H, Dk, Dv, N;
     int64_t rows() const { return (int64_t)B * T; }
@@ -106,22 +120,6 @@ osdn_status_t launch_chunk_c(int chunk, const void* q, const void* k, const void
         default:
             return OSDN_ERR_UNSUPPORTED;
     }
-}
-
-// cuTensorMapEncodeTiled from the driver, looked up once through the runtime (the library
-// does not link libcuda directly).
-using EncodeTiledFn = PFN_cuTensorMapEncodeTiled_v12000;
-EncodeTiledFn tensor_map_encoder() {
-    static EncodeTiledFn fn = []() -> EncodeTiledFn {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        return reinterpret_cast<EncodeTiledFn>(p);
-    }();
-    return fn;
 }
 
 // 3-D bf16 view [rows][H][D] of a [B, T, H, D] tensor; boxes of 64 channels x 1 head x 64

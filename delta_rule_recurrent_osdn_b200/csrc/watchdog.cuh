@@ -80,18 +80,4 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
 // last microseconds), short enough that a stuck kernel returns within seconds.
 constexpr int64_t kWaitLimitNs = 2000000000LL;
 
-// Diagnostic kernel: waits on a barrier that nobody arrives at, with a bounded number of
-// non-blocking polls, so that the timeout path runs and the kernel returns.
-__global__ void watchdog_selftest_kernel(int64_t spin_limit) {
-    __shared__ __align__(8) uint64_t bar;
-    if (threadIdx.x == 0) mbar_init(&bar, 1);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        bool done = false;
-        for (int64_t i = 0; i < spin_limit && !done; ++i) done = mbar_test_parity(&bar, 0);
-        if (!done) record_status(OSDN_ERR_DEVICE_TIMEOUT);
-    }
-    __syncthreads();
-}
-
 }  // namespace osdn
