@@ -238,7 +238,6 @@ osdn_status_t launch_tc_chain(const void* q, const void* k, const void* v, TcsAr
         return OSDN_ERR_CUDA;
     auto kern = ssm_tc_chain_kernel<DQ, MODE>;
     if (!set_smem(kern, L::BYTES)) return OSDN_ERR_CUDA;
-    a.limit_ns = (long long)kWaitLimitNs;
     kern<<<dim3((unsigned)ctas), dim3(L::THREADS), L::BYTES, stream>>>(mq, mk, mv, a);
     return launch_status();
 }

@@ -25,8 +25,8 @@
 // Rows past a sequence's end inside its last tile belong to the next sequence: the rows of B, X
 // and V' are zeroed in shared memory before a product sums over them.
 //
-// Warp roles: 0 TMA loads (two stages), 1 MMA issue, 2 the gates (softplus, sums of log decays),
-// 4-7 the state, 8-11 V' and the output rows, 12-15 and 16-19 P of even and odd chunks.
+// Warp roles: 0 TMA loads (two tiles each of C, B and X), 1 MMA issue, 2-3 the gates (softplus, sums of log decays),
+// 4-7 the state, 8-11 V', 12-15 the output rows, 16-23 P.
 // Hand-offs are mbarriers with bounded waits; a role that gives up leaves its loop, the others
 // run into their own bounds, and everything in flight is waited for before the CTA leaves.
 #pragma once
@@ -38,6 +38,7 @@ namespace osdn {
 
 constexpr int TCS_L = 128;   // tokens per chunk
 constexpr int TCS_BV = 64;   // value channels per CTA
+constexpr int TCS_GATES = 8; // chunks whose gates are kept: they are made well ahead of their use
 
 // What a launch of the chain does: the forward pass; the states in front of every chunk (stored
 // as bf16 hi / lo images); the same for the gradient's chain, backwards in time.
@@ -56,7 +57,6 @@ struct TcsArgs {
     const int32_t* cu;
     int64_t rows;
     int N, T, H, G, softplus, nvt;
-    long long limit_ns;
 };
 
 template <int DQ, int MODE> struct TcsSmem {
@@ -68,13 +68,13 @@ template <int DQ, int MODE> struct TcsSmem {
     static constexpr uint32_t S = VP + NVP * 32768;   // the state as an operand (or image)
     static constexpr uint32_t GATE = S + (OUT ? 16384 : 32768);
     static constexpr uint32_t GATE_BYTES = 1664;
-    static constexpr uint32_t BAR = GATE + 2 * GATE_BYTES;
-    static constexpr uint32_t TMEM_SLOT = BAR + 176;
+    static constexpr uint32_t BAR = GATE + TCS_GATES * GATE_BYTES;
+    static constexpr uint32_t TMEM_SLOT = BAR + (27 + 2 * TCS_GATES) * 8 + 8;
     static constexpr size_t BYTES = TMEM_SLOT + 16 + 1024;  // + alignment slack
-    static constexpr int THREADS = OUT ? 640 : 384;
-    // tensor memory: G / P (two buffers), B^T V', C S^T, P X
-    static constexpr uint32_t COL_G = 0, COL_U = OUT ? 256 : 0, COL_Y1 = 320, COL_Y2 = 384;
-    static constexpr uint32_t COLS = OUT ? 512 : 64;
+    static constexpr int THREADS = OUT ? 768 : 384;
+    // tensor memory: G / P (two buffers), B^T V' (hi and lo side by side), C S^T, P X
+    static constexpr uint32_t COL_G = 0, COL_U = OUT ? 256 : 0, COL_Y1 = 384, COL_Y2 = 448;
+    static constexpr uint32_t COLS = OUT ? 512 : 128;
 };
 static_assert(TcsSmem<128, TCS_FWD>::BYTES <= 232448, "shared memory");
 
@@ -106,32 +106,50 @@ __device__ __forceinline__ uint32_t pack2_rn(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Reading half of a chunk's gates (one warp): this lane's tokens 4 lane .. 4 lane + 3.
-struct TcsGateIn { float raw[4]; };
-__device__ __forceinline__ TcsGateIn tcs_gate_load(const float* __restrict__ dt, int64_t row0,
-                                                   int len, int H, int h, int lane) {
-    TcsGateIn in;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int t = 4 * lane + e;
-        in.raw[e] = t < len ? __ldg(dt + (row0 + t) * H + h) : 0.f;
-    }
-    return in;
+// Bounded wait on an mbarrier phase: at most 2^20 polls, each of which the hardware may hold back
+// for up to 2 us, so a wait that cannot end gives up (and records it) within about 2 seconds.
+// (A few instructions inline: five roles share the instruction cache.)
+__device__ __forceinline__ bool tcs_wait(uint64_t* bar, int phase) {
+    const uint32_t a = smem_u32(bar), par = (uint32_t)phase & 1u;
+    uint32_t done = 0;
+#pragma unroll 1
+    for (int n = 0; n < (1 << 20) && !done; ++n)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(a), "r"(par)
+            : "memory");
+    if (!done) record_status(OSDN_ERR_DEVICE_TIMEOUT);
+    return done != 0;
 }
+
+// A chunk's gates, by one warp: softplus and the log decays of its tokens, then their sums.
 template <bool REV>
-__device__ __forceinline__ void tcs_gate_store(const TcsGateIn& in, TcsGate* g, int len, float A,
-                                               float bias, int softplus, int lane) {
-    float st[4], l[4];
+__device__ __forceinline__ void tcs_gates(TcsGate* g, const float* __restrict__ dt, int64_t stride,
+                                          int len, float A, float bias, int softplus, int lane) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const bool live = 4 * lane + e < len;
-        st[e] = live ? scan_step(in.raw[e] + bias, softplus) : 0.f;
-        // 2^-1e5 is 0 like everything below it; a finite floor keeps differences defined
-        float d = live ? st[e] * A * 1.4426950408889634f : 0.f;
-        d = d < -1e5f ? -1e5f : d;
-        l[e] = e ? l[e - 1] + d : d;
+    for (int t = lane; t < TCS_L; t += 32)  // loads in flight together; each lane its own slots
+        g->st[t] = t < len ? __ldg(dt + t * stride) : 0.f;
+#pragma unroll 1
+    for (int t = lane; t < TCS_L; t += 32) {
+        float st = 0.f, d = 0.f;
+        if (t < len) {
+            st = scan_step(g->st[t] + bias, softplus);
+            // 2^-1e5 is 0 like everything below it; a finite floor keeps differences defined
+            d = st * A * 1.4426950408889634f;
+            d = d < -1e5f ? -1e5f : d;
+        }
+        g->st[t] = st;
+        g->l[t] = d;
     }
-    float own = l[3], pre = 0.f;  // prefix over the 4 lanes of the sub-block
+    __syncwarp();
+    // 4 tokens a lane, 4 lanes a sub-block
+    const float4 d4 = *reinterpret_cast<const float4*>(g->l + 4 * lane);
+    const float4 s4 = *reinterpret_cast<const float4*>(g->st + 4 * lane);
+    float4 l4 = make_float4(d4.x, d4.x + d4.y, (d4.x + d4.y) + d4.z, ((d4.x + d4.y) + d4.z) + d4.w);
+    float own = l4.w, pre = 0.f;
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) {
         const float o = __shfl_up_sync(0xffffffffu, own, off, 4);
@@ -151,13 +169,23 @@ __device__ __forceinline__ void tcs_gate_store(const TcsGateIn& in, TcsGate* g, 
         g->bl[b + 1] = (float)(base - (double)hi);
         if (b == 0) g->bh[0] = g->bl[0] = 0.f;
     }
+    l4.x += pre; l4.y += pre; l4.z += pre; l4.w += pre;
+    *reinterpret_cast<float4*>(g->l + 4 * lane) = l4;
+    *reinterpret_cast<float4*>(g->g + 4 * lane) =
+        REV ? make_float4(ex2f(l4.x), ex2f(l4.y), ex2f(l4.z), ex2f(l4.w))
+            : make_float4(ex2f(tot - l4.x) * s4.x, ex2f(tot - l4.y) * s4.y, ex2f(tot - l4.z) * s4.z,
+                          ex2f(tot - l4.w) * s4.w);
+}
+
+// One operand pair's K steps: `n` MMAs, the descriptors' start addresses (16-byte units) moving
+// by `da` and `db` per step, and by `ga` and `gb` more after every fourth.  Unrolled: a rolled
+// loop took 100 cycles per MMA, this 62.
+template <int n>
+__device__ __forceinline__ void tcs_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t da,
+                                        uint32_t db, uint32_t ga, uint32_t gb) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float le = pre + l[e];
-        g->l[4 * lane + e] = le;
-        g->st[4 * lane + e] = st[e];
-        g->g[4 * lane + e] = REV ? ex2f(le) : ex2f(tot - le) * st[e];
-    }
+    for (int e = 0; e < n; ++e)
+        tc::mma_bf16(d, a + e * da + (e >> 2) * ga, b + e * db + (e >> 2) * gb, id, e != 0);
 }
 
 template <int DQ, int MODE>
@@ -178,21 +206,27 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     const int DV = p.nvt * TCS_BV;
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
-    uint64_t* full = bars + 0;       // [2] tiles landed
-    uint64_t* empty = bars + 2;      // [2] tiles used up (MMA commit)
-    uint64_t* gate_full = bars + 4;  // [2]
-    uint64_t* g_full = bars + 6;     // [2] G = C B^T
-    uint64_t* p_full = bars + 8;     // [2] P written
-    uint64_t* vp_full = bars + 10;   // [2] V' written (and dead rows zeroed)
-    uint64_t* vp_free = bars + 12;   // [2] V' used up (MMA commit)
-    uint64_t* gate_free = bars + 14; // [2] the chunk's gates read by all
-    uint64_t* u_full = bars + 16;    // B^T V'
-    uint64_t* s_full = bars + 17;    // the state written as an operand, B^T V' read
-    uint64_t* y_full = bars + 18;    // C S^T and P X
-    uint64_t* y_free = bars + 19;    // ... read
-    uint64_t* drain = bars + 20;
+    uint64_t* q_full = bars + 0;     // [2] tiles landed
+    uint64_t* k_full = bars + 2;
+    uint64_t* v_full = bars + 4;
+    uint64_t* q_empty = bars + 6;    // [2] tiles used up (MMA commit)
+    uint64_t* k_empty = bars + 8;
+    uint64_t* v_empty = bars + 10;
+    uint64_t* g_full = bars + 12;    // [2] G = C B^T
+    uint64_t* p_full = bars + 14;    // [2] P written
+    uint64_t* vp_full = bars + 16;   // [2] V' written (and dead rows zeroed)
+    uint64_t* vp_free = bars + 18;   // [2] V' used up (MMA commit)
+    uint64_t* u_full = bars + 20;    // B^T V'
+    uint64_t* u_free = bars + 21;    // ... read
+    uint64_t* s_full = bars + 22;    // FWD: the state written as an operand
+    uint64_t* y1_done = bars + 23;   // FWD: ... used up (MMA commit)
+    uint64_t* y_full = bars + 24;    // C S^T and P X
+    uint64_t* y_free = bars + 25;    // ... read
+    uint64_t* drain = bars + 26;
+    uint64_t* gate_full = bars + 27;              // [TCS_GATES] the chunk's gates written
+    uint64_t* gate_free = gate_full + TCS_GATES;  // [TCS_GATES] ... read by all
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::TMEM_SLOT);
-    auto gate = [&](int i) { return reinterpret_cast<TcsGate*>(smem + L::GATE + (i & 1) * L::GATE_BYTES); };
+    auto gate = [&](int i) { return reinterpret_cast<TcsGate*>(smem + L::GATE + i % TCS_GATES * L::GATE_BYTES); };
     auto stage = [&](int i) { return smem + (i & 1) * L::STAGE; };
     auto chunk_of = [&](int i) { return REV ? nch - 1 - i : i; };
     auto row_of = [&](int i) { return first + (int64_t)chunk_of(i) * TCS_L; };
@@ -202,7 +236,7 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     };
     // every lane waits; the warp leaves together
     auto wait = [&](uint64_t* bar, int phase) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, (uint32_t)phase & 1u, p.limit_ns));
+        return __all_sync(0xffffffffu, tcs_wait(bar, phase));
     };
 
     if (warp == 0) {
@@ -211,18 +245,26 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     }
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
-            mbar_init(&gate_full[i], 1);
+            mbar_init(&q_full[i], 1);
+            mbar_init(&k_full[i], 1);
+            mbar_init(&v_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_empty[i], 1);
             mbar_init(&g_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[i], 8);
             mbar_init(&vp_full[i], 4);
             mbar_init(&vp_free[i], 1);
+        }
+        for (int i = 0; i < TCS_GATES; ++i) {
+            mbar_init(&gate_full[i], 1);
             // FWD: the output rows are the last readers; else V' and the state read them
             mbar_init(&gate_free[i], OUT ? 4 : 8);
         }
         mbar_init(u_full, 1);
+        mbar_init(u_free, 4);
         mbar_init(s_full, 4);
+        mbar_init(y1_done, 1);
         mbar_init(y_full, 1);
         mbar_init(y_free, 4);
         mbar_init(drain, 1);
@@ -234,111 +276,115 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     const uint32_t tmem = *tmem_slot;
     const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
 
+    // FWD: the launch's 6 x 80 registers are shared out 64 + 112 + 72 + 88 + 72 + 72
+    if (warp < 4) {
+        if constexpr (OUT) tc::reg_dec<64>();
     if (warp == 0) {
         // ------------------------------------------------------------ TMA
         if (lane == 0) {
-            int issued = 0;
+            int nq = 0, nk = 0, nv = 0;  // tiles asked for
             for (int i = 0; i < nch; ++i) {
-                if (i >= 2 && !mbar_wait_bounded(&empty[i & 1], ((i >> 1) - 1) & 1, p.limit_ns)) break;
                 uint8_t* s = stage(i);
-                uint64_t* bar = &full[i & 1];
-                const int row = (int)row_of(i);
-                tc::mbar_expect_tx(bar, L::STAGE);
+                const int b = i & 1, use = (i >> 1) - 1, row = (int)row_of(i);
+                // in the order in which chunk i - 2 gives its tiles back
+                if (i >= 2 && !tcs_wait(&k_empty[b], use & 1)) break;
+                tc::mbar_expect_tx(&k_full[b], L::KB);
 #pragma unroll
-                for (int b = 0; b < DQ / 64; ++b) {
-                    if constexpr (OUT) tc::tma_load_3d(s + L::Q + b * 16384, &tm_q, b * 64, g, row, bar);
-                    tc::tma_load_3d(s + L::K + b * 16384, &tm_k, b * 64, g, row, bar);
+                for (int e = 0; e < DQ / 64; ++e)
+                    tc::tma_load_3d(s + L::K + e * 16384, &tm_k, e * 64, g, row, &k_full[b]);
+                nk = i + 1;
+                if constexpr (OUT) {
+                    if (i >= 2 && !tcs_wait(&q_empty[b], use & 1)) break;
+                    tc::mbar_expect_tx(&q_full[b], L::QB);
+#pragma unroll
+                    for (int e = 0; e < DQ / 64; ++e)
+                        tc::tma_load_3d(s + L::Q + e * 16384, &tm_q, e * 64, g, row, &q_full[b]);
+                    nq = i + 1;
                 }
-                tc::tma_load_3d(s + L::V, &tm_v, vt * TCS_BV, h, row, bar);
-                issued = i + 1;
+                if (i >= 2 && !tcs_wait(&v_empty[b], use & 1)) break;
+                tc::mbar_expect_tx(&v_full[b], 16384);
+                tc::tma_load_3d(s + L::V, &tm_v, vt * TCS_BV, h, row, &v_full[b]);
+                nv = i + 1;
             }
-            // whatever was issued has landed before the CTA may leave
-            for (int i = issued > 2 ? issued - 2 : 0; i < issued; ++i)
-                mbar_wait_bounded(&full[i & 1], (i >> 1) & 1, p.limit_ns);
+            // whatever was asked for has landed before the CTA may leave
+            auto landed = [&](uint64_t* bar, int cnt) {
+                for (int i = cnt > 2 ? cnt - 2 : 0; i < cnt; ++i)
+                    tcs_wait(&bar[i & 1], (i >> 1) & 1);
+            };
+            landed(k_full, nk);
+            landed(q_full, nq);
+            landed(v_full, nv);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issue
+        // per chunk: B^T V', C S^T, the next chunk's G, P X; what a product waits for is ready by
+        // the time the one before is issued, so the pipe stays fed
         if (lane == 0) {
             constexpr uint32_t ID_G = tc::idesc(1, 0, 0, 128, 128);  // tokens x tokens
             constexpr uint32_t ID_Y = tc::idesc(1, 0, 1, 128, 64);   // tokens x value channels
-            constexpr uint32_t ID_U = tc::idesc(1, 1, 1, 128, 64);   // key x value channels
-            auto issue_g = [&](int i) {
+            constexpr uint32_t ID_U = tc::idesc(1, 1, 1, 128, 128);  // key x value channels, hi | lo
+            auto issue_g = [&](int i) -> bool {
+                if (!tcs_wait(&q_full[i & 1], (i >> 1) & 1) ||
+                    !tcs_wait(&k_full[i & 1], (i >> 1) & 1))
+                    return false;
                 const uint32_t q = smem_u32(stage(i) + L::Q), k = smem_u32(stage(i) + L::K);
-#pragma unroll
-                for (int s = 0; s < DQ / 16; ++s)
-                    tc::mma_bf16(tmem + L::COL_G + (i & 1) * 128,
-                                 tc::sw128_desc(q + (s >> 2) * 16384 + (s & 3) * 32, 16, 1024),
-                                 tc::sw128_desc(k + (s >> 2) * 16384 + (s & 3) * 32, 16, 1024), ID_G,
-                                 s != 0);
+                tcs_mma<DQ / 16>(tmem + L::COL_G + (i & 1) * 128, tc::sw128_desc(q, 16, 1024),
+                                 tc::sw128_desc(k, 16, 1024), ID_G, 2, 2, 1024 - 8, 1024 - 8);
                 tc::mma_commit(&g_full[i & 1]);
+                return true;
             };
-            bool ok = true;
-            if (OUT && nch > 0) {
-                ok = mbar_wait_bounded(&full[0], 0, p.limit_ns);
-                if (ok) issue_g(0);
-            }
+            bool ok = !OUT || nch == 0 || issue_g(0);
             for (int i = 0; ok && i < nch; ++i) {
                 const int s = i & 1, ph = (i >> 1) & 1;
-                if (OUT && i + 1 < nch) {
-                    if (!(ok = mbar_wait_bounded(&full[s ^ 1], ((i + 1) >> 1) & 1, p.limit_ns))) break;
-                    issue_g(i + 1);
-                }
-                if (!(ok = mbar_wait_bounded(s_full, i & 1, p.limit_ns))) break;
                 const uint32_t q = smem_u32(stage(i) + L::Q), k = smem_u32(stage(i) + L::K),
                                v = smem_u32(stage(i) + L::V);
-                if constexpr (OUT) {
-                    if (i > 0 && !(ok = mbar_wait_bounded(y_free, (i - 1) & 1, p.limit_ns))) break;
-                    tc::fence_after_sync();
-                    const uint32_t sb = smem_u32(smem + L::S);
-#pragma unroll
-                    for (int e = 0; e < DQ / 16; ++e)
-                        tc::mma_bf16(tmem + L::COL_Y1,
-                                     tc::sw128_desc(q + (e >> 2) * 16384 + (e & 3) * 32, 16, 1024),
-                                     tc::sw128_desc(sb + e * 2048, 16384, 1024), ID_Y, e != 0);
-                }
-                // the V' and output warpgroup has seen the tiles land: no wait for `full` here
-                if (!(ok = mbar_wait_bounded(&vp_full[i % L::NVP], (i / L::NVP) & 1, p.limit_ns))) break;
+                // X has landed before V' is made from it, B before G
+                if (!OUT && !(ok = tcs_wait(&k_full[s], ph))) break;
+                if (!(ok = tcs_wait(&vp_full[i % L::NVP], (i / L::NVP) & 1))) break;
+                if (i > 0 && !(ok = tcs_wait(u_free, (i - 1) & 1))) break;
                 tc::fence_after_sync();
                 const uint32_t vp = smem_u32(smem + L::VP + (i % L::NVP) * 32768);
                 // (DQ = 64: rows 64..127 read the next tile and are not used)
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        tc::mma_bf16(tmem + L::COL_U, tc::sw128_desc(k + e * 2048, 16384, 1024),
-                                     tc::sw128_desc(vp + t * 16384 + e * 2048, 16384, 1024), ID_U,
-                                     (t | e) != 0);
+                tcs_mma<8>(tmem + L::COL_U, tc::sw128_desc(k, 16384, 1024),
+                           tc::sw128_desc(vp, 16384, 1024), ID_U, 128, 128, 0, 0);
                 tc::mma_commit(u_full);
                 tc::mma_commit(&vp_free[i % L::NVP]);
+                tc::mma_commit(&k_empty[s]);
                 if constexpr (OUT) {
-                    if (!(ok = mbar_wait_bounded(&p_full[s], ph, p.limit_ns))) break;
+                    if (!(ok = tcs_wait(s_full, i & 1))) break;
+                    if (i > 0 && !(ok = tcs_wait(y_free, (i - 1) & 1))) break;
+                    tc::fence_after_sync();
+                    const uint32_t sb = smem_u32(smem + L::S);
+                    tcs_mma<DQ / 16>(tmem + L::COL_Y1, tc::sw128_desc(q, 16, 1024),
+                                     tc::sw128_desc(sb, 16384, 1024), ID_Y, 2, 128, 1024 - 8, 0);
+                    tc::mma_commit(y1_done);
+                    tc::mma_commit(&q_empty[s]);
+                    if (i + 1 < nch && !(ok = issue_g(i + 1))) break;
+                    if (!(ok = tcs_wait(&p_full[s], ph))) break;
                     tc::fence_after_sync();
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        tc::mma_bf16_ts(tmem + L::COL_Y2, tmem + L::COL_G + s * 128 + 8 * e,
+                        tc::mma_bf16_ts(tmem + L::COL_Y2, tmem + L::COL_G + s * 128 + 16 * e,
                                         tc::sw128_desc(v + e * 2048, 16384, 1024), ID_Y, e != 0);
                     tc::mma_commit(y_full);
                 }
-                tc::mma_commit(&empty[s]);
+                tc::mma_commit(&v_empty[s]);
             }
             tc::mma_commit(drain);
-            mbar_wait_bounded(drain, 0, p.limit_ns);
+            tcs_wait(drain, 0);
         }
-    } else if (warp == 2) {
-        // ------------------------------------------------------------ gates
+    } else {
+        // ------------------------------------------------------------ gates, every other chunk
         const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-        TcsGateIn in = {};
-        if (nch > 0) in = tcs_gate_load(p.dt, row_of(0), len_of(0), p.H, h, lane);
-        for (int i = 0; i < nch; ++i) {
-            TcsGateIn next = {};
-            if (i + 1 < nch) next = tcs_gate_load(p.dt, row_of(i + 1), len_of(i + 1), p.H, h, lane);
-            if (i >= 2 && !wait(&gate_free[i & 1], (i >> 1) - 1)) break;
-            tcs_gate_store<REV>(in, gate(i), len_of(i), A, bias, p.softplus, lane);
+        for (int i = warp - 2; i < nch; i += 2) {
+            if (i >= TCS_GATES && !wait(&gate_free[i % TCS_GATES], i / TCS_GATES - 1)) break;
+            tcs_gates<REV>(gate(i), p.dt + row_of(i) * p.H + h, p.H, len_of(i), A, bias, p.softplus, lane);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&gate_full[i & 1]);
-            in = next;
+            if (lane == 0) mbar_arrive(&gate_full[i % TCS_GATES]);
         }
-    } else if (warp >= 4 && warp < 8) {
+    }
+    } else if (warp < 8) {
+        if constexpr (OUT) tc::reg_inc<112>();
         // ------------------------------------------------------------ state
         const int r = tid - 128;  // key channel
         const bool on = DQ == 128 || r < DQ;
@@ -348,13 +394,14 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         for (int j = 0; j < TCS_BV; ++j) S[j] = on && p.S_in ? p.S_in[sbase + (int64_t)j * DQ] : 0.f;
         uint8_t* so = smem + L::S;
         for (int i = 0; i < nch; ++i) {
-            if (!wait(&gate_full[i & 1], i >> 1)) break;
+            if (!wait(&gate_full[i % TCS_GATES], i / TCS_GATES)) break;
             const float decay = ex2f(gate(i)->bh[8] + gate(i)->bl[8]);
             if (!OUT) {
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&gate_free[i & 1]);
+                if (lane == 0) mbar_arrive(&gate_free[i % TCS_GATES]);
             }
             if constexpr (OUT) {
+                if (i > 0 && !wait(y1_done, i - 1)) break;
                 if (on) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -366,6 +413,8 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     }
                 }
                 tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_full);
             } else {
                 // images: rows of 128 bytes, hi then lo, as the products read them
                 const int64_t slot = first / TCS_L + n + chunk_of(i);
@@ -419,179 +468,214 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     }
                 }
             }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(s_full);
             if (!wait(u_full, i)) break;
             tc::fence_after_sync();
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                float u[16];
+                float u[16], v[16];
                 tc::tmem_ld16(tmem + tlane + L::COL_U + 16 * q, u);
+                tc::tmem_ld16(tmem + tlane + L::COL_U + 64 + 16 * q, v);
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) S[16 * q + e] = fmaf(decay, S[16 * q + e], u[e]);
+                for (int e = 0; e < 16; e += 2) {
+                    const float2 t = __ffma2_rn(make_float2(decay, decay),
+                                                make_float2(S[16 * q + e], S[16 * q + e + 1]),
+                                                __fadd2_rn(make_float2(u[e], u[e + 1]), make_float2(v[e], v[e + 1])));
+                    S[16 * q + e] = t.x;
+                    S[16 * q + e + 1] = t.y;
+                }
             }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(u_free);
         }
         if (on && p.S_out && OSDN_IN_BOUNDS(nh, (int64_t)p.N * p.H)) {
 #pragma unroll
             for (int j = 0; j < TCS_BV; ++j) p.S_out[sbase + (int64_t)j * DQ] = S[j];
         }
         if (!OUT && lane == 0) tc::bulk_wait_all();
-    } else if (warp >= 8 && warp < 12) {
-        // ------------------------------------------------------------ V' and output rows
-        const int r = tid - 256;  // token of the chunk
-        const float skip = OUT && p.D ? p.D[h] : 0.f;
+    } else if (warp < 12) {
+        if constexpr (OUT) tc::reg_dec<72>();
+        // ------------------------------------------------------------ V'
+        const int r = tid - 256, b = r >> 4;  // token of the chunk
+        for (int i = 0; i < nch; ++i) {
+            if (!wait(&gate_full[i % TCS_GATES], i / TCS_GATES) || !wait(&v_full[i & 1], i >> 1)) break;
+            const TcsGate* gt = gate(i);
+            // FWD, SAVE: 2^(cum_L - end_b) 2^(end_b - cum_r) step;  RSAVE: 2^(base_b + l_r)
+            const float e = REV ? gt->bh[b] + gt->bl[b]
+                                : (gt->bh[8] - gt->bh[b + 1]) + (gt->bl[8] - gt->bl[b + 1]);
+            const float w = ex2f(e) * gt->g[r];
+            const float2 w2 = make_float2(w, w);
+            uint8_t* v = stage(i) + L::V;
+            uint8_t* vp = smem + L::VP + (i % L::NVP) * 32768;
+            const bool live = r < len_of(i);
+            if (len_of(i) < TCS_L && !wait(&k_full[i & 1], i >> 1)) break;
+            if (!live) {  // the next sequence's row: 0 x NaN must not reach a sum
+                const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t off = tc::sw128_off(r, j);
+                    *reinterpret_cast<uint4*>(v + off) = z;
+#pragma unroll
+                    for (int q = 0; q < DQ / 64; ++q)
+                        *reinterpret_cast<uint4*>(stage(i) + L::K + q * 16384 + off) = z;
+                }
+            }
+            uint4 x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = *reinterpret_cast<const uint4*>(v + tc::sw128_off(r, j));
+            if (i >= L::NVP && !wait(&vp_free[i % L::NVP], i / L::NVP - 1)) break;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t xw[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                uint32_t hw[4], lw[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 t = __fmul2_rn(w2, make_float2(__uint_as_float(xw[k] << 16),
+                                                                __uint_as_float(xw[k] & 0xffff0000u)));
+                    split2_rn(t.x, t.y, hw[k], lw[k]);
+                    if (!live) hw[k] = lw[k] = 0;
+                }
+                const uint32_t off = tc::sw128_off(r, j);
+                *reinterpret_cast<uint4*>(vp + off) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+                *reinterpret_cast<uint4*>(vp + 16384 + off) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+            }
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&vp_full[i % L::NVP]);
+                if (!OUT) mbar_arrive(&gate_free[i % TCS_GATES]);
+            }
+        }
+    } else if constexpr (OUT) {
+    if (warp < 16) {
+        tc::reg_inc<88>();
+        // ------------------------------------------------------------ output rows
+        const int r = tid - 384;  // token of the chunk
+        const float skip = p.D ? p.D[h] : 0.f;
         auto output = [&](int i) -> bool {
             const TcsGate* gt = gate(i);
             const bool live = r < len_of(i);
             const int64_t at = ((row_of(i) + r) * p.H + h) * DV + vt * TCS_BV;
-            uint4 xr[8];
-            if (p.D && live) {
+            const bool add = p.D && live;
+            uint4 xr[8];  // in flight while the products are waited for
 #pragma unroll
-                for (int j = 0; j < 8; ++j) xr[j] = __ldg(reinterpret_cast<const uint4*>(p.x + at) + j);
-            }
+            for (int j = 0; j < 8; ++j)
+                xr[j] = add ? __ldg(reinterpret_cast<const uint4*>(p.x + at) + j) : make_uint4(0, 0, 0, 0);
+            const float rf = ex2f(gt->bh[r >> 4] + gt->l[r] + gt->bl[r >> 4]);
             if (!wait(y_full, i)) return false;
             tc::fence_after_sync();
-            const float rf = ex2f(gt->bh[r >> 4] + gt->l[r] + gt->bl[r >> 4]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 float a[16], b[16];
                 tc::tmem_ld16(tmem + tlane + L::COL_Y1 + 16 * q, a);
                 tc::tmem_ld16(tmem + tlane + L::COL_Y2 + 16 * q, b);
                 tc::tmem_ld_wait();
+                if (q == 3) {  // all read: the next products may overwrite them
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(y_free);
+                        mbar_arrive(&gate_free[i % TCS_GATES]);
+                    }
+                }
+                const uint32_t xw[8] = {xr[2 * q].x, xr[2 * q].y, xr[2 * q].z, xr[2 * q].w,
+                                        xr[2 * q + 1].x, xr[2 * q + 1].y, xr[2 * q + 1].z, xr[2 * q + 1].w};
                 uint32_t w[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    float y0 = fmaf(rf, a[2 * e], b[2 * e]), y1 = fmaf(rf, a[2 * e + 1], b[2 * e + 1]);
-                    if (p.D) {
-                        const uint4 xv = xr[2 * q + (e >> 2)];
-                        const uint32_t xw = (e & 3) == 0 ? xv.x : (e & 3) == 1 ? xv.y : (e & 3) == 2 ? xv.z : xv.w;
-                        y0 = fmaf(skip, __uint_as_float(xw << 16), y0);
-                        y1 = fmaf(skip, __uint_as_float(xw & 0xffff0000u), y1);
-                    }
-                    w[e] = pack2_rn(y0, y1);
+                    const float2 y = __ffma2_rn(
+                        make_float2(skip, skip),
+                        make_float2(__uint_as_float(xw[e] << 16), __uint_as_float(xw[e] & 0xffff0000u)),
+                        __ffma2_rn(make_float2(rf, rf), make_float2(a[2 * e], a[2 * e + 1]),
+                                   make_float2(b[2 * e], b[2 * e + 1])));
+                    w[e] = pack2_rn(y.x, y.y);
                 }
                 if (live && OSDN_IN_BOUNDS(row_of(i) + r, p.rows)) {
                     uint4* o = reinterpret_cast<uint4*>(p.y + at) + 2 * q;
                     o[0] = make_uint4(w[0], w[1], w[2], w[3]);
                     o[1] = make_uint4(w[4], w[5], w[6], w[7]);
                 }
-            }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(y_free);
-                mbar_arrive(&gate_free[i & 1]);
+                __syncwarp();
             }
             return true;
         };
-        bool ok = true;
-        for (int i = 0; ok && i < nch; ++i) {
-            if (!(ok = wait(&full[i & 1], i >> 1) && wait(&gate_full[i & 1], i >> 1))) break;
-            if (i >= L::NVP && !(ok = wait(&vp_free[i % L::NVP], i / L::NVP - 1))) break;
-            const TcsGate* gt = gate(i);
-            const bool live = r < len_of(i);
-            uint8_t* v = stage(i) + L::V;
-            uint8_t* vp = smem + L::VP + (i % L::NVP) * 32768;
-            const int b = r >> 4;
-            // FWD: 2^(cum_L - end_b) 2^(end_b - cum_r) step;  RSAVE: 2^(base_b + l_r)
-            const float e = REV ? gt->bh[b] + gt->bl[b]
-                                : (gt->bh[8] - gt->bh[b + 1]) + (gt->bl[8] - gt->bl[b + 1]);
-            const float w = ex2f(e) * gt->g[r];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t off = tc::sw128_off(r, j);
-                uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-                if (live) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(v + off);
-                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t hw[4], lw[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        split2_rn(w * __uint_as_float(xw[k] << 16), w * __uint_as_float(xw[k] & 0xffff0000u),
-                                  hw[k], lw[k]);
-                    hi = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-                    lo = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-                } else {  // the next sequence's row: 0 x NaN must not reach a sum
-                    *reinterpret_cast<uint4*>(v + off) = hi;
-#pragma unroll
-                    for (int q = 0; q < DQ / 64; ++q)
-                        *reinterpret_cast<uint4*>(stage(i) + L::K + q * 16384 + off) = hi;
-                }
-                *reinterpret_cast<uint4*>(vp + off) = hi;
-                *reinterpret_cast<uint4*>(vp + 16384 + off) = lo;
-            }
-            tc::fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&vp_full[i % L::NVP]);
-                if (!OUT) mbar_arrive(&gate_free[i & 1]);
-            }
-            if (OUT && i > 0) ok = output(i - 1);
-        }
-        if (OUT && ok && nch > 0) output(nch - 1);
-    } else if (OUT && warp >= 12) {
+        for (int i = 0; i < nch; ++i)
+            if (!wait(&gate_full[i % TCS_GATES], i / TCS_GATES) || !output(i)) break;
+    } else {
+        tc::reg_dec<72>();
         // ------------------------------------------------------------ P
-        const int wg = (warp - 12) >> 2, wq = warp & 3;
+        // two warpgroups share P's columns by sub-blocks; P's 16 columns of sub-block b lie over the
+        // first half of their own scores, packed
+        const int wg = (warp - 16) >> 2, wq = warp & 3;
         const int r = 32 * wq + lane, rb = r >> 4;
-        for (int i = wg; i < nch; i += 2) {
-            if (!wait(&gate_full[i & 1], i >> 1) || !wait(&g_full[wg], i >> 1)) break;
-            tc::fence_after_sync();
+        for (int i = 0; i < nch; ++i) {
+            if (!wait(&gate_full[i % TCS_GATES], i / TCS_GATES)) break;
             const TcsGate* gt = gate(i);
             const float lr = gt->l[r], bh = gt->bh[rb], bl = gt->bl[rb];
-            const uint32_t col = tmem + tlane + L::COL_G + wg * 128;
+            if (!wait(&g_full[i & 1], i >> 1)) break;
+            tc::fence_after_sync();
+            const uint32_t col = tmem + tlane + L::COL_G + (i & 1) * 128;
+            float x[16];
+            uint32_t w[8];
 #pragma unroll 1
-            for (int b = 0; b < 8; ++b) {
-                uint32_t w[8];
-                if (b > 2 * wq + 1) {  // past the diagonal for every row of the warp
+            for (int k = 0; k < wq; ++k) {  // sub-blocks in front of every row of the warp
+                const int b = 2 * k + wg;
+                tc::tmem_ld16(col + 16 * b, x);
+                const float f = ex2f((bh - gt->bh[b + 1]) + (bl - gt->bl[b + 1]) + lr);
+                const float4* gp = reinterpret_cast<const float4*>(gt->g + 16 * b);
+                float4 g4[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = 0;
-                } else {
-                    float x[16];
-                    tc::tmem_ld16(col + 16 * b, x);
-                    const float f = ex2f((bh - gt->bh[b + 1]) + (bl - gt->bl[b + 1]) + lr);
-                    const float4* gp = reinterpret_cast<const float4*>(gt->g + 16 * b);
-                    float wt[16];
+                for (int e = 0; e < 4; ++e) g4[e] = gp[e];
+                tc::tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float4 t = gp[e];
-                        wt[4 * e] = f * t.x; wt[4 * e + 1] = f * t.y;
-                        wt[4 * e + 2] = f * t.z; wt[4 * e + 3] = f * t.w;
-                    }
-                    if (b >= 2 * wq) {  // the diagonal's sub-blocks
-                        const float4* lp = reinterpret_cast<const float4*>(gt->l + 16 * b);
-                        const float4* sp = reinterpret_cast<const float4*>(gt->st + 16 * b);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float4 t = lp[e], s = sp[e];
-                            const float tv[4] = {t.x, t.y, t.z, t.w}, sv[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int c = 16 * b + 4 * e + k;
-                                if (b == rb) wt[4 * e + k] = ex2f(lr - tv[k]) * sv[k];
-                                if (c > r) wt[4 * e + k] = 0.f;
-                            }
-                        }
-                    }
-                    tc::tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float p0 = x[2 * e] * wt[2 * e], p1 = x[2 * e + 1] * wt[2 * e + 1];
-                        if (b >= 2 * wq) {  // a NaN or infinity past the diagonal is left out too
-                            if (16 * b + 2 * e > r) p0 = 0.f;
-                            if (16 * b + 2 * e + 1 > r) p1 = 0.f;
-                        }
-                        w[e] = pack2_rn(p0, p1);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f2 = make_float2(f, f);
+                    const float2 t = __fmul2_rn(__fmul2_rn(f2, make_float2(g4[e].x, g4[e].y)),
+                                                make_float2(x[4 * e], x[4 * e + 1]));
+                    const float2 u = __fmul2_rn(__fmul2_rn(f2, make_float2(g4[e].z, g4[e].w)),
+                                                make_float2(x[4 * e + 2], x[4 * e + 3]));
+                    w[2 * e] = pack2_rn(t.x, t.y);
+                    w[2 * e + 1] = pack2_rn(u.x, u.y);
                 }
-                tc::tmem_st8(col + 8 * b, w);
+                tc::tmem_st8(col + 16 * b, w);
             }
+            {  // the sub-blocks on the diagonal: wg = 0: of the first 16 rows, wg = 1: of the others
+                const int b = 2 * wq + wg;
+                tc::tmem_ld16(col + 16 * b, x);
+                // cum_r - (the sum in front of the sub-block): l_r itself where it is the row's own
+                const float d = (bh - gt->bh[b]) + (bl - gt->bl[b]) + lr;
+                const float4* lp = reinterpret_cast<const float4*>(gt->l + 16 * b);
+                const float4* sp = reinterpret_cast<const float4*>(gt->st + 16 * b);
+                const int c0 = 16 * b;
+                float wt[16];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float4 l4 = lp[e], s4 = sp[e];
+                    wt[4 * e] = ex2f(d - l4.x) * s4.x;
+                    wt[4 * e + 1] = ex2f(d - l4.y) * s4.y;
+                    wt[4 * e + 2] = ex2f(d - l4.z) * s4.z;
+                    wt[4 * e + 3] = ex2f(d - l4.w) * s4.w;
+                }
+                tc::tmem_ld_wait();
+                // what lies past the diagonal is left out, infinities and NaN too
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    w[e] = pack2_rn(c0 + 2 * e > r ? 0.f : x[2 * e] * wt[2 * e],
+                                    c0 + 2 * e + 1 > r ? 0.f : x[2 * e + 1] * wt[2 * e + 1]);
+                __syncwarp();
+                tc::tmem_st8(col + 16 * b, w);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = 0;
+#pragma unroll 1
+            for (int k = wq + 1; k < 4; ++k) tc::tmem_st8(col + 16 * (2 * k + wg), w);
             tc::tmem_st_wait();
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[wg]);
+            if (lane == 0) mbar_arrive(&p_full[i & 1]);
         }
+    }
     }
     tc::fence_before_sync();
     __syncthreads();

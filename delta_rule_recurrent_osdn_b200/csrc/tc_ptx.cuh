@@ -138,6 +138,16 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
         : "memory");
 }
 
+// ---------------------------------------------------------------- registers
+// Every warp of a warpgroup gives registers back to, or takes them from, what its block was
+// launched with (threads x registers at launch): the warpgroups' shares must not add up to more.
+template <int N> __device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ---------------------------------------------------------------- thread-block clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
