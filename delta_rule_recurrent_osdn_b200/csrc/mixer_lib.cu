@@ -224,12 +224,44 @@ bool make_chunk_map(CUtensorMap* m, const void* base, int D, int heads, int64_t 
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// q, k: [rows][G][DQ], v: [rows][H][nvt * 64] (q only in the forward pass).
+// How the forward pass cuts sequences into segments: tokens of one (INT_MAX: no cuts), how many
+// numbers they take, and the bytes they need.  148 SMs (a constant, so that the workspace's size
+// does not need a device) take one CTA each.
+//   Equal sequences: as many segments each as keep every CTA on an SM of its own, if a sequence
+//   still gives 4 chunks to a segment (the first launch re-reads b and x and costs about half
+//   a chunk's time per chunk: two segments win from about 8 chunks on).
+//   Packed sequences, whose lengths the host does not know: twice the tokens that an even split
+//   of the whole would give a CTA, so only sequences far above the average are cut.
+struct SsmSegments { int seg; int64_t slots; size_t state, decay, bytes; };
+SsmSegments ssm_segments(bool packed, int64_t rows, int64_t N, int64_t T, int H, int Dk, int Dv) {
+    const int64_t nvt = Dv / TCS_BV, chunks = ceil_div(packed ? rows : T, TCS_L), sms = 148;
+    SsmSegments s = {INT_MAX, N, 0, 0, 0};
+    int64_t len = chunks;
+    if (packed) {
+        len = 2 * ceil_div(chunks * H * nvt, sms);
+        len = len < 4 ? 4 : len;
+    } else if (N * H * nvt > 0) {
+        const int64_t most = chunks / 4, fit = sms / (N * H * nvt);
+        const int64_t segs = fit < most ? fit : most;
+        if (segs >= 2) len = ceil_div(chunks, segs);
+    }
+    if (len < chunks && len * TCS_L < INT_MAX) {
+        s.seg = (int)(len * TCS_L);
+        s.slots = rows / s.seg + N;
+        s.state = 0;
+        s.decay = up256((size_t)s.slots * H * Dv * Dk * 4);
+        s.bytes = s.decay + up256((size_t)s.slots * H * 4);
+    }
+    return s;
+}
+
+// q, k: [rows][G][DQ], v: [rows][H][nvt * 64] (q only in the forward pass).  slots: the segments'
+// numbers, or the sequences'.
 template <int DQ, int MODE>
-osdn_status_t launch_tc_chain(const void* q, const void* k, const void* v, TcsArgs a,
-                              cudaStream_t stream) {
+osdn_status_t launch_tc_chain(const void* q, const void* k, const void* v, const TcsArgs& a,
+                              int64_t slots, cudaStream_t stream) {
     using L = TcsSmem<DQ, MODE>;
-    const int64_t ctas = (int64_t)a.N * a.H * a.nvt;
+    const int64_t ctas = slots * a.H * a.nvt;
     if (ctas == 0) return OSDN_OK;
     if (ctas > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
     CUtensorMap mq, mk, mv;
@@ -240,6 +272,16 @@ osdn_status_t launch_tc_chain(const void* q, const void* k, const void* v, TcsAr
     if (!set_smem(kern, L::BYTES)) return OSDN_ERR_CUDA;
     kern<<<dim3((unsigned)ctas), dim3(L::THREADS), L::BYTES, stream>>>(mq, mk, mv, a);
     return launch_status();
+}
+
+template <int DQ>
+osdn_status_t launch_tc_fwd(const void* q, const void* k, const void* v, const TcsArgs& a,
+                            int64_t slots, cudaStream_t stream) {
+    if (a.seg != INT_MAX) {
+        const osdn_status_t st = launch_tc_chain<DQ, TCS_SEG>(nullptr, k, v, a, slots, stream);
+        if (st != OSDN_OK) return st;
+    }
+    return launch_tc_chain<DQ, TCS_FWD>(q, k, v, a, slots, stream);
 }
 
 osdn_status_t check_ssm(int32_t H, int32_t G, int32_t Dk, int32_t Dv) {
@@ -431,7 +473,8 @@ osdn_status_t osdn_ssm_fwd(const void* x, const float* dt, const float* A, const
     if (st != OSDN_OK) return st;
     if (softplus != 0 && softplus != 1) return OSDN_ERR_INVALID_ARG;
     if (!A || (rows > 0 && (!x || !dt || !b || !c || !y))) return OSDN_ERR_INVALID_ARG;
-    const size_t need = osdn_ssm_fwd_workspace_bytes(num_seqs, B, T, H, Dk, Dv, io);
+    const size_t need =
+        osdn_ssm_fwd_workspace_bytes(cu_seqlens ? num_seqs : 0, B, T, H, Dk, Dv, io);
     st = check_workspace(workspace, workspace_bytes, need);
     if (st != OSDN_OK) return st;
     const size_t es = io_size(io), xb = (size_t)rows * H * Dv * es, gb = (size_t)rows * G * Dk * es,
@@ -454,15 +497,22 @@ osdn_status_t osdn_ssm_fwd(const void* x, const float* dt, const float* A, const
         t.S_in = S0; t.y = static_cast<__nv_bfloat16*>(y); t.S_out = ST; t.cu = cu_seqlens;
         t.rows = rows; t.N = (int)N; t.T = T; t.H = H; t.G = G; t.softplus = softplus;
         t.nvt = Dv / TCS_BV;
-        return Dk == 128 ? launch_tc_chain<128, TCS_FWD>(c, b, x, t, s)
-                         : launch_tc_chain<64, TCS_FWD>(c, b, x, t, s);
+        const SsmSegments sg = ssm_segments(cu_seqlens != nullptr, rows, N, T, H, Dk, Dv);
+        t.seg = sg.seg;
+        t.seg_state = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sg.state);
+        t.seg_decay = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sg.decay);
+        return Dk == 128 ? launch_tc_fwd<128>(c, b, x, t, sg.slots, s)
+                         : launch_tc_fwd<64>(c, b, x, t, sg.slots, s);
     }
     return launch_ssm_scan<SSM_FWD, float>(a, Dk, Dv, s);
 }
 
-size_t osdn_ssm_fwd_workspace_bytes(int32_t, int32_t, int32_t, int32_t, int32_t, int32_t,
-                                    osdn_dtype_t) {
-    return 0;
+size_t osdn_ssm_fwd_workspace_bytes(int32_t num_seqs, int32_t B, int32_t T, int32_t H, int32_t Dk,
+                                    int32_t Dv, osdn_dtype_t io) {
+    if (B < 0 || T < 0 || H < 1 || num_seqs < 0 || (Dk != 64 && Dk != 128) ||
+        (Dv != 64 && Dv != 128) || io != OSDN_BF16 || (int64_t)B * T == 0)
+        return 0;
+    return ssm_segments(num_seqs > 0, (int64_t)B * T, num_seqs > 0 ? num_seqs : B, T, H, Dk, Dv).bytes;
 }
 
 osdn_status_t osdn_ssm_step(const void* x, const float* dt, const float* A, const void* b,

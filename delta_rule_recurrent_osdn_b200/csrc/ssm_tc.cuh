@@ -31,6 +31,8 @@
 // run into their own bounds, and everything in flight is waited for before the CTA leaves.
 #pragma once
 
+#include <limits.h>
+
 #include "mixer_common.cuh"
 #include "tc_ptx.cuh"
 
@@ -41,8 +43,9 @@ constexpr int TCS_BV = 64;   // value channels per CTA
 constexpr int TCS_GATES = 8; // chunks whose gates are kept: they are made well ahead of their use
 
 // What a launch of the chain does: the forward pass; the states in front of every chunk (stored
-// as bf16 hi / lo images); the same for the gradient's chain, backwards in time.
-enum { TCS_FWD = 0, TCS_SAVE = 1, TCS_RSAVE = 2 };
+// as bf16 hi / lo images); the same for the gradient's chain, backwards in time; what each
+// segment of a sequence adds to a zero state.
+enum { TCS_FWD = 0, TCS_SAVE = 1, TCS_RSAVE = 2, TCS_SEG = 3 };
 
 struct TcsArgs {
     const float *dt, *A, *dt_bias;
@@ -56,6 +59,9 @@ struct TcsArgs {
     float* gs;                     // RSAVE: <G, S> shares [DV / 64 * DQ / 32][slot][H]
     const int32_t* cu;
     int64_t rows;
+    float* seg_state;              // SEG writes, FWD reads: [slot][H][nvt][64][DQ]
+    float* seg_decay;              // ... and the segment's whole log2 decay [slot][H]
+    int seg;                       // tokens of a segment (a multiple of TCS_L; INT_MAX: none)
     int N, T, H, G, softplus, nvt;
 };
 
@@ -188,6 +194,24 @@ __device__ __forceinline__ void tcs_mma(uint32_t d, uint64_t a, uint64_t b, uint
         tc::mma_bf16(d, a + e * da + (e >> 2) * ga, b + e * db + (e >> 2) * gb, id, e != 0);
 }
 
+// Segments.  When there are too few (sequence, head) chains for the machine, sequences are cut into
+// segments of p.seg tokens that run side by side: a first launch (SEG) makes what each segment
+// adds to a zero state, and a segment of the forward pass builds its initial state from S0 and
+// the segments in front of it.  Segments are numbered like blocks of tokens (ssm_slots): sequence
+// n's from first / seg + n on, with unused numbers in between.
+__device__ __forceinline__ bool tcs_segment(const TcsArgs& p, int slot, int& n, int& s) {
+    int lo = 0, hi = p.N - 1;  // the last n whose numbers start at or before slot
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        const int64_t first = p.cu ? (int64_t)__ldg(p.cu + mid) : (int64_t)mid * p.T;
+        if (first / p.seg + mid <= slot) lo = mid; else hi = mid - 1;
+    }
+    const int64_t first = p.cu ? (int64_t)__ldg(p.cu + lo) : (int64_t)lo * p.T;
+    n = lo;
+    s = (int)(slot - (first / p.seg + lo));
+    return s >= 0;
+}
+
 template <int DQ, int MODE>
 __global__ void __launch_bounds__(TcsSmem<DQ, MODE>::THREADS, 1)
 ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -198,11 +222,21 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     uint8_t* smem = smem_align1024(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int vt = blockIdx.x % p.nvt;
-    const int64_t nh = blockIdx.x / p.nvt;
-    const int n = (int)(nh / p.H), h = (int)(nh - (int64_t)n * p.H), g = h / (p.H / p.G);
+    const int slot = (int)(blockIdx.x / p.nvt / p.H), h = (int)(blockIdx.x / p.nvt - (int64_t)slot * p.H);
+    const int g = h / (p.H / p.G);
+    int n, seg;
     int64_t first, count;
-    if (!seq_range(p.cu, n, p.N, p.T, first, count)) return;  // uniform over the CTA
+    // every sequence's offsets are checked here, whether or not a number leads to it
+    if (slot < p.N && !seq_range(p.cu, slot, p.N, p.T, first, count) && p.seg == INT_MAX) return;
+    if (!tcs_segment(p, slot, n, seg) || !seq_range(p.cu, n, p.N, p.T, first, count)) return;
+    const int64_t start = (int64_t)seg * p.seg;  // of the segment in its sequence
+    if (seg > 0 && start >= count) return;       // a number that no segment has
+    const bool last = count - start <= p.seg;
+    if (MODE == TCS_SEG && last) return;
+    first += start;                              // all uniform over the CTA
+    count = last ? count - start : p.seg;
     const int nch = (int)((count + TCS_L - 1) / TCS_L);
+    const int64_t nh = (int64_t)n * p.H + h;
     const int DV = p.nvt * TCS_BV;
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
@@ -392,6 +426,15 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         const int64_t sbase = (nh * DV + vt * TCS_BV) * DQ + r;  // stored [value][key]
 #pragma unroll
         for (int j = 0; j < TCS_BV; ++j) S[j] = on && p.S_in ? p.S_in[sbase + (int64_t)j * DQ] : 0.f;
+        if constexpr (OUT) {
+            for (int e = slot - seg; on && e < slot; ++e) {  // the segments in front
+                const float d = ex2f(p.seg_decay[(int64_t)e * p.H + h]);
+                const float* a = p.seg_state + (((int64_t)e * p.H + h) * p.nvt + vt) * (TCS_BV * DQ) + r;
+#pragma unroll
+                for (int j = 0; j < TCS_BV; ++j) S[j] = fmaf(d, S[j], a[j * DQ]);
+            }
+        }
+        float total = 0.f;  // SEG: log2 decay so far
         uint8_t* so = smem + L::S;
         for (int i = 0; i < nch; ++i) {
             if (!wait(&gate_full[i % TCS_GATES], i / TCS_GATES)) break;
@@ -415,10 +458,12 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 tc::fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_full);
+            } else if constexpr (MODE == TCS_SEG) {
+                total += gate(i)->bh[8];
             } else {
                 // images: rows of 128 bytes, hi then lo, as the products read them
-                const int64_t slot = first / TCS_L + n + chunk_of(i);
-                const int64_t at = ((slot * p.H + h) * p.nvt + vt) * (2 * DQ * 128);
+                const int64_t cs = first / TCS_L + n + chunk_of(i);
+                const int64_t at = ((cs * p.H + h) * p.nvt + vt) * (2 * DQ * 128);
                 if constexpr (REV) {  // <G, S> against the forward chain's state
                     float dot = 0.f;
                     if (on) {
@@ -440,8 +485,8 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     dot = warp_sum_f(dot) * decay;
                     if (on && lane == 0) {
                         const int64_t slots = ssm_slots(p.rows, p.N, TCS_L);
-                        if (OSDN_IN_BOUNDS(slot, slots))
-                            p.gs[((int64_t)(vt * (DQ / 32) + (warp & 3)) * slots + slot) * p.H + h] = dot;
+                        if (OSDN_IN_BOUNDS(cs, slots))
+                            p.gs[((int64_t)(vt * (DQ / 32) + (warp & 3)) * slots + cs) * p.H + h] = dot;
                     }
                 }
                 if (on) {
@@ -460,7 +505,7 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     }
                     tc::fence_async_smem();
                     __syncwarp();
-                    if (lane == 0 && OSDN_IN_BOUNDS(slot, ssm_slots(p.rows, p.N, TCS_L))) {
+                    if (lane == 0 && OSDN_IN_BOUNDS(cs, ssm_slots(p.rows, p.N, TCS_L))) {
                         const uint32_t w0 = (warp & 3) * 4096;
                         tc::bulk_store(p.img + at + w0, so + w0, 4096);
                         tc::bulk_store(p.img + at + DQ * 128 + w0, so + 16384 + w0, 4096);
@@ -489,7 +534,15 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(u_free);
         }
-        if (on && p.S_out && OSDN_IN_BOUNDS(nh, (int64_t)p.N * p.H)) {
+        if constexpr (MODE == TCS_SEG) {
+            const int64_t at = (int64_t)slot * p.H + h;
+            if (on && OSDN_IN_BOUNDS(slot, p.rows / p.seg + p.N)) {
+#pragma unroll
+                for (int j = 0; j < TCS_BV; ++j)
+                    p.seg_state[(at * p.nvt + vt) * (TCS_BV * DQ) + j * DQ + r] = S[j];
+                if (r == 0 && vt == 0) p.seg_decay[at] = total;
+            }
+        } else if (on && p.S_out && last && OSDN_IN_BOUNDS(nh, (int64_t)p.N * p.H)) {
 #pragma unroll
             for (int j = 0; j < TCS_BV; ++j) p.S_out[sbase + (int64_t)j * DQ] = S[j];
         }

@@ -186,6 +186,10 @@ SCANS = [  # io, lens, packed, H, G, Dk, Dv, D, bias, state, softplus
     ("bf16", [3, 257, 0, 0, 128, 1], True, 4, 1, 128, 128, True, True, True, True),
     ("bf16", [40, 1, 200], True, 6, 3, 64, 64, True, True, False, True),
     ("bf16", [600], False, 2, 1, 128, 64, True, True, True, True),
+    # long enough for the few heads that sequences are cut into segments
+    ("bf16", [1100], False, 2, 1, 64, 128, True, True, True, True),
+    ("bf16", [1400, 3, 0, 512, 200], True, 2, 2, 128, 64, True, True, True, True),
+    ("bf16", [1, 1025], True, 3, 1, 128, 128, False, True, False, True),
 ]
 SCAN_IDS = [f"{s[0]}-{'.'.join(map(str, s[1]))}-H{s[3]}G{s[4]}k{s[5]}v{s[6]}" for s in SCANS]
 
