@@ -14,6 +14,7 @@
 #include "ssm_step.cuh"
 #include "ssm_scan.cuh"
 #include "ssm_tc.cuh"
+#include "ssm_tc_bwd.cuh"
 
 namespace osdn {
 
@@ -290,11 +291,15 @@ osdn_status_t check_ssm(int32_t H, int32_t G, int32_t Dk, int32_t Dv) {
     return OSDN_OK;
 }
 
-// Workspace of osdn_ssm_bwd, each part rounded up to 256 bytes.
+// Workspace of osdn_ssm_bwd, each part rounded up to 256 bytes.  fp32 tokens: the heads' dc and
+// db, the state behind each block of SSM_BLOCK tokens.  bf16 tokens: the states in front of and
+// the gradients behind each chunk as bf16 hi / lo images, the heads' dc and db when heads share
+// rows of b and c.  Both: the sums that the step gradient is made of.
 struct SsmBwdWorkspace {
-    size_t dch, dbh, ckpt, gs, pos, rneg, vk, part, total;
+    size_t dch, dbh, ckpt, ckpt_r, gs, pos, ri, rn, vk, part, total;
 };
-SsmBwdWorkspace ssm_bwd_workspace(int64_t rows, int64_t N, int32_t H, int32_t Dk, int32_t Dv) {
+SsmBwdWorkspace ssm_bwd_workspace(int64_t rows, int64_t N, int32_t H, int32_t G, int32_t Dk,
+                                  int32_t Dv, osdn_dtype_t io) {
     SsmBwdWorkspace w;
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -302,67 +307,127 @@ SsmBwdWorkspace ssm_bwd_workspace(int64_t rows, int64_t N, int32_t H, int32_t Dk
         off += up256(bytes);
         return at;
     };
-    const size_t th = (size_t)rows * H, slots = (size_t)ssm_slots(rows, N, SSM_BLOCK);
-    w.dch = take(th * Dk * 4);
-    w.dbh = take(th * Dk * 4);
+    const bool tc = io == OSDN_BF16;
+    const size_t th = (size_t)rows * H, slots = (size_t)ssm_slots(rows, N, tc ? TCS_L : SSM_BLOCK);
+    const size_t heads = !tc || G < H ? th * Dk * 4 : 0, shares = tc ? 2 : 1;
+    w.dch = take(heads);
+    w.dbh = take(heads);
     w.ckpt = take(slots * H * Dk * Dv * 4);
-    w.gs = take(slots * H * (Dk / SSM_BV) * 4);
-    w.pos = take(th * 4);
-    w.rneg = take(th * 4);
+    w.ckpt_r = take(tc ? slots * H * Dk * Dv * 4 : 0);
+    w.gs = take(slots * H * (tc ? Dv / TCS_BV * (Dk / 32) : Dk / SSM_BV) * 4);
+    w.pos = take(shares * th * 4);
+    w.ri = take(shares * th * 4);
+    w.rn = take(tc ? shares * th * 4 : 0);
     w.vk = take(th * 4);
     w.part = take((size_t)3 * N * H * 8);
     w.total = off;
     return w;
 }
 
-template <typename IO>
-osdn_status_t launch_ssm_bwd(const void* x, const float* dt, const float* A, const void* b,
-                             const void* c, const float* D, const float* dt_bias, int softplus,
-                             const float* S0, const void* dy, const float* dST, void* dx,
-                             float* ddt, float* dA, void* db, void* dc, float* dD, float* ddt_bias,
-                             float* dS0, const int32_t* cu, int64_t N, int T, int H, int G, int Dk,
-                             int Dv, int64_t rows, uint8_t* ws, cudaStream_t stream) {
-    const SsmBwdWorkspace w = ssm_bwd_workspace(rows, N, H, Dk, Dv);
-    auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
+struct SsmBwdCall {
+    const void* x; const float *dt, *A; const void *b, *c; const float *D, *dt_bias; int softplus;
+    const float* S0; const void* dy; const float* dST; void* dx; float *ddt, *dA; void *db, *dc;
+    float *dD, *ddt_bias, *dS0; const int32_t* cu; int64_t N; int T, H, G, Dk, Dv; int64_t rows;
+    uint8_t* ws; cudaStream_t stream;
+};
+
+// ddt of every token, then dA, dD and ddt_bias.
+template <int BLOCK>
+osdn_status_t launch_ssm_gates(const SsmBwdCall& k, const SsmBwdWorkspace& w, const float* rn,
+                               int shares, int nslice) {
+    auto f32 = [&](size_t at) { return reinterpret_cast<float*>(k.ws + at); };
+    double* part = reinterpret_cast<double*>(k.ws + w.part);
+    if (k.N > 0) {
+        ssm_gate_kernel<BLOCK><<<dim3((unsigned)(k.N * k.H)), dim3(32 * SSM_GATE_WARPS), 0, k.stream>>>(
+            f32(w.pos), f32(w.ri), rn, shares, f32(w.gs), nslice, k.dD ? f32(w.vk) : nullptr, k.dt, k.A,
+            k.dt_bias, k.softplus, k.ddt, part, k.cu, (int)k.N, k.T, k.H, k.rows);
+        const osdn_status_t st = launch_status();
+        if (st != OSDN_OK) return st;
+    }
+    ssm_param_kernel<<<3, 256, 0, k.stream>>>(part, (int)k.N, k.H, k.dA, k.dD, k.ddt_bias);
+    return launch_status();
+}
+
+// fp32 tokens, and calls without tokens: three scans token by token.
+osdn_status_t launch_ssm_bwd_f32(const SsmBwdCall& k) {
+    const SsmBwdWorkspace w = ssm_bwd_workspace(k.rows, k.N, k.H, k.G, k.Dk, k.Dv, OSDN_F32);
+    auto f32 = [&](size_t at) { return reinterpret_cast<float*>(k.ws + at); };
     SsmArgs a = {};
-    a.dt = dt; a.A = A; a.D = D; a.dt_bias = dt_bias; a.softplus = softplus;
-    a.cu = cu; a.rows = rows; a.N = (int)N; a.T = T; a.H = H; a.G = G;
+    a.dt = k.dt; a.A = k.A; a.D = k.D; a.dt_bias = k.dt_bias; a.softplus = k.softplus;
+    a.cu = k.cu; a.rows = k.rows; a.N = (int)k.N; a.T = k.T; a.H = k.H; a.G = k.G;
     a.ckpt = f32(w.ckpt);
     a.gs = f32(w.gs);
     SsmArgs dcp = a, dxp = a, dbp = a;
-    dcp.q = dy; dcp.k = x; dcp.v = b; dcp.S_in = S0; dcp.out = f32(w.dch); dcp.vk = dD ? f32(w.vk) : nullptr;
-    dxp.q = b; dxp.k = c; dxp.v = dy; dxp.S_in = dST; dxp.out = dx; dxp.S_out = dS0;
-    dbp.q = x; dbp.k = dy; dbp.v = c; dbp.S_in = dST; dbp.out = f32(w.dbh);
-    osdn_status_t st = launch_ssm_scan<SSM_DC, IO>(dcp, Dv, Dk, stream);
-    if (st == OSDN_OK) st = launch_ssm_scan<SSM_DX, IO>(dxp, Dk, Dv, stream);
-    if (st == OSDN_OK) st = launch_ssm_scan<SSM_DB, IO>(dbp, Dv, Dk, stream);
+    dcp.q = k.dy; dcp.k = k.x; dcp.v = k.b; dcp.S_in = k.S0; dcp.out = f32(w.dch);
+    dcp.vk = k.dD ? f32(w.vk) : nullptr;
+    dxp.q = k.b; dxp.k = k.c; dxp.v = k.dy; dxp.S_in = k.dST; dxp.out = k.dx; dxp.S_out = k.dS0;
+    dbp.q = k.x; dbp.k = k.dy; dbp.v = k.c; dbp.S_in = k.dST; dbp.out = f32(w.dbh);
+    osdn_status_t st = launch_ssm_scan<SSM_DC, float>(dcp, k.Dv, k.Dk, k.stream);
+    if (st == OSDN_OK) st = launch_ssm_scan<SSM_DX, float>(dxp, k.Dk, k.Dv, k.stream);
+    if (st == OSDN_OK) st = launch_ssm_scan<SSM_DB, float>(dbp, k.Dv, k.Dk, k.stream);
     if (st != OSDN_OK) return st;
-    if (rows > 0) {
-        const int64_t need = ceil_div(rows * G, 8), cap = 16LL * sm_count();
+    if (k.rows > 0) {
+        const int64_t need = ceil_div(k.rows * k.G, 8), cap = 16LL * sm_count();
         const dim3 grid((unsigned)(need < cap ? need : cap));
-        if (Dk == 128)
-            ssm_group_kernel<128, IO><<<grid, 256, 0, stream>>>(
-                f32(w.dch), f32(w.dbh), static_cast<const IO*>(b), static_cast<const IO*>(c), dt,
-                dt_bias, softplus, static_cast<IO*>(db), static_cast<IO*>(dc), f32(w.pos),
-                f32(w.rneg), rows, H, G);
-        else
-            ssm_group_kernel<64, IO><<<grid, 256, 0, stream>>>(
-                f32(w.dch), f32(w.dbh), static_cast<const IO*>(b), static_cast<const IO*>(c), dt,
-                dt_bias, softplus, static_cast<IO*>(db), static_cast<IO*>(dc), f32(w.pos),
-                f32(w.rneg), rows, H, G);
+        auto kern = k.Dk == 128 ? ssm_group_kernel<128, float> : ssm_group_kernel<64, float>;
+        kern<<<grid, 256, 0, k.stream>>>(f32(w.dch), f32(w.dbh), static_cast<const float*>(k.b),
+                                         static_cast<const float*>(k.c), k.dt, k.dt_bias, k.softplus,
+                                         static_cast<float*>(k.db), static_cast<float*>(k.dc),
+                                         f32(w.pos), f32(w.ri), k.rows, k.H, k.G);
         st = launch_status();
         if (st != OSDN_OK) return st;
     }
-    double* part = reinterpret_cast<double*>(ws + w.part);
-    if (N > 0) {
-        ssm_gate_kernel<<<dim3((unsigned)(N * H)), dim3(32 * SSM_GATE_WARPS), 0, stream>>>(
-            f32(w.pos), f32(w.rneg), f32(w.gs), Dk / SSM_BV, dcp.vk, dt, A, dt_bias, softplus, ddt,
-            part, cu, (int)N, T, H, rows);
+    return launch_ssm_gates<SSM_BLOCK>(k, w, nullptr, 1, k.Dk / SSM_BV);
+}
+
+// bf16 tokens: the two chains of states, then all chunks at once.
+template <int DK, int DV> osdn_status_t launch_ssm_bwd_tc(const SsmBwdCall& k) {
+    using bf16 = __nv_bfloat16;
+    const SsmBwdWorkspace w = ssm_bwd_workspace(k.rows, k.N, k.H, k.G, DK, DV, OSDN_BF16);
+    auto f32 = [&](size_t at) { return reinterpret_cast<float*>(k.ws + at); };
+    TcsArgs a = {};
+    a.dt = k.dt; a.A = k.A; a.dt_bias = k.dt_bias; a.softplus = k.softplus; a.cu = k.cu;
+    a.rows = k.rows; a.N = (int)k.N; a.T = k.T; a.H = k.H; a.G = k.G; a.nvt = DV / TCS_BV;
+    a.seg = INT_MAX;
+    TcsArgs f = a, r = a;
+    f.S_in = k.S0; f.img = k.ws + w.ckpt;
+    r.S_in = k.dST; r.img = k.ws + w.ckpt_r; r.img_fwd = k.ws + w.ckpt; r.gs = f32(w.gs);
+    r.S_out = k.dS0;
+    osdn_status_t st = launch_tc_chain<DK, TCS_SAVE>(nullptr, k.b, k.x, f, k.N, k.stream);
+    if (st == OSDN_OK) st = launch_tc_chain<DK, TCS_RSAVE>(nullptr, k.c, k.dy, r, k.N, k.stream);
+    if (st != OSDN_OK) return st;
+    TcgArgs g = {};
+    g.dt = k.dt; g.A = k.A; g.dt_bias = k.dt_bias; g.D = k.D; g.softplus = k.softplus;
+    g.img = k.ws + w.ckpt; g.img_r = k.ws + w.ckpt_r; g.dx = static_cast<bf16*>(k.dx);
+    if (k.G == k.H) {
+        g.db = static_cast<bf16*>(k.db);
+        g.dc = static_cast<bf16*>(k.dc);
+    } else {
+        g.dbh = f32(w.dbh);
+        g.dch = f32(w.dch);
+    }
+    g.pos = f32(w.pos); g.ri = f32(w.ri); g.rn = f32(w.rn); g.vk = k.dD ? f32(w.vk) : nullptr;
+    g.cu = k.cu; g.rows = k.rows; g.N = (int)k.N; g.T = k.T; g.H = k.H; g.G = k.G;
+    g.slots = ssm_slots(k.rows, k.N, TCS_L);
+    if (g.slots * k.H > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
+    using L = TcgSmem<DK, DV>;
+    CUtensorMap mx, my, mb, mc;
+    if (!make_chunk_map(&mx, k.x, DV, k.H, k.rows) || !make_chunk_map(&my, k.dy, DV, k.H, k.rows) ||
+        !make_chunk_map(&mb, k.b, DK, k.G, k.rows) || !make_chunk_map(&mc, k.c, DK, k.G, k.rows))
+        return OSDN_ERR_CUDA;
+    auto kern = ssm_tc_grad_kernel<DK, DV>;
+    if (!set_smem(kern, L::BYTES)) return OSDN_ERR_CUDA;
+    kern<<<dim3((unsigned)(g.slots * k.H)), dim3(L::THREADS), L::BYTES, k.stream>>>(mx, my, mb, mc, g);
+    st = launch_status();
+    if (st != OSDN_OK) return st;
+    if (k.G < k.H) {
+        const int64_t n = k.rows * k.G * DK / 8, need = ceil_div(n, 256), cap = 16LL * sm_count();
+        ssm_group_sum_kernel<<<dim3((unsigned)(need < cap ? need : cap)), 256, 0, k.stream>>>(
+            f32(w.dbh), f32(w.dch), static_cast<bf16*>(k.db), static_cast<bf16*>(k.dc), n, k.H / k.G, DK);
         st = launch_status();
         if (st != OSDN_OK) return st;
     }
-    ssm_param_kernel<<<3, 256, 0, stream>>>(part, (int)N, H, dA, dD, ddt_bias);
-    return launch_status();
+    return launch_ssm_gates<TCS_L>(k, w, g.rn, 2, DV / TCS_BV * (DK / 32));
 }
 
 }  // namespace
@@ -557,7 +622,9 @@ size_t osdn_ssm_bwd_workspace_bytes(int32_t num_seqs, int32_t B, int32_t T, int3
     if (B < 0 || T < 0 || H < 1 || num_seqs < 0 || (Dk != 64 && Dk != 128) ||
         (Dv != 64 && Dv != 128) || (io != OSDN_BF16 && io != OSDN_F32))
         return 0;
-    return ssm_bwd_workspace((int64_t)B * T, num_seqs > 0 ? num_seqs : B, H, Dk, Dv).total;
+    // enough for heads that share rows of b and c, and for a call without tokens
+    const int64_t rows = (int64_t)B * T, N = num_seqs > 0 ? num_seqs : B;
+    return ssm_bwd_workspace(rows, N, H, 1, Dk, Dv, rows > 0 ? io : OSDN_F32).total;
 }
 
 osdn_status_t osdn_ssm_bwd(const void* x, const float* dt, const float* A, const void* b,
@@ -574,7 +641,8 @@ osdn_status_t osdn_ssm_bwd(const void* x, const float* dt, const float* A, const
     if (softplus != 0 && softplus != 1) return OSDN_ERR_INVALID_ARG;
     if (!A || !dA || (rows > 0 && (!x || !dt || !b || !c || !dy || !dx || !ddt || !db || !dc)))
         return OSDN_ERR_INVALID_ARG;
-    const size_t need = ssm_bwd_workspace(rows, N, H, Dk, Dv).total;
+    const osdn_dtype_t path = rows > 0 ? io : OSDN_F32;
+    const size_t need = ssm_bwd_workspace(rows, N, H, G, Dk, Dv, path).total;
     st = check_workspace(workspace, workspace_bytes, need);
     if (st != OSDN_OK) return st;
     if (N * H > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
@@ -586,14 +654,12 @@ osdn_status_t osdn_ssm_bwd(const void* x, const float* dt, const float* A, const
                        {ddt_bias, hb}, {dS0, sb}, {workspace, need}};
     st = check_buffers(in, 11, out, 9);
     if (st != OSDN_OK) return st;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    if (io == OSDN_BF16)
-        return launch_ssm_bwd<__nv_bfloat16>(x, dt, A, b, c, D, dt_bias, softplus, S0, dy, dST, dx,
-                                             ddt, dA, db, dc, dD, ddt_bias, dS0, cu_seqlens, N, T, H,
-                                             G, Dk, Dv, rows, ws, s);
-    return launch_ssm_bwd<float>(x, dt, A, b, c, D, dt_bias, softplus, S0, dy, dST, dx, ddt, dA, db,
-                                 dc, dD, ddt_bias, dS0, cu_seqlens, N, T, H, G, Dk, Dv, rows, ws, s);
+    const SsmBwdCall k = {x, dt, A, b, c, D, dt_bias, softplus, S0, dy, dST, dx, ddt, dA, db, dc, dD,
+                          ddt_bias, dS0, cu_seqlens, N, T, H, G, Dk, Dv, rows,
+                          static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream)};
+    if (path == OSDN_F32) return launch_ssm_bwd_f32(k);
+    if (Dk == 128) return Dv == 128 ? launch_ssm_bwd_tc<128, 128>(k) : launch_ssm_bwd_tc<128, 64>(k);
+    return Dv == 128 ? launch_ssm_bwd_tc<64, 128>(k) : launch_ssm_bwd_tc<64, 64>(k);
 }
 
 // ---------------------------------------------------------------- block norm

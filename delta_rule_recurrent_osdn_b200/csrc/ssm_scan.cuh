@@ -305,15 +305,21 @@ ssm_group_kernel(const float* __restrict__ dch, const float* __restrict__ dbh,
 }
 
 // ddt of every token, and per (sequence, head) the sums that dA, dD and ddt_bias are made of.
-// One CTA per (sequence, head), a warp per block of tokens; part: [3][N][H].
+// Within a block of BLOCK tokens (gs its <G, S> term, nslice shares of it; pos, ri and rn have
+// `shares` shares each, rn may be null for 0):
+//   d(log a_t) = sum_{i >= t} (pos_i - step_i ri_i) + sum_{j < t} step_j rn_j + gs
+//   dstep_t = ri_t + rn_t + A d(log a_t)
+// One CTA per (sequence, head), a warp per block; part: [3][N][H].
 constexpr int SSM_GATE_WARPS = 16;
+template <int BLOCK>
 __global__ void __launch_bounds__(32 * SSM_GATE_WARPS)
-ssm_gate_kernel(const float* __restrict__ pos, const float* __restrict__ rneg,
-                const float* __restrict__ gs, int nslice, const float* __restrict__ vk,
-                const float* __restrict__ dt, const float* __restrict__ A,
-                const float* __restrict__ dt_bias, int softplus, float* __restrict__ ddt,
-                double* __restrict__ part, const int32_t* __restrict__ cu, int N, int T, int H,
-                int64_t rows) {
+ssm_gate_kernel(const float* __restrict__ pos, const float* __restrict__ ri,
+                const float* __restrict__ rn, int shares, const float* __restrict__ gs, int nslice,
+                const float* __restrict__ vk, const float* __restrict__ dt,
+                const float* __restrict__ A, const float* __restrict__ dt_bias, int softplus,
+                float* __restrict__ ddt, double* __restrict__ part, const int32_t* __restrict__ cu,
+                int N, int T, int H, int64_t rows) {
+    constexpr int PT = BLOCK / 32;  // neighbouring tokens of a lane
     __shared__ double red[3][SSM_GATE_WARPS];
     const int n = blockIdx.x / H, h = blockIdx.x - n * H;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -321,35 +327,58 @@ ssm_gate_kernel(const float* __restrict__ pos, const float* __restrict__ rneg,
     const bool ok = seq_range(cu, n, N, T, first, count);
     double sA = 0.0, sD = 0.0, sb = 0.0;
     const float Ah = A[h], bias = dt_bias ? dt_bias[h] : 0.f;
-    const int64_t slots = ssm_slots(rows, N, SSM_BLOCK);
-    for (int64_t t0 = (int64_t)warp * SSM_BLOCK; ok && t0 < count;
-         t0 += SSM_BLOCK * SSM_GATE_WARPS) {
-        const int64_t slot = first / SSM_BLOCK + n + t0 / SSM_BLOCK;
-        float tail = 0.f;  // <G, S> behind the block, then plus the sums of the later half
-        for (int s = 0; s < nslice; ++s) tail += gs[(s * slots + slot) * H + h];
+    const int64_t slots = ssm_slots(rows, N, BLOCK), share = (int64_t)H * rows;
+    for (int64_t t0 = (int64_t)warp * BLOCK; ok && t0 < count; t0 += BLOCK * SSM_GATE_WARPS) {
+        const int64_t slot = first / BLOCK + n + t0 / BLOCK;
+        float edge = 0.f;
+        for (int s = 0; s < nslice; ++s) edge += gs[(s * slots + slot) * H + h];
+        float raw[PT], step[PT], r[PT], back[PT], fore[PT];
+        float own_b = 0.f, own_f = 0.f;
 #pragma unroll
-        for (int half = 1; half >= 0; --half) {
-            const int64_t t = t0 + half * 32 + lane;
+        for (int e = 0; e < PT; ++e) {
+            const int64_t t = t0 + lane * PT + e, at = h * rows + first + t;
             const bool live = t < count;
-            const int64_t at = h * rows + first + t;
-            const float raw = live ? dt[(first + t) * H + h] + bias : 0.f;
-            const float step = scan_step(raw, softplus);
-            const float r = live ? rneg[at] : 0.f;
-            float s = live ? pos[at] - step * r : 0.f;  // suffix sum over the half
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const float o = __shfl_down_sync(0xffffffffu, s, off);
-                if (lane + off < 32) s += o;
+            raw[e] = live ? dt[(first + t) * H + h] + bias : 0.f;
+            step[e] = live ? scan_step(raw[e], softplus) : 0.f;
+            float ps = 0.f, a = 0.f, b = 0.f;
+            for (int s = 0; live && s < shares; ++s) {
+                ps += pos[s * share + at];
+                a += ri[s * share + at];
+                if (rn) b += rn[s * share + at];
             }
-            const float dla = s + tail;
-            tail += __shfl_sync(0xffffffffu, s, 0);
-            if (live) {
-                float d = fmaf(Ah, dla, r);
-                if (softplus) d *= 1.f / (1.f + expf(-raw));
+            r[e] = a + b;
+            back[e] = ps - step[e] * a;
+            fore[e] = step[e] * b;
+            own_b += back[e];
+            own_f += fore[e];
+            if (vk && live) sD += (double)vk[at];
+        }
+        float sum_b = own_b, sum_f = own_f;  // over this lane and the later (earlier) ones
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float o = __shfl_down_sync(0xffffffffu, sum_b, off);
+            if (lane + off < 32) sum_b += o;
+            const float u = __shfl_up_sync(0xffffffffu, sum_f, off);
+            if (lane >= off) sum_f += u;
+        }
+        float after = sum_b - own_b, before = sum_f - own_f;
+        float dla[PT];
+#pragma unroll
+        for (int e = PT - 1; e >= 0; --e) {
+            after += back[e];
+            dla[e] = after;
+        }
+#pragma unroll
+        for (int e = 0; e < PT; ++e) {
+            dla[e] = (dla[e] + before) + edge;
+            before += fore[e];
+            const int64_t t = t0 + lane * PT + e;
+            if (t < count) {
+                float d = fmaf(Ah, dla[e], r[e]);
+                if (softplus) d *= 1.f / (1.f + expf(-raw[e]));
                 if (OSDN_IN_BOUNDS(first + t, rows)) ddt[(first + t) * H + h] = d;
-                sA += (double)(step * dla);
+                sA += (double)(step[e] * dla[e]);
                 sb += (double)d;
-                if (vk) sD += (double)vk[at];
             }
         }
     }

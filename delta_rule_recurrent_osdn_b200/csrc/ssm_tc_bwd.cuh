@@ -1,0 +1,562 @@
+// ssm_tc_bwd.cuh -- the selective scan's gradient on the sm_100a tensor cores (bf16 tokens): one
+// CTA per chunk of 128 tokens and head, after the chains of ssm_tc.cuh have stored the state S in
+// front of every chunk and the gradient R that reaches the state behind it.
+//
+// With L_ij = 2^(cum_i - cum_j) for i >= j (0 otherwise), all within the chunk:
+//   dx_j = step_j [ sum_i (b_j.c_i) L_ij dy_i + 2^(cum_L - cum_j) R b_j ] + D dy_j
+//   db_j = step_j [ sum_i (x_j.dy_i) L_ij c_i + 2^(cum_L - cum_j) R^T x_j ]
+//   dc_i = sum_j (dy_i.x_j) L_ij step_j b_j + 2^cum_i S^T dy_i
+// and for the steps, with W_ij = (c_i.b_j)(dy_i.x_j) L_ij in fp32:
+//   pos_i = sum_j W_ij step_j + 2^cum_i c_i.(S^T dy_i),   ri_j = sum_i W_ij,
+//   rn_j = 2^(cum_L - cum_j) b_j.(R^T x_j)
+//   d(log a_t) = sum_{i >= t} (pos_i - step_i ri_i) + sum_{j < t} step_j rn_j + 2^cum_L <R, S>
+//   dstep_t = ri_t + rn_t + A d(log a_t)       (sums over the chunk; see ssm_gate_kernel)
+// The pairs inside the chunk enter both sums with the same fp32 products of exact scores, so what
+// cancels between them does so to fp32; what crosses the chunk's ends is summed without cancelling.
+// Rounding: the weighted scores go into a product as bf16 (errors that reach dx, db, dc only,
+// bf16 themselves); S and R as two bf16 terms, since pos and rn lead to fp32 results.
+//
+// Ten products a chunk: four of scores (both orientations, so that every sum over a chunk's
+// tokens is a thread's own row), three with the states, three with the weighted scores.  Tensor
+// memory holds the two score tiles of an orientation and two accumulators; the state products go
+// in first, are scaled by their rows' decays in place, and the weighted scores accumulate on top.
+//
+// Warps 0-7: element-wise work, thread = row, the two warpgroups taking alternate 16-column
+// sub-blocks of scores and halves of the outputs' columns; warp 8: loads and MMAs; warp 9: gates.
+#pragma once
+
+#include <stddef.h>
+
+#include "ssm_tc.cuh"
+
+namespace osdn {
+
+struct TcgArgs {
+    const float *dt, *A, *dt_bias, *D;
+    const uint8_t *img, *img_r;    // S in front of each chunk, R behind it
+    __nv_bfloat16* dx;
+    __nv_bfloat16 *db, *dc;        // G == H: written; else null
+    float *dbh, *dch;              // G < H: the heads' shares [rows][H][DK]
+    float *pos, *ri, *rn;          // [2][H][rows], a share from each warpgroup
+    float* vk;                     // dy . x [H][rows], or null
+    const int32_t* cu;
+    int64_t rows, slots;
+    int N, T, H, G, softplus;
+};
+
+template <int DK, int DV> struct TcgSmem {
+    static constexpr uint32_t TK = DK / 64 * 16384, TV = DV / 64 * 16384;
+    static constexpr uint32_t X = 0, DY = TV, B = 2 * TV, C = 2 * TV + TK, IMG = 2 * TV + 2 * TK;
+    static constexpr uint32_t IMG_ONE = DK * 128, IMG_BYTES = 2 * (DV / 64) * IMG_ONE;
+    static constexpr uint32_t GATE = IMG + IMG_BYTES;
+    static constexpr uint32_t BAR = GATE + 2304;
+    static constexpr uint32_t TMEM_SLOT = BAR + 20 * 8;
+    static constexpr size_t BYTES = TMEM_SLOT + 16 + 1024;
+    static constexpr int THREADS = 320;
+};
+static_assert(TcgSmem<128, 128>::BYTES <= 232448, "shared memory");
+
+// The chunk's gates: TcsGate's arrays of the forward orientation, and 2^l of the other.
+struct TcgGate {
+    float r[TCS_L];
+    TcsGate f;
+};
+static_assert(sizeof(TcgGate) <= 2304, "gate arrays");
+static_assert(offsetof(TcgGate, f) % 16 == 0 && offsetof(TcsGate, g) % 16 == 0 &&
+                  offsetof(TcsGate, st) % 16 == 0 && TcsSmem<128, TCS_FWD>::GATE_BYTES % 16 == 0,
+              "the arrays are read 16 bytes at a time");
+
+// K steps of a product: n MMAs, start addresses moving by da / db (16-byte units) per step and by
+// ga / gb more after every fourth; `acc`: add to the accumulator from the first step on.
+template <int n>
+__device__ __forceinline__ void tcg_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t da,
+                                        uint32_t db, uint32_t ga, uint32_t gb, bool acc) {
+#pragma unroll
+    for (int e = 0; e < n; ++e)
+        tc::mma_bf16(d, a + e * da + (e >> 2) * ga, b + e * db + (e >> 2) * gb, id, acc || e != 0);
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(TcgSmem<DK, DV>::THREADS, 1)
+ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_dy,
+                   const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_c,
+                   const TcgArgs p) {
+    using L = TcgSmem<DK, DV>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_align1024(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t slot = blockIdx.x / p.H;
+    const int h = (int)(blockIdx.x - slot * p.H), g = h / (p.H / p.G);
+    // the chunk with this number: sequence n's start at first / TCS_L + n
+    int lo = 0, hi = p.N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        const int64_t f = p.cu ? (int64_t)__ldg(p.cu + mid) : (int64_t)mid * p.T;
+        if (f / TCS_L + mid <= slot) lo = mid; else hi = mid - 1;
+    }
+    int64_t first, count;
+    if (!seq_range(p.cu, lo, p.N, p.T, first, count)) return;
+    const int64_t start = (slot - (first / TCS_L + lo)) * TCS_L;
+    if (start < 0 || start >= count) return;  // all uniform over the CTA
+    const int64_t row0 = first + start;
+    const int len = count - start < TCS_L ? (int)(count - start) : TCS_L;
+
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
+    uint64_t* tiles = bars + 0;    // x, dy, b, c landed
+    uint64_t* imgs = bars + 1;     // R, then S landed
+    uint64_t* gates = bars + 2;
+    uint64_t* zeroed = bars + 3;   // dead rows of a short chunk
+    uint64_t* sc1 = bars + 4;      // scores [j][i]
+    uint64_t* in1 = bars + 5;      // R products
+    uint64_t* ew1 = bars + 6;      // weighted scores and scaled R products written
+    uint64_t* acc1 = bars + 7;     // dx, db complete
+    uint64_t* out1 = bars + 8;     // ... read
+    uint64_t* sc2 = bars + 9;      // scores [i][j]
+    uint64_t* in2 = bars + 10;     // S product
+    uint64_t* ew2 = bars + 11;
+    uint64_t* acc2 = bars + 12;    // dc complete
+    uint64_t* drain = bars + 13;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::TMEM_SLOT);
+    TcgGate* gt = reinterpret_cast<TcgGate*>(smem + L::GATE);
+    auto wait = [&](uint64_t* bar, int phase) -> bool {
+        return __all_sync(0xffffffffu, tcs_wait(bar, phase));
+    };
+
+    if (warp == 8) {
+        tc::tmem_alloc(tmem_slot, 512);
+        tc::tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int i = 0; i < 14; ++i) {
+            uint64_t* b = bars + i;
+            mbar_init(b, b == zeroed || b == ew1 || b == out1 || b == ew2 ? 8 : 1);
+        }
+        tc::fence_mbar_init();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t T0 = 0, T1 = 128, A0 = 256, A1 = 384;  // score tiles, accumulators
+
+    if (warp == 8) {
+        // ------------------------------------------------------------ loads and MMAs
+        if (lane == 0) {
+            const uint8_t* im = p.img + (slot * p.H + h) * (int64_t)L::IMG_BYTES;
+            const uint8_t* imr = p.img_r + (slot * p.H + h) * (int64_t)L::IMG_BYTES;
+            tc::mbar_expect_tx(tiles, 2 * L::TV + 2 * L::TK);
+#pragma unroll
+            for (int e = 0; e < DK / 64; ++e) {
+                tc::tma_load_3d(smem + L::B + e * 16384, &tm_b, e * 64, g, (int)row0, tiles);
+                tc::tma_load_3d(smem + L::C + e * 16384, &tm_c, e * 64, g, (int)row0, tiles);
+            }
+#pragma unroll
+            for (int e = 0; e < DV / 64; ++e) {
+                tc::tma_load_3d(smem + L::X + e * 16384, &tm_x, e * 64, h, (int)row0, tiles);
+                tc::tma_load_3d(smem + L::DY + e * 16384, &tm_dy, e * 64, h, (int)row0, tiles);
+            }
+            tc::mbar_expect_tx(imgs, L::IMG_BYTES);
+            tc::bulk_load(smem + L::IMG, imr, L::IMG_BYTES, imgs);
+            constexpr uint32_t ID_S = tc::idesc(1, 0, 0, 128, 128);   // scores
+            constexpr uint32_t ID_KK = tc::idesc(1, 0, 0, 128, DK);   // rows x key channels, K-major
+            constexpr uint32_t ID_MV = tc::idesc(1, 0, 1, 128, DV);   // rows x value channels, MN-major
+            constexpr uint32_t ID_MK = tc::idesc(1, 0, 1, 128, DK);
+            const uint32_t ax = smem_u32(smem + L::X), ady = smem_u32(smem + L::DY),
+                           ab = smem_u32(smem + L::B), ac = smem_u32(smem + L::C),
+                           ai = smem_u32(smem + L::IMG);
+            auto kd = [](uint32_t a) { return tc::sw128_desc(a, 16, 1024); };
+            auto scores = [&](uint32_t t, uint32_t a, uint32_t b, auto steps) {
+                tcg_mma<decltype(steps)::value>(tmem + t, kd(a), kd(b), ID_S, 2, 2, 1024 - 8, 1024 - 8,
+                                                false);
+            };
+            using NK = std::integral_constant<int, DK / 16>;
+            using NV = std::integral_constant<int, DV / 16>;
+            constexpr uint32_t VB = 2 * L::IMG_ONE;  // from one block of 64 value channels to the next
+            // a [tokens][value channels] times the state's [key][value]: hi, then lo terms
+            auto state_k = [&](uint32_t d, uint32_t a) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    tcg_mma<DV / 16>(tmem + d, kd(a), kd(ai + t * L::IMG_ONE), ID_KK, 2, 2, 1024 - 8,
+                                     (VB >> 4) - 8, t != 0);
+            };
+            // weighted scores times a token tile, added
+            auto weighted = [&](uint32_t d, uint32_t s, uint32_t b, uint32_t id) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    tc::mma_bf16_ts(tmem + d, tmem + s + 16 * e, tc::sw128_desc(b + e * 2048, 16384, 1024),
+                                    id, 1);
+            };
+            bool ok = tcs_wait(tiles, 0) && (len == TCS_L || tcs_wait(zeroed, 0));
+            if (ok) {
+                scores(T0, ab, ac, NK{});   // b_j . c_i
+                scores(T1, ax, ady, NV{});  // x_j . dy_i
+                tc::mma_commit(sc1);
+                ok = tcs_wait(imgs, 0);
+            }
+            if (ok) {
+                // R b_j: key channels summed, [key][value] read MN-major
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    tcg_mma<DK / 16>(tmem + A0, kd(ab), tc::sw128_desc(ai + t * L::IMG_ONE, VB, 1024),
+                                     ID_MV, 2, 128, 1024 - 8, 0, t != 0);
+                state_k(A1, ax);            // R^T x_j
+                tc::mma_commit(in1);
+                ok = tcs_wait(in1, 0);      // R is used up: S into its place
+            }
+            bool asked = false;
+            if (ok) {
+                tc::mbar_expect_tx(imgs, L::IMG_BYTES);
+                tc::bulk_load(smem + L::IMG, im, L::IMG_BYTES, imgs);
+                asked = true;
+                ok = tcs_wait(ew1, 0);
+            }
+            if (ok) {
+                tc::fence_after_sync();
+                weighted(A0, T0, ady, ID_MV);
+                weighted(A1, T1, ac, ID_MK);
+                tc::mma_commit(acc1);
+                scores(T0, ac, ab, NK{});   // c_i . b_j
+                scores(T1, ady, ax, NV{});  // dy_i . x_j
+                tc::mma_commit(sc2);
+                ok = tcs_wait(imgs, 1) && tcs_wait(out1, 0);
+            }
+            if (ok) {
+                tc::fence_after_sync();
+                state_k(A0, ady);           // S^T dy_i
+                tc::mma_commit(in2);
+                ok = tcs_wait(ew2, 0);
+            }
+            if (ok) {
+                tc::fence_after_sync();
+                weighted(A0, T1, ab, ID_MK);
+                tc::mma_commit(acc2);
+            }
+            tc::mma_commit(drain);
+            tcs_wait(drain, 0);
+            tcs_wait(tiles, 0);             // nothing in flight when the CTA leaves
+            tcs_wait(imgs, asked ? 1 : 0);
+        }
+    } else if (warp == 9) {
+        tcs_gates<false>(&gt->f, p.dt + row0 * p.H + h, p.H, len, p.A[h], p.dt_bias ? p.dt_bias[h] : 0.f,
+                         p.softplus, lane);
+        __syncwarp();
+#pragma unroll
+        for (int t = lane; t < TCS_L; t += 32) gt->r[t] = ex2f(gt->f.l[t]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(gates);
+    } else {
+        const int wg = warp >> 2, wq = warp & 3;
+        const int r = 32 * wq + lane, rb = r >> 4;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+        const bool live = r < len;
+        const int64_t row = row0 + r;
+        const TcsGate* f = &gt->f;
+        // 16 bytes (8 channels from ch on) of this thread's row of a token tile
+        auto tile16 = [&](uint32_t tile, int ch) {
+            return *reinterpret_cast<const uint4*>(smem + tile + (ch >> 6) * 16384 +
+                                                   tc::sw128_off(r, (ch & 63) >> 3));
+        };
+        auto arrive = [&](uint64_t* bar) {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        bool ok = true;
+        if (len < TCS_L && (ok = wait(tiles, 0))) {  // rows of the next sequence: 0 x NaN must not
+            if (!live && wg == 0) {                  // reach a sum
+                const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+                for (int t = 0; t < (int)(L::IMG / 16384); ++t)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<uint4*>(smem + t * 16384 + tc::sw128_off(r, j)) = z;
+            }
+            tc::fence_async_smem();
+            arrive(zeroed);
+        }
+        ok = ok && wait(gates, 0) && wait(sc1, 0);
+        if (ok) {
+            tc::fence_after_sync();
+            // ---- scores [j][i], i >= j: 2^(cum_i - cum_j) = 2^l_i 2^(base_b - cum_j)
+            float ri = 0.f;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                const int b = 2 * k + wg;
+                uint32_t w1[8], w2[8];
+                if (k < wq) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w1[e] = w2[e] = 0;
+                } else {
+                    float s1[16], s2[16], wt[16];
+                    tc::tmem_ld16(tl + T0 + 16 * b, s1);
+                    tc::tmem_ld16(tl + T1 + 16 * b, s2);
+                    const float d = (f->bh[b] - f->bh[rb]) + (f->bl[b] - f->bl[rb]) - f->l[r];
+                    if (k == wq) {
+                        const float4* lp = reinterpret_cast<const float4*>(f->l + 16 * b);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 l4 = lp[e];
+                            const int c = 16 * b + 4 * e;
+                            wt[4 * e] = c < r ? 0.f : ex2f(d + l4.x);
+                            wt[4 * e + 1] = c + 1 < r ? 0.f : ex2f(d + l4.y);
+                            wt[4 * e + 2] = c + 2 < r ? 0.f : ex2f(d + l4.z);
+                            wt[4 * e + 3] = c + 3 < r ? 0.f : ex2f(d + l4.w);
+                        }
+                    } else {
+                        const float fr = ex2f(d);
+                        const float4* gp = reinterpret_cast<const float4*>(gt->r + 16 * b);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 g4 = gp[e];
+                            wt[4 * e] = fr * g4.x; wt[4 * e + 1] = fr * g4.y;
+                            wt[4 * e + 2] = fr * g4.z; wt[4 * e + 3] = fr * g4.w;
+                        }
+                    }
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 t = make_float2(wt[2 * e], wt[2 * e + 1]);
+                        const float2 u = __fmul2_rn(t, make_float2(s1[2 * e], s1[2 * e + 1]));
+                        const float2 v = __fmul2_rn(t, make_float2(s2[2 * e], s2[2 * e + 1]));
+                        ri = fmaf(u.x, s2[2 * e], ri);
+                        ri = fmaf(u.y, s2[2 * e + 1], ri);
+                        w1[e] = pack2_rn(u.x, u.y);
+                        w2[e] = pack2_rn(v.x, v.y);
+                    }
+                }
+                tc::tmem_st8(tl + T0 + 16 * b, w1);
+                tc::tmem_st8(tl + T1 + 16 * b, w2);
+            }
+            if (live && OSDN_IN_BOUNDS(row, p.rows)) p.ri[(wg * p.H + h) * p.rows + row] = ri;
+        }
+        ok = ok && wait(in1, 0);
+        const float st = f->st[r];
+        if (ok) {
+            tc::fence_after_sync();
+            // ---- R products scaled by 2^(cum_L - cum_j) in place
+            const float e1 = ex2f((f->bh[8] - f->bh[rb]) + (f->bl[8] - f->bl[rb]) - f->l[r]);
+            const float2 e2 = make_float2(e1, e1);
+            float rn = 0.f;
+#pragma unroll 1
+            for (int q = 0; q < DV / 32; ++q) {
+                const int c = wg * (DV / 2) + 16 * q;
+                float v[16];
+                tc::tmem_ld16(tl + A0 + c, v);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] *= e1;
+                tc::tmem_st16(tl + A0 + c, v);
+            }
+#pragma unroll 1
+            for (int q = 0; q < DK / 32; ++q) {
+                const int c = wg * (DK / 2) + 16 * q;
+                float v[16];
+                tc::tmem_ld16(tl + A1 + c, v);
+                const uint4 u0 = tile16(L::B, c), u1 = tile16(L::B, c + 8);
+                const uint32_t bw[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float2 t = __fmul2_rn(e2, make_float2(v[2 * e], v[2 * e + 1]));
+                    rn = fmaf(t.x, __uint_as_float(bw[e] << 16), rn);
+                    rn = fmaf(t.y, __uint_as_float(bw[e] & 0xffff0000u), rn);
+                    v[2 * e] = t.x;
+                    v[2 * e + 1] = t.y;
+                }
+                tc::tmem_st16(tl + A1 + c, v);
+            }
+            tc::tmem_st_wait();
+            if (live && OSDN_IN_BOUNDS(row, p.rows)) p.rn[(wg * p.H + h) * p.rows + row] = rn;
+            arrive(ew1);
+            ok = wait(acc1, 0);
+        }
+        if (ok) {
+            tc::fence_after_sync();
+            // ---- dx and db
+            const float skip = p.D ? p.D[h] : 0.f;
+#pragma unroll 1
+            for (int q = 0; q < DV / 32; ++q) {
+                const int c = wg * (DV / 2) + 16 * q;
+                float v[16];
+                tc::tmem_ld16(tl + A0 + c, v);
+                const uint4 u0 = tile16(L::DY, c), u1 = tile16(L::DY, c + 8);
+                const uint32_t yw[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+                tc::tmem_ld_wait();
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    w[e] = pack2_rn(fmaf(st, v[2 * e], skip * __uint_as_float(yw[e] << 16)),
+                                    fmaf(st, v[2 * e + 1], skip * __uint_as_float(yw[e] & 0xffff0000u)));
+                if (live && OSDN_IN_BOUNDS(row, p.rows)) {
+                    uint4* o = reinterpret_cast<uint4*>(p.dx + (row * p.H + h) * DV + c);
+                    o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+                __syncwarp();
+            }
+        }
+        // a head's row of db or dc, 16 channels
+        auto put = [&](__nv_bfloat16* o16, float* o32, int c, const float* v) {
+            if (!live || !OSDN_IN_BOUNDS(row, p.rows)) return;
+            const int64_t at = (row * p.H + h) * DK + c;
+            if (o16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = pack2_rn(v[2 * e], v[2 * e + 1]);
+                uint4* o = reinterpret_cast<uint4*>(o16 + at);
+                o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<float4*>(o32 + at + 4 * e) =
+                        make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            }
+        };
+        if (ok) {
+#pragma unroll 1
+            for (int q = 0; q < DK / 32; ++q) {
+                const int c = wg * (DK / 2) + 16 * q;
+                float v[16];
+                tc::tmem_ld16(tl + A1 + c, v);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] *= st;
+                put(p.db, p.dbh, c, v);
+                __syncwarp();
+            }
+            arrive(out1);
+            ok = wait(sc2, 0);
+        }
+        float pos = 0.f;
+        if (ok) {
+            tc::fence_after_sync();
+            // ---- scores [i][j], j <= i
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                const int b = 2 * k + wg;
+                uint32_t w2[8];
+                if (k > wq) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w2[e] = 0;
+                } else {
+                    float s1[16], s2[16], wt[16];
+                    tc::tmem_ld16(tl + T0 + 16 * b, s1);
+                    tc::tmem_ld16(tl + T1 + 16 * b, s2);
+                    if (k == wq) {
+                        const float d = (f->bh[rb] - f->bh[b]) + (f->bl[rb] - f->bl[b]) + f->l[r];
+                        const float4* lp = reinterpret_cast<const float4*>(f->l + 16 * b);
+                        const float4* sp = reinterpret_cast<const float4*>(f->st + 16 * b);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 l4 = lp[e], s4 = sp[e];
+                            const int c = 16 * b + 4 * e;
+                            wt[4 * e] = c > r ? 0.f : ex2f(d - l4.x) * s4.x;
+                            wt[4 * e + 1] = c + 1 > r ? 0.f : ex2f(d - l4.y) * s4.y;
+                            wt[4 * e + 2] = c + 2 > r ? 0.f : ex2f(d - l4.z) * s4.z;
+                            wt[4 * e + 3] = c + 3 > r ? 0.f : ex2f(d - l4.w) * s4.w;
+                        }
+                    } else {
+                        const float fr = ex2f((f->bh[rb] - f->bh[b + 1]) + (f->bl[rb] - f->bl[b + 1]) + f->l[r]);
+                        const float4* gp = reinterpret_cast<const float4*>(f->g + 16 * b);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 g4 = gp[e];
+                            wt[4 * e] = fr * g4.x; wt[4 * e + 1] = fr * g4.y;
+                            wt[4 * e + 2] = fr * g4.z; wt[4 * e + 3] = fr * g4.w;
+                        }
+                    }
+                    tc::tmem_ld_wait();
+                    if (b == rb && p.vk && live) {
+                        float v = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v = e == (r & 15) ? s2[e] : v;
+                        p.vk[h * p.rows + row] = v;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 v = __fmul2_rn(make_float2(wt[2 * e], wt[2 * e + 1]),
+                                                    make_float2(s2[2 * e], s2[2 * e + 1]));
+                        pos = fmaf(v.x, s1[2 * e], pos);
+                        pos = fmaf(v.y, s1[2 * e + 1], pos);
+                        w2[e] = pack2_rn(v.x, v.y);
+                    }
+                }
+                tc::tmem_st8(tl + T1 + 16 * b, w2);
+            }
+            ok = wait(in2, 0);
+        }
+        if (ok) {
+            tc::fence_after_sync();
+            // ---- the S product scaled by 2^cum_i in place
+            const float e1 = ex2f(f->bh[rb] + f->l[r] + f->bl[rb]);
+            const float2 e2 = make_float2(e1, e1);
+#pragma unroll 1
+            for (int q = 0; q < DK / 32; ++q) {
+                const int c = wg * (DK / 2) + 16 * q;
+                float v[16];
+                tc::tmem_ld16(tl + A0 + c, v);
+                const uint4 u0 = tile16(L::C, c), u1 = tile16(L::C, c + 8);
+                const uint32_t cw[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float2 t = __fmul2_rn(e2, make_float2(v[2 * e], v[2 * e + 1]));
+                    pos = fmaf(t.x, __uint_as_float(cw[e] << 16), pos);
+                    pos = fmaf(t.y, __uint_as_float(cw[e] & 0xffff0000u), pos);
+                    v[2 * e] = t.x;
+                    v[2 * e + 1] = t.y;
+                }
+                tc::tmem_st16(tl + A0 + c, v);
+            }
+            tc::tmem_st_wait();
+            if (live && OSDN_IN_BOUNDS(row, p.rows)) p.pos[(wg * p.H + h) * p.rows + row] = pos;
+            arrive(ew2);
+            ok = wait(acc2, 0);
+        }
+        if (ok) {
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int q = 0; q < DK / 32; ++q) {
+                const int c = wg * (DK / 2) + 16 * q;
+                float v[16];
+                tc::tmem_ld16(tl + A0 + c, v);
+                tc::tmem_ld_wait();
+                put(p.dc, p.dch, c, v);
+                __syncwarp();
+            }
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 8) tc::tmem_dealloc(tmem, 512);
+}
+
+// db and dc of the groups: the heads' fp32 shares summed in order, rounded once.  8 channels a
+// thread; n = rows * G * DK / 8.
+__global__ void __launch_bounds__(256)
+ssm_group_sum_kernel(const float* __restrict__ dbh, const float* __restrict__ dch,
+                     __nv_bfloat16* __restrict__ db, __nv_bfloat16* __restrict__ dc, int64_t n, int rep,
+                     int DK) {
+    const int64_t stride = (int64_t)gridDim.x * 256;
+    const int v = DK / 8;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += stride) {
+        const int64_t at = (i / v) * rep * DK + (i % v) * 8;
+        float s[8], t[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = t[e] = 0.f;
+        for (int r = 0; r < rep; ++r) {
+            float a[8], b[8];
+            vec_io<8, float>::load(dbh + at + (int64_t)r * DK, a);
+            vec_io<8, float>::load(dch + at + (int64_t)r * DK, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) { s[e] += a[e]; t[e] += b[e]; }
+        }
+        vec_io<8, __nv_bfloat16>::store(db + i * 8, s);
+        vec_io<8, __nv_bfloat16>::store(dc + i * 8, t);
+    }
+}
+
+}  // namespace osdn
