@@ -425,7 +425,8 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         float S[TCS_BV];
         const int64_t sbase = (nh * DV + vt * TCS_BV) * DQ + r;  // stored [value][key]
 #pragma unroll
-        for (int j = 0; j < TCS_BV; ++j) S[j] = on && p.S_in ? p.S_in[sbase + (int64_t)j * DQ] : 0.f;
+        for (int j = 0; j < TCS_BV; ++j)
+            S[j] = MODE != TCS_SEG && on && p.S_in ? p.S_in[sbase + (int64_t)j * DQ] : 0.f;
         if constexpr (OUT) {
             for (int e = slot - seg; on && e < slot; ++e) {  // the segments in front
                 const float d = ex2f(p.seg_decay[(int64_t)e * p.H + h]);

@@ -11,14 +11,16 @@
 //   rn_j = 2^(cum_L - cum_j) b_j.(R^T x_j)
 //   d(log a_t) = sum_{i >= t} (pos_i - step_i ri_i) + sum_{j < t} step_j rn_j + 2^cum_L <R, S>
 //   dstep_t = ri_t + rn_t + A d(log a_t)       (sums over the chunk; see ssm_gate_kernel)
-// The pairs inside the chunk enter both sums with the same fp32 products of exact scores, so what
-// cancels between them does so to fp32; what crosses the chunk's ends is summed without cancelling.
+// The pairs inside the chunk enter both sums as one and the same W_ij, summed over rows by each
+// thread and over columns across them, so what cancels between the sums does so to fp32 (two
+// evaluations of W, each good to 2^-22, left dA wrong by up to 1e-5); what crosses the chunk's
+// ends is summed without cancelling.
 // Rounding: the weighted scores go into a product as bf16 (errors that reach dx, db, dc only,
 // bf16 themselves); S and R as two bf16 terms, since pos and rn lead to fp32 results.
 //
-// Ten products a chunk: four of scores (both orientations, so that every sum over a chunk's
-// tokens is a thread's own row), three with the states, three with the weighted scores.  Tensor
-// memory holds the two score tiles of an orientation and two accumulators; the state products go
+// Nine products a chunk: three of scores (x.dy in both orientations: P X-like products read the
+// weighted scores as rows), three with the states, three with the weighted scores.  Tensor
+// memory holds two score tiles and two accumulators; the state products go
 // in first, are scaled by their rows' decays in place, and the weighted scores accumulate on top.
 //
 // Warps 0-7: element-wise work, thread = row, the two warpgroups taking alternate 16-column
@@ -49,7 +51,8 @@ template <int DK, int DV> struct TcgSmem {
     static constexpr uint32_t X = 0, DY = TV, B = 2 * TV, C = 2 * TV + TK, IMG = 2 * TV + 2 * TK;
     static constexpr uint32_t IMG_ONE = DK * 128, IMG_BYTES = 2 * (DV / 64) * IMG_ONE;
     static constexpr uint32_t GATE = IMG + IMG_BYTES;
-    static constexpr uint32_t BAR = GATE + 2304;
+    static constexpr uint32_t ROWSUM = GATE + 2304;  // [4 row quarters][128] shares of sum_j W_ij step_j
+    static constexpr uint32_t BAR = ROWSUM + 4 * TCS_L * 4;
     static constexpr uint32_t TMEM_SLOT = BAR + 20 * 8;
     static constexpr size_t BYTES = TMEM_SLOT + 16 + 1024;
     static constexpr int THREADS = 320;
@@ -215,7 +218,6 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 weighted(A0, T0, ady, ID_MV);
                 weighted(A1, T1, ac, ID_MK);
                 tc::mma_commit(acc1);
-                scores(T0, ac, ab, NK{});   // c_i . b_j
                 scores(T1, ady, ax, NV{});  // dy_i . x_j
                 tc::mma_commit(sc2);
                 ok = tcs_wait(imgs, 1) && tcs_wait(out1, 0);
@@ -279,6 +281,8 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             tc::fence_after_sync();
             // ---- scores [j][i], i >= j: 2^(cum_i - cum_j) = 2^l_i 2^(base_b - cum_j)
             float ri = 0.f;
+            const float sj = f->st[r];
+            float* rowsum = reinterpret_cast<float*>(smem + L::ROWSUM) + wq * TCS_L;
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
                 const int b = 2 * k + wg;
@@ -286,6 +290,7 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 if (k < wq) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) w1[e] = w2[e] = 0;
+                    if (lane < 16) rowsum[16 * b + lane] = 0.f;
                 } else {
                     float s1[16], s2[16], wt[16];
                     tc::tmem_ld16(tl + T0 + 16 * b, s1);
@@ -318,11 +323,28 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                         const float2 t = make_float2(wt[2 * e], wt[2 * e + 1]);
                         const float2 u = __fmul2_rn(t, make_float2(s1[2 * e], s1[2 * e + 1]));
                         const float2 v = __fmul2_rn(t, make_float2(s2[2 * e], s2[2 * e + 1]));
-                        ri = fmaf(u.x, s2[2 * e], ri);
-                        ri = fmaf(u.y, s2[2 * e + 1], ri);
                         w1[e] = pack2_rn(u.x, u.y);
                         w2[e] = pack2_rn(v.x, v.y);
+                        const float2 x = __fmul2_rn(u, make_float2(s2[2 * e], s2[2 * e + 1]));  // W
+                        ri += x.x;
+                        ri += x.y;
+                        s1[2 * e] = sj * x.x;
+                        s1[2 * e + 1] = sj * x.y;
                     }
+                    // 16 columns summed over the warp's 32 rows: each step halves the columns a
+                    // lane keeps and doubles the rows that they stand for
+#pragma unroll
+                    for (int half = 8; half > 0; half >>= 1) {
+                        const bool up = lane & (2 * half);
+#pragma unroll
+                        for (int e = 0; e < half; ++e) {
+                            const float send = up ? s1[e] : s1[e + half];
+                            const float keep = up ? s1[e + half] : s1[e];
+                            s1[e] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * half);
+                        }
+                    }
+                    const float sum = s1[0] + __shfl_xor_sync(0xffffffffu, s1[0], 1);
+                    if (!(lane & 1)) rowsum[16 * b + (lane >> 1)] = sum;
                 }
                 tc::tmem_st8(tl + T0 + 16 * b, w1);
                 tc::tmem_st8(tl + T1 + 16 * b, w2);
@@ -429,6 +451,10 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             ok = wait(sc2, 0);
         }
         float pos = 0.f;
+        if (ok && wg == 0 && (ok = wait(ew1, 0))) {  // every quarter's shares are written
+            const float* rowsum = reinterpret_cast<const float*>(smem + L::ROWSUM) + r;
+            pos = (rowsum[0] + rowsum[TCS_L]) + (rowsum[2 * TCS_L] + rowsum[3 * TCS_L]);
+        }
         if (ok) {
             tc::fence_after_sync();
             // ---- scores [i][j], j <= i
@@ -440,8 +466,7 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 #pragma unroll
                     for (int e = 0; e < 8; ++e) w2[e] = 0;
                 } else {
-                    float s1[16], s2[16], wt[16];
-                    tc::tmem_ld16(tl + T0 + 16 * b, s1);
+                    float s2[16], wt[16];
                     tc::tmem_ld16(tl + T1 + 16 * b, s2);
                     if (k == wq) {
                         const float d = (f->bh[rb] - f->bh[b]) + (f->bl[rb] - f->bl[b]) + f->l[r];
@@ -478,8 +503,6 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     for (int e = 0; e < 8; ++e) {
                         const float2 v = __fmul2_rn(make_float2(wt[2 * e], wt[2 * e + 1]),
                                                     make_float2(s2[2 * e], s2[2 * e + 1]));
-                        pos = fmaf(v.x, s1[2 * e], pos);
-                        pos = fmaf(v.y, s1[2 * e + 1], pos);
                         w2[e] = pack2_rn(v.x, v.y);
                     }
                 }

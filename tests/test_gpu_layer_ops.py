@@ -342,6 +342,38 @@ def test_scan_keeps_sequences_apart(osdn, io):
     finish(osdn)
 
 
+@pytest.mark.parametrize("io,lens,packed", [("bf16", [1100], False), ("bf16", [700, 900, 1], True),
+                                            ("f32", [150], False)])
+def test_scan_slow_decay(osdn, io, lens, packed):
+    """States that hardly decay: what a sequence starts from, and every segment and chunk, reaches
+    all of what follows."""
+    H, G, Dk, Dv = 2, 1, 64, 64
+    a, rng = scan_inputs(io, lens, H, G, Dk, Dv, True, True, True, True, seed=6)
+    a["A"][:] = rounded([-0.002, -0.05], "f32")
+    a["S0"] *= 8
+    dy = rounded(rng.standard_normal(a["x"].shape), io)
+    dST = rounded(rng.standard_normal(a["S0"].shape), "f32")
+    want = scan_ref(a, True, lens, dy=dy, dST=dST)
+    mag = scan_ref(a, True, lens, dy=dy, dST=dST, absolute=True)
+    t = scan_dev(a, io, lens, packed)
+    y, ST = scan_fwd(osdn, t)
+    g = scan_bwd(osdn, t, dev(dy, io).reshape(t["x"].shape), dev(dST))
+    finish(osdn)
+    coarse, fine = scan_factors(io, lens, Dk)
+    close(y.reshape(want["y"].shape), want["y"], U[io] * np.abs(want["y"]) + coarse * mag["y"], "y")
+    close(ST, want["ST"], fine * mag["ST"], "ST")
+    for name in ("dx", "db", "dc"):
+        close(g[name].reshape(want[name].shape), want[name],
+              U[io] * np.abs(want[name]) + coarse * mag[name], name)
+    close(g["dS0"], want["dS0"], fine * mag["dS0"], "dS0")
+    close(g["ddt"].reshape(-1, H), want["ddt"],
+          (np.abs(a["A"]) * mag["cancel"] + mag["ddt"]) * fine, "ddt")
+    # norms: errors are random, so they stay far below the sums of their bounds
+    for got, ref in ((ST, want["ST"]), (g["dS0"], want["dS0"])):
+        assert np.linalg.norm(host(got) - ref) <= 1e-5 * np.linalg.norm(ref)
+    assert np.linalg.norm(host(y).reshape(-1) - want["y"].reshape(-1)) <= 2.0 ** -8 * np.linalg.norm(want["y"])
+
+
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_scan_extreme_steps(osdn, io):
     """Steps of 0 (masked tokens: dt = -inf), steps so large that the state is forgotten, and
