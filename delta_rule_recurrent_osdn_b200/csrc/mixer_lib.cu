@@ -256,22 +256,22 @@ SsmSegments ssm_segments(bool packed, int64_t rows, int64_t N, int64_t T, int H,
     return s;
 }
 
-// q, k: [rows][G][DQ], v: [rows][H][nvt * 64] (q only in the forward pass).  slots: the segments'
-// numbers, or the sequences'.
+// q, k: [rows][G][DQ], v, v2: [rows][H][nvt * 64] (v2: dy, used by SAVE alone).  slots: the
+// segments' numbers, or the sequences'.
 template <int DQ, int MODE>
-osdn_status_t launch_tc_chain(const void* q, const void* k, const void* v, const TcsArgs& a,
-                              int64_t slots, cudaStream_t stream) {
+osdn_status_t launch_tc_chain(const void* q, const void* k, const void* v, const void* v2,
+                              const TcsArgs& a, int64_t slots, cudaStream_t stream) {
     using L = TcsSmem<DQ, MODE>;
-    const int64_t ctas = slots * a.H * a.nvt;
+    const int64_t ctas = slots * a.H * a.nvt * (MODE == TCS_SAVE ? 2 : 1);
     if (ctas == 0) return OSDN_OK;
     if (ctas > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mv2;
     if (!make_chunk_map(&mk, k, DQ, a.G, a.rows) || !make_chunk_map(&mv, v, a.nvt * TCS_BV, a.H, a.rows) ||
-        !make_chunk_map(&mq, q ? q : k, DQ, a.G, a.rows))
+        !make_chunk_map(&mq, q, DQ, a.G, a.rows) || !make_chunk_map(&mv2, v2, a.nvt * TCS_BV, a.H, a.rows))
         return OSDN_ERR_CUDA;
     auto kern = ssm_tc_chain_kernel<DQ, MODE>;
     if (!set_smem(kern, L::BYTES)) return OSDN_ERR_CUDA;
-    kern<<<dim3((unsigned)ctas), dim3(L::THREADS), L::BYTES, stream>>>(mq, mk, mv, a);
+    kern<<<dim3((unsigned)ctas), dim3(L::THREADS), L::BYTES, stream>>>(mq, mk, mv, mv2, a);
     return launch_status();
 }
 
@@ -279,21 +279,21 @@ template <int DQ>
 osdn_status_t launch_tc_fwd(const void* q, const void* k, const void* v, const TcsArgs& a,
                             int64_t slots, cudaStream_t stream) {
     if (a.seg != INT_MAX) {
-        const osdn_status_t st = launch_tc_chain<DQ, TCS_SEG>(nullptr, k, v, a, slots, stream);
+        const osdn_status_t st = launch_tc_chain<DQ, TCS_SEG>(q, k, v, v, a, slots, stream);
         if (st != OSDN_OK) return st;
     }
-    return launch_tc_chain<DQ, TCS_FWD>(q, k, v, a, slots, stream);
+    return launch_tc_chain<DQ, TCS_FWD>(q, k, v, v, a, slots, stream);
 }
 
 osdn_status_t check_ssm(int32_t H, int32_t G, int32_t Dk, int32_t Dv) {
     if (H < 1 || G < 1 || H % G != 0) return OSDN_ERR_INVALID_ARG;
     if ((Dk != 64 && Dk != 128) || (Dv != 64 && Dv != 128)) return OSDN_ERR_UNSUPPORTED;
-    return OSDN_OK;
+    return H > 65535 ? OSDN_ERR_UNSUPPORTED : OSDN_OK;
 }
 
 // Workspace of osdn_ssm_bwd, each part rounded up to 256 bytes.  fp32 tokens: the heads' dc and
 // db, the state behind each block of SSM_BLOCK tokens.  bf16 tokens: the states in front of and
-// the gradients behind each chunk as bf16 hi / lo images, the heads' dc and db when heads share
+// the gradients behind each chunk as images of bf16 terms, the heads' dc and db when heads share
 // rows of b and c.  Both: the sums that the step gradient is made of.
 struct SsmBwdWorkspace {
     size_t dch, dbh, ckpt, ckpt_r, gs, pos, ri, rn, vk, part, total;
@@ -309,17 +309,18 @@ SsmBwdWorkspace ssm_bwd_workspace(int64_t rows, int64_t N, int32_t H, int32_t G,
     };
     const bool tc = io == OSDN_BF16;
     const size_t th = (size_t)rows * H, slots = (size_t)ssm_slots(rows, N, tc ? TCS_L : SSM_BLOCK);
-    const size_t heads = !tc || G < H ? th * Dk * 4 : 0, shares = tc ? 2 : 1;
+    const size_t heads = !tc || G < H ? th * Dk * 4 : 0, shares = tc ? 4 : 1;
+    const size_t image = slots * H * Dk * Dv * (tc ? TCS_TERMS * 2 : 4);
     w.dch = take(heads);
     w.dbh = take(heads);
-    w.ckpt = take(slots * H * Dk * Dv * 4);
-    w.ckpt_r = take(tc ? slots * H * Dk * Dv * 4 : 0);
-    w.gs = take(slots * H * (tc ? Dv / TCS_BV * (Dk / 32) : Dk / SSM_BV) * 4);
+    w.ckpt = take(image);
+    w.ckpt_r = take(tc ? image : 0);
+    w.gs = take(slots * H * (tc ? 16 : Dk / SSM_BV) * 4);
     w.pos = take(shares * th * 4);
     w.ri = take(shares * th * 4);
     w.rn = take(tc ? shares * th * 4 : 0);
     w.vk = take(th * 4);
-    w.part = take((size_t)3 * N * H * 8);
+    w.part = take((size_t)3 * slots * H * 4);
     w.total = off;
     return w;
 }
@@ -336,15 +337,18 @@ template <int BLOCK>
 osdn_status_t launch_ssm_gates(const SsmBwdCall& k, const SsmBwdWorkspace& w, const float* rn,
                                int shares, int nslice) {
     auto f32 = [&](size_t at) { return reinterpret_cast<float*>(k.ws + at); };
-    double* part = reinterpret_cast<double*>(k.ws + w.part);
+    const int64_t slots = ssm_slots(k.rows, k.N, BLOCK), units = slots * k.H;
+    const int64_t blocks = ceil_div(units, SSM_GATE_WARPS);
+    if (blocks > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
     if (k.N > 0) {
-        ssm_gate_kernel<BLOCK><<<dim3((unsigned)(k.N * k.H)), dim3(32 * SSM_GATE_WARPS), 0, k.stream>>>(
+        ssm_gate_kernel<BLOCK><<<dim3((unsigned)blocks), dim3(32 * SSM_GATE_WARPS), 0, k.stream>>>(
             f32(w.pos), f32(w.ri), rn, shares, f32(w.gs), nslice, k.dD ? f32(w.vk) : nullptr, k.dt, k.A,
-            k.dt_bias, k.softplus, k.ddt, part, k.cu, (int)k.N, k.T, k.H, k.rows);
+            k.dt_bias, k.softplus, k.ddt, f32(w.part), k.cu, (int)k.N, k.T, k.H, k.rows);
         const osdn_status_t st = launch_status();
         if (st != OSDN_OK) return st;
     }
-    ssm_param_kernel<<<3, 256, 0, k.stream>>>(part, (int)k.N, k.H, k.dA, k.dD, k.ddt_bias);
+    ssm_param_kernel<<<dim3(3, k.H), 128, 0, k.stream>>>(f32(w.part), k.N > 0 ? slots : 0, k.H, k.dA,
+                                                         k.dD, k.ddt_bias);
     return launch_status();
 }
 
@@ -380,7 +384,7 @@ osdn_status_t launch_ssm_bwd_f32(const SsmBwdCall& k) {
     return launch_ssm_gates<SSM_BLOCK>(k, w, nullptr, 1, k.Dk / SSM_BV);
 }
 
-// bf16 tokens: the two chains of states, then all chunks at once.
+// bf16 tokens: the chains of states in both directions, then all chunks at once.
 template <int DK, int DV> osdn_status_t launch_ssm_bwd_tc(const SsmBwdCall& k) {
     using bf16 = __nv_bfloat16;
     const SsmBwdWorkspace w = ssm_bwd_workspace(k.rows, k.N, k.H, k.G, DK, DV, OSDN_BF16);
@@ -389,12 +393,9 @@ template <int DK, int DV> osdn_status_t launch_ssm_bwd_tc(const SsmBwdCall& k) {
     a.dt = k.dt; a.A = k.A; a.dt_bias = k.dt_bias; a.softplus = k.softplus; a.cu = k.cu;
     a.rows = k.rows; a.N = (int)k.N; a.T = k.T; a.H = k.H; a.G = k.G; a.nvt = DV / TCS_BV;
     a.seg = INT_MAX;
-    TcsArgs f = a, r = a;
-    f.S_in = k.S0; f.img = k.ws + w.ckpt;
-    r.S_in = k.dST; r.img = k.ws + w.ckpt_r; r.img_fwd = k.ws + w.ckpt; r.gs = f32(w.gs);
-    r.S_out = k.dS0;
-    osdn_status_t st = launch_tc_chain<DK, TCS_SAVE>(nullptr, k.b, k.x, f, k.N, k.stream);
-    if (st == OSDN_OK) st = launch_tc_chain<DK, TCS_RSAVE>(nullptr, k.c, k.dy, r, k.N, k.stream);
+    a.S_in = k.S0; a.img = k.ws + w.ckpt; a.img_r = k.ws + w.ckpt_r;
+    a.dST = k.dST; a.dS0 = k.dS0;
+    osdn_status_t st = launch_tc_chain<DK, TCS_SAVE>(k.c, k.b, k.x, k.dy, a, k.N, k.stream);
     if (st != OSDN_OK) return st;
     TcgArgs g = {};
     g.dt = k.dt; g.A = k.A; g.dt_bias = k.dt_bias; g.D = k.D; g.softplus = k.softplus;
@@ -406,7 +407,7 @@ template <int DK, int DV> osdn_status_t launch_ssm_bwd_tc(const SsmBwdCall& k) {
         g.dbh = f32(w.dbh);
         g.dch = f32(w.dch);
     }
-    g.pos = f32(w.pos); g.ri = f32(w.ri); g.rn = f32(w.rn); g.vk = k.dD ? f32(w.vk) : nullptr;
+    g.pos = f32(w.pos); g.ri = f32(w.ri); g.rn = f32(w.rn); g.gs = f32(w.gs); g.vk = k.dD ? f32(w.vk) : nullptr;
     g.cu = k.cu; g.rows = k.rows; g.N = (int)k.N; g.T = k.T; g.H = k.H; g.G = k.G;
     g.slots = ssm_slots(k.rows, k.N, TCS_L);
     if (g.slots * k.H > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
@@ -427,7 +428,7 @@ template <int DK, int DV> osdn_status_t launch_ssm_bwd_tc(const SsmBwdCall& k) {
         st = launch_status();
         if (st != OSDN_OK) return st;
     }
-    return launch_ssm_gates<TCS_L>(k, w, g.rn, 2, DV / TCS_BV * (DK / 32));
+    return launch_ssm_gates<TCS_L>(k, w, g.rn, 4, 16);
 }
 
 }  // namespace

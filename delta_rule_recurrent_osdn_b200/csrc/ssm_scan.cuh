@@ -309,27 +309,35 @@ ssm_group_kernel(const float* __restrict__ dch, const float* __restrict__ dbh,
 // `shares` shares each, rn may be null for 0):
 //   d(log a_t) = sum_{i >= t} (pos_i - step_i ri_i) + sum_{j < t} step_j rn_j + gs
 //   dstep_t = ri_t + rn_t + A d(log a_t)
-// One CTA per (sequence, head), a warp per block; part: [3][N][H].
-constexpr int SSM_GATE_WARPS = 16;
+// A warp per (block, head); part: the block's sums for dA, dD and ddt_bias, [3][slots][H].
+constexpr int SSM_GATE_WARPS = 8;
 template <int BLOCK>
 __global__ void __launch_bounds__(32 * SSM_GATE_WARPS)
 ssm_gate_kernel(const float* __restrict__ pos, const float* __restrict__ ri,
                 const float* __restrict__ rn, int shares, const float* __restrict__ gs, int nslice,
                 const float* __restrict__ vk, const float* __restrict__ dt,
                 const float* __restrict__ A, const float* __restrict__ dt_bias, int softplus,
-                float* __restrict__ ddt, double* __restrict__ part, const int32_t* __restrict__ cu,
+                float* __restrict__ ddt, float* __restrict__ part, const int32_t* __restrict__ cu,
                 int N, int T, int H, int64_t rows) {
     constexpr int PT = BLOCK / 32;  // neighbouring tokens of a lane
-    __shared__ double red[3][SSM_GATE_WARPS];
-    const int n = blockIdx.x / H, h = blockIdx.x - n * H;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int64_t first, count;
-    const bool ok = seq_range(cu, n, N, T, first, count);
-    double sA = 0.0, sD = 0.0, sb = 0.0;
-    const float Ah = A[h], bias = dt_bias ? dt_bias[h] : 0.f;
     const int64_t slots = ssm_slots(rows, N, BLOCK), share = (int64_t)H * rows;
-    for (int64_t t0 = (int64_t)warp * BLOCK; ok && t0 < count; t0 += BLOCK * SSM_GATE_WARPS) {
-        const int64_t slot = first / BLOCK + n + t0 / BLOCK;
+    const int64_t unit = (int64_t)blockIdx.x * SSM_GATE_WARPS + (threadIdx.x >> 5);
+    if (unit >= slots * H) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t slot = unit / H;
+    const int h = (int)(unit - slot * H);
+    int lo = 0, hi = N - 1;  // the sequence that the block belongs to
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        const int64_t f = cu ? (int64_t)__ldg(cu + mid) : (int64_t)mid * T;
+        if (f / BLOCK + mid <= slot) lo = mid; else hi = mid - 1;
+    }
+    int64_t first = 0, count = 0;
+    float sA = 0.f, sD = 0.f, sb = 0.f;
+    const bool ok = seq_range(cu, lo, N, T, first, count);
+    const int64_t t0 = (slot - (first / BLOCK + lo)) * BLOCK;
+    if (ok && t0 >= 0 && t0 < count) {
+        const float Ah = A[h], bias = dt_bias ? dt_bias[h] : 0.f;
         float edge = 0.f;
         for (int s = 0; s < nslice; ++s) edge += gs[(s * slots + slot) * H + h];
         float raw[PT], step[PT], r[PT], back[PT], fore[PT];
@@ -351,7 +359,7 @@ ssm_gate_kernel(const float* __restrict__ pos, const float* __restrict__ ri,
             fore[e] = step[e] * b;
             own_b += back[e];
             own_f += fore[e];
-            if (vk && live) sD += (double)vk[at];
+            if (vk && live) sD += vk[at];
         }
         float sum_b = own_b, sum_f = own_f;  // over this lane and the later (earlier) ones
 #pragma unroll
@@ -377,37 +385,37 @@ ssm_gate_kernel(const float* __restrict__ pos, const float* __restrict__ ri,
                 float d = fmaf(Ah, dla[e], r[e]);
                 if (softplus) d *= 1.f / (1.f + expf(-raw[e]));
                 if (OSDN_IN_BOUNDS(first + t, rows)) ddt[(first + t) * H + h] = d;
-                sA += (double)(step[e] * dla[e]);
-                sb += (double)d;
+                sA = fmaf(step[e], dla[e], sA);
+                sb += d;
             }
         }
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        sA += __shfl_xor_sync(0xffffffffu, sA, off);
-        sD += __shfl_xor_sync(0xffffffffu, sD, off);
-        sb += __shfl_xor_sync(0xffffffffu, sb, off);
-    }
-    if (lane == 0) { red[0][warp] = sA; red[1][warp] = sD; red[2][warp] = sb; }
-    __syncthreads();
-    if (threadIdx.x < 3) {
-        double s = 0.0;
-        for (int w = 0; w < SSM_GATE_WARPS; ++w) s += red[threadIdx.x][w];
-        part[((int64_t)threadIdx.x * N + n) * H + h] = s;
+    sA = warp_sum_f(sA);
+    sD = warp_sum_f(sD);
+    sb = warp_sum_f(sb);
+    if (lane == 0) {  // a block that is not there adds 0
+        part[slot * H + h] = sA;
+        part[(slots + slot) * H + h] = sD;
+        part[(2 * slots + slot) * H + h] = sb;
     }
 }
 
-// dA, dD, ddt_bias [H]: the sequences' sums in order.  blockIdx.x: which of the three.
-__global__ void __launch_bounds__(256)
-ssm_param_kernel(const double* __restrict__ part, int N, int H, float* __restrict__ dA,
+// dA, dD, ddt_bias [H]: the blocks' sums, in a fixed order and 64 bits.  blockIdx.x: which of the
+// three, blockIdx.y: the head.
+__global__ void __launch_bounds__(128)
+ssm_param_kernel(const float* __restrict__ part, int64_t slots, int H, float* __restrict__ dA,
                  float* __restrict__ dD, float* __restrict__ ddt_bias) {
+    __shared__ double red[4];
     float* out = blockIdx.x == 0 ? dA : blockIdx.x == 1 ? dD : ddt_bias;
-    if (!out) return;
-    for (int h = threadIdx.x; h < H; h += blockDim.x) {
-        double s = 0.0;
-        for (int n = 0; n < N; ++n) s += part[((int64_t)blockIdx.x * N + n) * H + h];
-        out[h] = (float)s;
-    }
+    if (!out) return;  // uniform over the block
+    double s = 0.0;
+    for (int64_t e = threadIdx.x; e < slots; e += 128)
+        s += (double)part[(blockIdx.x * slots + e) * H + blockIdx.y];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) out[blockIdx.y] = (float)((red[0] + red[1]) + (red[2] + red[3]));
 }
 
 }  // namespace osdn

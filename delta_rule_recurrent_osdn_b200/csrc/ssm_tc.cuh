@@ -18,7 +18,8 @@
 // value per token and the first one per row and sub-block, so only the 16 x 16 blocks on the
 // diagonal take an exponential per element.
 //
-// Precision.  b, c and x enter products as stored.  V' goes in as two bf16 terms (2^-17 off), so
+// Precision.  b, c and x enter products as stored.  V' goes in as two bf16 terms (2.4e-6 rms off),
+// three where the state leads to gradients of steps (sums over many tokens that nearly cancel), so
 // states are fp32 results; P and the state in C S^T are rounded once to bf16: their errors reach
 // only y, which is rounded to bf16 itself.
 //
@@ -42,21 +43,23 @@ constexpr int TCS_L = 128;   // tokens per chunk
 constexpr int TCS_BV = 64;   // value channels per CTA
 constexpr int TCS_GATES = 8; // chunks whose gates are kept: they are made well ahead of their use
 
-// What a launch of the chain does: the forward pass; the states in front of every chunk (stored
-// as bf16 hi / lo images); the same for the gradient's chain, backwards in time; what each
+// What a launch of the chain does: the forward pass; for the backward pass the states S in front
+// of every chunk and, backwards in time over c and dy, the gradients R that reach the states
+// behind them, both stored as images of TCS_TERMS bf16 terms (half the CTAs each); what each
 // segment of a sequence adds to a zero state.
-enum { TCS_FWD = 0, TCS_SAVE = 1, TCS_RSAVE = 2, TCS_SEG = 3 };
+enum { TCS_FWD = 0, TCS_SAVE = 1, TCS_SEG = 2 };
+constexpr int TCS_TERMS = 3;
 
 struct TcsArgs {
     const float *dt, *A, *dt_bias;
     const float* D;                // FWD
     const __nv_bfloat16* x;        // FWD: x again, for D x
-    const float* S_in;             // S0 (RSAVE: dST), or null
+    const float* S_in;             // S0, or null
     __nv_bfloat16* y;              // FWD
-    float* S_out;                  // ST (RSAVE: dS0), or null
-    uint8_t* img;                  // SAVE, RSAVE: images written
-    const uint8_t* img_fwd;        // RSAVE: SAVE's images
-    float* gs;                     // RSAVE: <G, S> shares [DV / 64 * DQ / 32][slot][H]
+    float* S_out;                  // ST, or null
+    uint8_t *img, *img_r;          // SAVE: images of S and R [chunk][H][term][nvt][DQ][64]
+    const float* dST;              // SAVE: dST, or null
+    float* dS0;                    // SAVE: dS0, or null
     const int32_t* cu;
     int64_t rows;
     float* seg_state;              // SEG writes, FWD reads: [slot][H][nvt][64][DQ]
@@ -69,25 +72,26 @@ template <int DQ, int MODE> struct TcsSmem {
     static constexpr bool OUT = MODE == TCS_FWD;
     static constexpr uint32_t KB = DQ / 64 * 16384, QB = OUT ? KB : 0;
     static constexpr uint32_t Q = 0, K = QB, V = QB + KB, STAGE = V + 16384;
-    static constexpr int NVP = OUT ? 1 : 2;           // V' buffers, hi then lo
+    static constexpr int NT = OUT ? 2 : TCS_TERMS;    // bf16 terms of V'
     static constexpr uint32_t VP = 2 * STAGE;
-    static constexpr uint32_t S = VP + NVP * 32768;   // the state as an operand (or image)
-    static constexpr uint32_t GATE = S + (OUT ? 16384 : 32768);
+    static constexpr uint32_t S = VP + NT * 16384;    // the state as an operand (or image)
+    static constexpr uint32_t GATE = S + (OUT ? 16384 : TCS_TERMS * 16384);
     static constexpr uint32_t GATE_BYTES = 1664;
     static constexpr uint32_t BAR = GATE + TCS_GATES * GATE_BYTES;
     static constexpr uint32_t TMEM_SLOT = BAR + (27 + 2 * TCS_GATES) * 8 + 8;
     static constexpr size_t BYTES = TMEM_SLOT + 16 + 1024;  // + alignment slack
     static constexpr int THREADS = OUT ? 768 : 384;
-    // tensor memory: G / P (two buffers), B^T V' (hi and lo side by side), C S^T, P X
+    // tensor memory: G / P (two buffers), B^T V' (its terms side by side), C S^T, P X
     static constexpr uint32_t COL_G = 0, COL_U = OUT ? 256 : 0, COL_Y1 = 384, COL_Y2 = 448;
-    static constexpr uint32_t COLS = OUT ? 512 : 128;
+    static constexpr uint32_t COLS = OUT ? 512 : 256;
 };
-static_assert(TcsSmem<128, TCS_FWD>::BYTES <= 232448, "shared memory");
+static_assert(TcsSmem<128, TCS_FWD>::BYTES <= 232448 && TcsSmem<128, TCS_SAVE>::BYTES <= 232448,
+              "shared memory");
 
 // One chunk's gates in shared memory.
 struct TcsGate {
     float l[TCS_L];    // sum of log2 decays from the token's sub-block's start, itself included
-    float g[TCS_L];    // FWD, SAVE: 2^(end - l) step;  RSAVE: 2^l
+    float g[TCS_L];    // 2^(end - l) step;  backwards in time: 2^l
     float st[TCS_L];   // step
     float bh[9], bl[9];  // sums in front of each sub-block and behind the last, two terms each
 };
@@ -106,6 +110,12 @@ __device__ __forceinline__ void split2_rn(float a, float b, uint32_t& hi, uint32
     const __nv_bfloat162 l = __floats2bfloat162_rn(a - __uint_as_float(hi << 16),
                                                    b - __uint_as_float(hi & 0xffff0000u));
     lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+// The same in three terms: all 24 bits.
+__device__ __forceinline__ void split3_rn(float a, float b, uint32_t& t0, uint32_t& t1, uint32_t& t2) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    t0 = *reinterpret_cast<const uint32_t*>(&h);
+    split2_rn(a - __uint_as_float(t0 << 16), b - __uint_as_float(t0 & 0xffff0000u), t1, t2);
 }
 __device__ __forceinline__ uint32_t pack2_rn(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -132,8 +142,7 @@ __device__ __forceinline__ bool tcs_wait(uint64_t* bar, int phase) {
 }
 
 // A chunk's gates, by one warp: softplus and the log decays of its tokens, then their sums.
-template <bool REV>
-__device__ __forceinline__ void tcs_gates(TcsGate* g, const float* __restrict__ dt, int64_t stride,
+__device__ __forceinline__ void tcs_gates(bool rev, TcsGate* g, const float* __restrict__ dt, int64_t stride,
                                           int len, float A, float bias, int softplus, int lane) {
 #pragma unroll
     for (int t = lane; t < TCS_L; t += 32)  // loads in flight together; each lane its own slots
@@ -178,7 +187,7 @@ __device__ __forceinline__ void tcs_gates(TcsGate* g, const float* __restrict__ 
     l4.x += pre; l4.y += pre; l4.z += pre; l4.w += pre;
     *reinterpret_cast<float4*>(g->l + 4 * lane) = l4;
     *reinterpret_cast<float4*>(g->g + 4 * lane) =
-        REV ? make_float4(ex2f(l4.x), ex2f(l4.y), ex2f(l4.z), ex2f(l4.w))
+        rev ? make_float4(ex2f(l4.x), ex2f(l4.y), ex2f(l4.z), ex2f(l4.w))
             : make_float4(ex2f(tot - l4.x) * s4.x, ex2f(tot - l4.y) * s4.y, ex2f(tot - l4.z) * s4.z,
                           ex2f(tot - l4.w) * s4.w);
 }
@@ -215,14 +224,20 @@ __device__ __forceinline__ bool tcs_segment(const TcsArgs& p, int slot, int& n, 
 template <int DQ, int MODE>
 __global__ void __launch_bounds__(TcsSmem<DQ, MODE>::THREADS, 1)
 ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                    const __grid_constant__ CUtensorMap tm_v, const TcsArgs p) {
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v2,
+                    const TcsArgs p) {
     using L = TcsSmem<DQ, MODE>;
-    constexpr bool OUT = L::OUT, REV = MODE == TCS_RSAVE;
+    constexpr bool OUT = L::OUT;
+    // SAVE: the second half of the grid goes backwards over q and v2 (c and dy)
+    const bool rev = MODE == TCS_SAVE && blockIdx.x >= gridDim.x / 2;
+    const uint32_t block = rev ? blockIdx.x - gridDim.x / 2 : blockIdx.x;
+    const CUtensorMap* map_k = rev ? &tm_q : &tm_k;
+    const CUtensorMap* map_v = rev ? &tm_v2 : &tm_v;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align1024(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int vt = blockIdx.x % p.nvt;
-    const int slot = (int)(blockIdx.x / p.nvt / p.H), h = (int)(blockIdx.x / p.nvt - (int64_t)slot * p.H);
+    const int vt = block % p.nvt;
+    const int slot = (int)(block / p.nvt / p.H), h = (int)(block / p.nvt - (int64_t)slot * p.H);
     const int g = h / (p.H / p.G);
     int n, seg;
     int64_t first, count;
@@ -248,8 +263,8 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     uint64_t* v_empty = bars + 10;
     uint64_t* g_full = bars + 12;    // [2] G = C B^T
     uint64_t* p_full = bars + 14;    // [2] P written
-    uint64_t* vp_full = bars + 16;   // [2] V' written (and dead rows zeroed)
-    uint64_t* vp_free = bars + 18;   // [2] V' used up (MMA commit)
+    uint64_t* vp_full = bars + 16;   // V' written (and dead rows zeroed)
+    uint64_t* vp_free = bars + 18;   // V' used up (MMA commit)
     uint64_t* u_full = bars + 20;    // B^T V'
     uint64_t* u_free = bars + 21;    // ... read
     uint64_t* s_full = bars + 22;    // FWD: the state written as an operand
@@ -262,7 +277,7 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::TMEM_SLOT);
     auto gate = [&](int i) { return reinterpret_cast<TcsGate*>(smem + L::GATE + i % TCS_GATES * L::GATE_BYTES); };
     auto stage = [&](int i) { return smem + (i & 1) * L::STAGE; };
-    auto chunk_of = [&](int i) { return REV ? nch - 1 - i : i; };
+    auto chunk_of = [&](int i) { return rev ? nch - 1 - i : i; };
     auto row_of = [&](int i) { return first + (int64_t)chunk_of(i) * TCS_L; };
     auto len_of = [&](int i) -> int {
         const int64_t rem = count - (int64_t)chunk_of(i) * TCS_L;
@@ -325,7 +340,7 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 tc::mbar_expect_tx(&k_full[b], L::KB);
 #pragma unroll
                 for (int e = 0; e < DQ / 64; ++e)
-                    tc::tma_load_3d(s + L::K + e * 16384, &tm_k, e * 64, g, row, &k_full[b]);
+                    tc::tma_load_3d(s + L::K + e * 16384, map_k, e * 64, g, row, &k_full[b]);
                 nk = i + 1;
                 if constexpr (OUT) {
                     if (i >= 2 && !tcs_wait(&q_empty[b], use & 1)) break;
@@ -337,7 +352,7 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 }
                 if (i >= 2 && !tcs_wait(&v_empty[b], use & 1)) break;
                 tc::mbar_expect_tx(&v_full[b], 16384);
-                tc::tma_load_3d(s + L::V, &tm_v, vt * TCS_BV, h, row, &v_full[b]);
+                tc::tma_load_3d(s + L::V, map_v, vt * TCS_BV, h, row, &v_full[b]);
                 nv = i + 1;
             }
             // whatever was asked for has landed before the CTA may leave
@@ -356,7 +371,7 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         if (lane == 0) {
             constexpr uint32_t ID_G = tc::idesc(1, 0, 0, 128, 128);  // tokens x tokens
             constexpr uint32_t ID_Y = tc::idesc(1, 0, 1, 128, 64);   // tokens x value channels
-            constexpr uint32_t ID_U = tc::idesc(1, 1, 1, 128, 128);  // key x value channels, hi | lo
+            constexpr uint32_t ID_U = tc::idesc(1, 1, 1, 128, 64 * L::NT);  // key x value channels, terms
             auto issue_g = [&](int i) -> bool {
                 if (!tcs_wait(&q_full[i & 1], (i >> 1) & 1) ||
                     !tcs_wait(&k_full[i & 1], (i >> 1) & 1))
@@ -374,15 +389,15 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                                v = smem_u32(stage(i) + L::V);
                 // X has landed before V' is made from it, B before G
                 if (!OUT && !(ok = tcs_wait(&k_full[s], ph))) break;
-                if (!(ok = tcs_wait(&vp_full[i % L::NVP], (i / L::NVP) & 1))) break;
+                if (!(ok = tcs_wait(vp_full, i & 1))) break;
                 if (i > 0 && !(ok = tcs_wait(u_free, (i - 1) & 1))) break;
                 tc::fence_after_sync();
-                const uint32_t vp = smem_u32(smem + L::VP + (i % L::NVP) * 32768);
+                const uint32_t vp = smem_u32(smem + L::VP);
                 // (DQ = 64: rows 64..127 read the next tile and are not used)
                 tcs_mma<8>(tmem + L::COL_U, tc::sw128_desc(k, 16384, 1024),
                            tc::sw128_desc(vp, 16384, 1024), ID_U, 128, 128, 0, 0);
                 tc::mma_commit(u_full);
-                tc::mma_commit(&vp_free[i % L::NVP]);
+                tc::mma_commit(vp_free);
                 tc::mma_commit(&k_empty[s]);
                 if constexpr (OUT) {
                     if (!(ok = tcs_wait(s_full, i & 1))) break;
@@ -412,7 +427,7 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
         for (int i = warp - 2; i < nch; i += 2) {
             if (i >= TCS_GATES && !wait(&gate_free[i % TCS_GATES], i / TCS_GATES - 1)) break;
-            tcs_gates<REV>(gate(i), p.dt + row_of(i) * p.H + h, p.H, len_of(i), A, bias, p.softplus, lane);
+            tcs_gates(rev, gate(i), p.dt + row_of(i) * p.H + h, p.H, len_of(i), A, bias, p.softplus, lane);
             __syncwarp();
             if (lane == 0) mbar_arrive(&gate_full[i % TCS_GATES]);
         }
@@ -424,9 +439,10 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         const bool on = DQ == 128 || r < DQ;
         float S[TCS_BV];
         const int64_t sbase = (nh * DV + vt * TCS_BV) * DQ + r;  // stored [value][key]
+        const float* s_in = rev ? p.dST : MODE == TCS_SEG ? nullptr : p.S_in;
 #pragma unroll
         for (int j = 0; j < TCS_BV; ++j)
-            S[j] = MODE != TCS_SEG && on && p.S_in ? p.S_in[sbase + (int64_t)j * DQ] : 0.f;
+            S[j] = on && s_in ? s_in[sbase + (int64_t)j * DQ] : 0.f;
         if constexpr (OUT) {
             for (int e = slot - seg; on && e < slot; ++e) {  // the segments in front
                 const float d = ex2f(p.seg_decay[(int64_t)e * p.H + h]);
@@ -462,54 +478,31 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             } else if constexpr (MODE == TCS_SEG) {
                 total += gate(i)->bh[8];
             } else {
-                // images: rows of 128 bytes, hi then lo, as the products read them
+                // images: rows of 128 bytes as the products read them, the terms one after another
                 const int64_t cs = first / TCS_L + n + chunk_of(i);
-                const int64_t at = ((cs * p.H + h) * p.nvt + vt) * (2 * DQ * 128);
-                if constexpr (REV) {  // <G, S> against the forward chain's state
-                    float dot = 0.f;
-                    if (on) {
-                        const uint8_t* f = p.img_fwd + at;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint4 a = *reinterpret_cast<const uint4*>(f + tc::sw128_off(r, j));
-                            const uint4 b = *reinterpret_cast<const uint4*>(f + DQ * 128 + tc::sw128_off(r, j));
-                            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float x0 = __uint_as_float(aw[e] << 16) + __uint_as_float(bw[e] << 16);
-                                const float x1 = __uint_as_float(aw[e] & 0xffff0000u) +
-                                                 __uint_as_float(bw[e] & 0xffff0000u);
-                                dot = fmaf(S[8 * j + 2 * e], x0, fmaf(S[8 * j + 2 * e + 1], x1, dot));
-                            }
-                        }
-                    }
-                    dot = warp_sum_f(dot) * decay;
-                    if (on && lane == 0) {
-                        const int64_t slots = ssm_slots(p.rows, p.N, TCS_L);
-                        if (OSDN_IN_BOUNDS(cs, slots))
-                            p.gs[((int64_t)(vt * (DQ / 32) + (warp & 3)) * slots + cs) * p.H + h] = dot;
-                    }
-                }
                 if (on) {
                     if (lane == 0) tc::bulk_wait_read_all();
                     __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        uint32_t w[4], x[4];
+                        uint32_t t0[4], t1[4], t2[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            split2_rn(S[8 * j + 2 * e], S[8 * j + 2 * e + 1], w[e], x[e]);
-                        *reinterpret_cast<uint4*>(so + tc::sw128_off(r, j)) =
-                            make_uint4(w[0], w[1], w[2], w[3]);
-                        *reinterpret_cast<uint4*>(so + 16384 + tc::sw128_off(r, j)) =
-                            make_uint4(x[0], x[1], x[2], x[3]);
+                            split3_rn(S[8 * j + 2 * e], S[8 * j + 2 * e + 1], t0[e], t1[e], t2[e]);
+                        uint4* o = reinterpret_cast<uint4*>(so + tc::sw128_off(r, j));
+                        o[0] = make_uint4(t0[0], t0[1], t0[2], t0[3]);
+                        o[1024] = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+                        o[2048] = make_uint4(t2[0], t2[1], t2[2], t2[3]);
                     }
                     tc::fence_async_smem();
                     __syncwarp();
                     if (lane == 0 && OSDN_IN_BOUNDS(cs, ssm_slots(p.rows, p.N, TCS_L))) {
                         const uint32_t w0 = (warp & 3) * 4096;
-                        tc::bulk_store(p.img + at + w0, so + w0, 4096);
-                        tc::bulk_store(p.img + at + DQ * 128 + w0, so + 16384 + w0, 4096);
+                        uint8_t* im = (rev ? p.img_r : p.img) + w0 +
+                                      ((cs * p.H + h) * (TCS_TERMS * p.nvt) + vt) * (DQ * 128);
+#pragma unroll
+                        for (int t = 0; t < TCS_TERMS; ++t)
+                            tc::bulk_store(im + t * p.nvt * (DQ * 128), so + t * 16384 + w0, 4096);
                         tc::bulk_commit();
                     }
                 }
@@ -518,15 +511,19 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             tc::fence_after_sync();
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                float u[16], v[16];
-                tc::tmem_ld16(tmem + tlane + L::COL_U + 16 * q, u);
-                tc::tmem_ld16(tmem + tlane + L::COL_U + 64 + 16 * q, v);
+                float u[L::NT][16];
+#pragma unroll
+                for (int t = 0; t < L::NT; ++t)
+                    tc::tmem_ld16(tmem + tlane + L::COL_U + 64 * t + 16 * q, u[t]);
                 tc::tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
+                    float2 a = make_float2(u[0][e], u[0][e + 1]);
+                    float2 b = make_float2(u[1][e], u[1][e + 1]);
+                    if constexpr (L::NT == 3) b = __fadd2_rn(b, make_float2(u[2][e], u[2][e + 1]));
                     const float2 t = __ffma2_rn(make_float2(decay, decay),
                                                 make_float2(S[16 * q + e], S[16 * q + e + 1]),
-                                                __fadd2_rn(make_float2(u[e], u[e + 1]), make_float2(v[e], v[e + 1])));
+                                                __fadd2_rn(a, b));
                     S[16 * q + e] = t.x;
                     S[16 * q + e + 1] = t.y;
                 }
@@ -543,9 +540,12 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     p.seg_state[(at * p.nvt + vt) * (TCS_BV * DQ) + j * DQ + r] = S[j];
                 if (r == 0 && vt == 0) p.seg_decay[at] = total;
             }
-        } else if (on && p.S_out && last && OSDN_IN_BOUNDS(nh, (int64_t)p.N * p.H)) {
+        } else {
+            float* s_out = rev ? p.dS0 : p.S_out;
+            if (on && s_out && last && OSDN_IN_BOUNDS(nh, (int64_t)p.N * p.H)) {
 #pragma unroll
-            for (int j = 0; j < TCS_BV; ++j) p.S_out[sbase + (int64_t)j * DQ] = S[j];
+                for (int j = 0; j < TCS_BV; ++j) s_out[sbase + (int64_t)j * DQ] = S[j];
+            }
         }
         if (!OUT && lane == 0) tc::bulk_wait_all();
     } else if (warp < 12) {
@@ -555,13 +555,13 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         for (int i = 0; i < nch; ++i) {
             if (!wait(&gate_full[i % TCS_GATES], i / TCS_GATES) || !wait(&v_full[i & 1], i >> 1)) break;
             const TcsGate* gt = gate(i);
-            // FWD, SAVE: 2^(cum_L - end_b) 2^(end_b - cum_r) step;  RSAVE: 2^(base_b + l_r)
-            const float e = REV ? gt->bh[b] + gt->bl[b]
+            // 2^(cum_L - end_b) 2^(end_b - cum_r) step;  backwards: 2^(base_b + l_r)
+            const float e = rev ? gt->bh[b] + gt->bl[b]
                                 : (gt->bh[8] - gt->bh[b + 1]) + (gt->bl[8] - gt->bl[b + 1]);
             const float w = ex2f(e) * gt->g[r];
             const float2 w2 = make_float2(w, w);
             uint8_t* v = stage(i) + L::V;
-            uint8_t* vp = smem + L::VP + (i % L::NVP) * 32768;
+            uint8_t* vp = smem + L::VP;
             const bool live = r < len_of(i);
             if (len_of(i) < TCS_L && !wait(&k_full[i & 1], i >> 1)) break;
             if (!live) {  // the next sequence's row: 0 x NaN must not reach a sum
@@ -578,26 +578,28 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             uint4 x[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = *reinterpret_cast<const uint4*>(v + tc::sw128_off(r, j));
-            if (i >= L::NVP && !wait(&vp_free[i % L::NVP], i / L::NVP - 1)) break;
+            if (i > 0 && !wait(vp_free, i - 1)) break;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t xw[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-                uint32_t hw[4], lw[4];
+                uint32_t t0[4], t1[4], t2[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float2 t = __fmul2_rn(w2, make_float2(__uint_as_float(xw[k] << 16),
                                                                 __uint_as_float(xw[k] & 0xffff0000u)));
-                    split2_rn(t.x, t.y, hw[k], lw[k]);
-                    if (!live) hw[k] = lw[k] = 0;
+                    if constexpr (L::NT == 3) split3_rn(t.x, t.y, t0[k], t1[k], t2[k]);
+                    else split2_rn(t.x, t.y, t0[k], t1[k]);
+                    if (!live) t0[k] = t1[k] = t2[k] = 0;
                 }
-                const uint32_t off = tc::sw128_off(r, j);
-                *reinterpret_cast<uint4*>(vp + off) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-                *reinterpret_cast<uint4*>(vp + 16384 + off) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+                uint4* o = reinterpret_cast<uint4*>(vp + tc::sw128_off(r, j));
+                o[0] = make_uint4(t0[0], t0[1], t0[2], t0[3]);
+                o[1024] = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+                if constexpr (L::NT == 3) o[2048] = make_uint4(t2[0], t2[1], t2[2], t2[3]);
             }
             tc::fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&vp_full[i % L::NVP]);
+                mbar_arrive(vp_full);
                 if (!OUT) mbar_arrive(&gate_free[i % TCS_GATES]);
             }
         }

@@ -16,15 +16,17 @@
 // evaluations of W, each good to 2^-22, left dA wrong by up to 1e-5); what crosses the chunk's
 // ends is summed without cancelling.
 // Rounding: the weighted scores go into a product as bf16 (errors that reach dx, db, dc only,
-// bf16 themselves); S and R as two bf16 terms, since pos and rn lead to fp32 results.
+// bf16 themselves); S and R as three bf16 terms where pos and rn are made from them (with two, dA
+// was up to 1e-5 off), as one in R b_j.
 //
 // Nine products a chunk: three of scores (x.dy in both orientations: P X-like products read the
 // weighted scores as rows), three with the states, three with the weighted scores.  Tensor
 // memory holds two score tiles and two accumulators; the state products go
 // in first, are scaled by their rows' decays in place, and the weighted scores accumulate on top.
 //
-// Warps 0-7: element-wise work, thread = row, the two warpgroups taking alternate 16-column
-// sub-blocks of scores and halves of the outputs' columns; warp 8: loads and MMAs; warp 9: gates.
+// Warps 0-15: element-wise work, thread = row, the four warpgroups taking every fourth 16-column
+// sub-block of scores and a quarter of the outputs' columns; warp 16: loads and MMAs; 17: gates.
+// The images' terms pass through two slots of shared memory, each loaded again once used up.
 #pragma once
 
 #include <stddef.h>
@@ -39,7 +41,8 @@ struct TcgArgs {
     __nv_bfloat16* dx;
     __nv_bfloat16 *db, *dc;        // G == H: written; else null
     float *dbh, *dch;              // G < H: the heads' shares [rows][H][DK]
-    float *pos, *ri, *rn;          // [2][H][rows], a share from each warpgroup
+    float *pos, *ri, *rn;          // [4][H][rows], a share from each warpgroup
+    float* gs;                     // 2^cum_L <R, S> [16][slots][H], a share from each warp
     float* vk;                     // dy . x [H][rows], or null
     const int32_t* cu;
     int64_t rows, slots;
@@ -49,13 +52,13 @@ struct TcgArgs {
 template <int DK, int DV> struct TcgSmem {
     static constexpr uint32_t TK = DK / 64 * 16384, TV = DV / 64 * 16384;
     static constexpr uint32_t X = 0, DY = TV, B = 2 * TV, C = 2 * TV + TK, IMG = 2 * TV + 2 * TK;
-    static constexpr uint32_t IMG_ONE = DK * 128, IMG_BYTES = 2 * (DV / 64) * IMG_ONE;
-    static constexpr uint32_t GATE = IMG + IMG_BYTES;
+    static constexpr uint32_t IMG_ONE = DK * 128, TERM = DV / 64 * IMG_ONE;
+    static constexpr uint32_t GATE = IMG + 2 * TERM;
     static constexpr uint32_t ROWSUM = GATE + 2304;  // [4 row quarters][128] shares of sum_j W_ij step_j
     static constexpr uint32_t BAR = ROWSUM + 4 * TCS_L * 4;
     static constexpr uint32_t TMEM_SLOT = BAR + 20 * 8;
     static constexpr size_t BYTES = TMEM_SLOT + 16 + 1024;
-    static constexpr int THREADS = 320;
+    static constexpr int THREADS = 576;
 };
 static_assert(TcgSmem<128, 128>::BYTES <= 232448, "shared memory");
 
@@ -106,7 +109,10 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
     uint64_t* tiles = bars + 0;    // x, dy, b, c landed
-    uint64_t* imgs = bars + 1;     // R, then S landed
+    uint64_t* img0 = bars + 1;     // slots 0 and 1: a term landed
+    uint64_t* img1 = bars + 14;
+    uint64_t* use0 = bars + 15;    // ... used up (MMA commit)
+    uint64_t* use1 = bars + 16;
     uint64_t* gates = bars + 2;
     uint64_t* zeroed = bars + 3;   // dead rows of a short chunk
     uint64_t* sc1 = bars + 4;      // scores [j][i]
@@ -125,14 +131,14 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         return __all_sync(0xffffffffu, tcs_wait(bar, phase));
     };
 
-    if (warp == 8) {
+    if (warp == 16) {
         tc::tmem_alloc(tmem_slot, 512);
         tc::tmem_relinquish();
     }
     if (tid == 0) {
-        for (int i = 0; i < 14; ++i) {
+        for (int i = 0; i < 17; ++i) {
             uint64_t* b = bars + i;
-            mbar_init(b, b == zeroed || b == ew1 || b == out1 || b == ew2 ? 8 : 1);
+            mbar_init(b, b == zeroed || b == ew1 || b == out1 || b == ew2 ? 16 : 1);
         }
         tc::fence_mbar_init();
     }
@@ -142,11 +148,16 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     const uint32_t tmem = *tmem_slot;
     constexpr uint32_t T0 = 0, T1 = 128, A0 = 256, A1 = 384;  // score tiles, accumulators
 
-    if (warp == 8) {
+    if (warp == 16) {
         // ------------------------------------------------------------ loads and MMAs
         if (lane == 0) {
-            const uint8_t* im = p.img + (slot * p.H + h) * (int64_t)L::IMG_BYTES;
-            const uint8_t* imr = p.img_r + (slot * p.H + h) * (int64_t)L::IMG_BYTES;
+            const int64_t at = (slot * p.H + h) * (int64_t)(TCS_TERMS * L::TERM);
+            const uint8_t *im = p.img + at, *imr = p.img_r + at;
+            auto load_term = [&](int s, const uint8_t* src) {
+                uint64_t* bar = s ? img1 : img0;
+                tc::mbar_expect_tx(bar, L::TERM);
+                tc::bulk_load(smem + L::IMG + s * L::TERM, src, L::TERM, bar);
+            };
             tc::mbar_expect_tx(tiles, 2 * L::TV + 2 * L::TK);
 #pragma unroll
             for (int e = 0; e < DK / 64; ++e) {
@@ -158,8 +169,9 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 tc::tma_load_3d(smem + L::X + e * 16384, &tm_x, e * 64, h, (int)row0, tiles);
                 tc::tma_load_3d(smem + L::DY + e * 16384, &tm_dy, e * 64, h, (int)row0, tiles);
             }
-            tc::mbar_expect_tx(imgs, L::IMG_BYTES);
-            tc::bulk_load(smem + L::IMG, imr, L::IMG_BYTES, imgs);
+            load_term(0, imr);
+            load_term(1, imr + L::TERM);
+            int n0 = 1, n1 = 1;  // terms asked for
             constexpr uint32_t ID_S = tc::idesc(1, 0, 0, 128, 128);   // scores
             constexpr uint32_t ID_KK = tc::idesc(1, 0, 0, 128, DK);   // rows x key channels, K-major
             constexpr uint32_t ID_MV = tc::idesc(1, 0, 1, 128, DV);   // rows x value channels, MN-major
@@ -174,13 +186,10 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             };
             using NK = std::integral_constant<int, DK / 16>;
             using NV = std::integral_constant<int, DV / 16>;
-            constexpr uint32_t VB = 2 * L::IMG_ONE;  // from one block of 64 value channels to the next
-            // a [tokens][value channels] times the state's [key][value]: hi, then lo terms
-            auto state_k = [&](uint32_t d, uint32_t a) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    tcg_mma<DV / 16>(tmem + d, kd(a), kd(ai + t * L::IMG_ONE), ID_KK, 2, 2, 1024 - 8,
-                                     (VB >> 4) - 8, t != 0);
+            // a [tokens][value channels] times the state's [key][value] in slot s
+            auto state_k = [&](uint32_t d, uint32_t a, int s, bool acc) {
+                tcg_mma<DV / 16>(tmem + d, kd(a), kd(ai + s * L::TERM), ID_KK, 2, 2, 1024 - 8,
+                                 (L::IMG_ONE >> 4) - 8, acc);
             };
             // weighted scores times a token tile, added
             auto weighted = [&](uint32_t d, uint32_t s, uint32_t b, uint32_t id) {
@@ -194,23 +203,39 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 scores(T0, ab, ac, NK{});   // b_j . c_i
                 scores(T1, ax, ady, NV{});  // x_j . dy_i
                 tc::mma_commit(sc1);
-                ok = tcs_wait(imgs, 0);
+                ok = tcs_wait(img0, 0);
             }
             if (ok) {
                 // R b_j: key channels summed, [key][value] read MN-major
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    tcg_mma<DK / 16>(tmem + A0, kd(ab), tc::sw128_desc(ai + t * L::IMG_ONE, VB, 1024),
-                                     ID_MV, 2, 128, 1024 - 8, 0, t != 0);
-                state_k(A1, ax);            // R^T x_j
-                tc::mma_commit(in1);
-                ok = tcs_wait(in1, 0);      // R is used up: S into its place
+                tcg_mma<DK / 16>(tmem + A0, kd(ab), tc::sw128_desc(ai, L::IMG_ONE, 1024), ID_MV, 2, 128,
+                                 1024 - 8, 0, false);
+                state_k(A1, ax, 0, false);  // R^T x_j
+                tc::mma_commit(use0);
+                ok = tcs_wait(img1, 0);
             }
-            bool asked = false;
             if (ok) {
-                tc::mbar_expect_tx(imgs, L::IMG_BYTES);
-                tc::bulk_load(smem + L::IMG, im, L::IMG_BYTES, imgs);
-                asked = true;
+                state_k(A1, ax, 1, true);
+                tc::mma_commit(use1);
+                ok = tcs_wait(use0, 0);
+            }
+            if (ok) {
+                load_term(0, imr + 2 * L::TERM);
+                n0 = 2;
+                ok = tcs_wait(use1, 0);
+            }
+            if (ok) {
+                load_term(1, im);
+                n1 = 2;
+                ok = tcs_wait(img0, 1);
+            }
+            if (ok) {
+                state_k(A1, ax, 0, true);
+                tc::mma_commit(in1);
+                ok = tcs_wait(in1, 0);
+            }
+            if (ok) {
+                load_term(0, im + L::TERM);
+                n0 = 3;
                 ok = tcs_wait(ew1, 0);
             }
             if (ok) {
@@ -220,11 +245,25 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 tc::mma_commit(acc1);
                 scores(T1, ady, ax, NV{});  // dy_i . x_j
                 tc::mma_commit(sc2);
-                ok = tcs_wait(imgs, 1) && tcs_wait(out1, 0);
+                ok = tcs_wait(img1, 1) && tcs_wait(out1, 0);
             }
             if (ok) {
                 tc::fence_after_sync();
-                state_k(A0, ady);           // S^T dy_i
+                state_k(A0, ady, 1, false);  // S^T dy_i
+                tc::mma_commit(use1);
+                ok = tcs_wait(use1, 1);
+            }
+            if (ok) {
+                load_term(1, im + 2 * L::TERM);
+                n1 = 3;
+                ok = tcs_wait(img0, 2);
+            }
+            if (ok) {
+                state_k(A0, ady, 0, true);
+                ok = tcs_wait(img1, 2);
+            }
+            if (ok) {
+                state_k(A0, ady, 1, true);
                 tc::mma_commit(in2);
                 ok = tcs_wait(ew2, 0);
             }
@@ -236,10 +275,11 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             tc::mma_commit(drain);
             tcs_wait(drain, 0);
             tcs_wait(tiles, 0);             // nothing in flight when the CTA leaves
-            tcs_wait(imgs, asked ? 1 : 0);
+            tcs_wait(img0, n0 - 1);
+            tcs_wait(img1, n1 - 1);
         }
-    } else if (warp == 9) {
-        tcs_gates<false>(&gt->f, p.dt + row0 * p.H + h, p.H, len, p.A[h], p.dt_bias ? p.dt_bias[h] : 0.f,
+    } else if (warp == 17) {
+        tcs_gates(false, &gt->f, p.dt + row0 * p.H + h, p.H, len, p.A[h], p.dt_bias ? p.dt_bias[h] : 0.f,
                          p.softplus, lane);
         __syncwarp();
 #pragma unroll
@@ -263,6 +303,29 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
+        // ---- 2^cum_L <R, S> from the two leading terms (both also on their way to shared memory)
+        float dot = 0.f;
+        {
+            const int64_t at = (slot * p.H + h) * (int64_t)(TCS_TERMS * L::TERM);
+            const uint4* a = reinterpret_cast<const uint4*>(p.img_r + at);
+            const uint4* b = reinterpret_cast<const uint4*>(p.img + at);
+            constexpr int NB = L::TERM / 16;
+#pragma unroll 2
+            for (int e = tid; e < NB; e += 512) {
+                const uint4 a0 = __ldg(a + e), a1 = __ldg(a + NB + e), b0 = __ldg(b + e), b1 = __ldg(b + NB + e);
+                const uint32_t x0[4] = {a0.x, a0.y, a0.z, a0.w}, x1[4] = {a1.x, a1.y, a1.z, a1.w};
+                const uint32_t y0[4] = {b0.x, b0.y, b0.z, b0.w}, y1[4] = {b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    dot = fmaf(__uint_as_float(x0[k] << 16) + __uint_as_float(x1[k] << 16),
+                               __uint_as_float(y0[k] << 16) + __uint_as_float(y1[k] << 16), dot);
+                    dot = fmaf(__uint_as_float(x0[k] & 0xffff0000u) + __uint_as_float(x1[k] & 0xffff0000u),
+                               __uint_as_float(y0[k] & 0xffff0000u) + __uint_as_float(y1[k] & 0xffff0000u),
+                               dot);
+                }
+            }
+            dot = warp_sum_f(dot);
+        }
         bool ok = true;
         if (len < TCS_L && (ok = wait(tiles, 0))) {  // rows of the next sequence: 0 x NaN must not
             if (!live && wg == 0) {                  // reach a sum
@@ -279,15 +342,16 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         ok = ok && wait(gates, 0) && wait(sc1, 0);
         if (ok) {
             tc::fence_after_sync();
+            if (lane == 0 && OSDN_IN_BOUNDS(slot, p.slots))
+                p.gs[(warp * p.slots + slot) * p.H + h] = dot * ex2f(f->bh[8] + f->bl[8]);
             // ---- scores [j][i], i >= j: 2^(cum_i - cum_j) = 2^l_i 2^(base_b - cum_j)
             float ri = 0.f;
             const float sj = f->st[r];
             float* rowsum = reinterpret_cast<float*>(smem + L::ROWSUM) + wq * TCS_L;
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-                const int b = 2 * k + wg;
+            for (int b = wg; b < 8; b += 4) {
                 uint32_t w1[8], w2[8];
-                if (k < wq) {
+                if (b < 2 * wq) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) w1[e] = w2[e] = 0;
                     if (lane < 16) rowsum[16 * b + lane] = 0.f;
@@ -296,7 +360,7 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     tc::tmem_ld16(tl + T0 + 16 * b, s1);
                     tc::tmem_ld16(tl + T1 + 16 * b, s2);
                     const float d = (f->bh[b] - f->bh[rb]) + (f->bl[b] - f->bl[rb]) - f->l[r];
-                    if (k == wq) {
+                    if (b <= 2 * wq + 1) {
                         const float4* lp = reinterpret_cast<const float4*>(f->l + 16 * b);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -360,8 +424,8 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             const float2 e2 = make_float2(e1, e1);
             float rn = 0.f;
 #pragma unroll 1
-            for (int q = 0; q < DV / 32; ++q) {
-                const int c = wg * (DV / 2) + 16 * q;
+            for (int q = 0; q < DV / 64; ++q) {
+                const int c = wg * (DV / 4) + 16 * q;
                 float v[16];
                 tc::tmem_ld16(tl + A0 + c, v);
                 tc::tmem_ld_wait();
@@ -370,8 +434,8 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 tc::tmem_st16(tl + A0 + c, v);
             }
 #pragma unroll 1
-            for (int q = 0; q < DK / 32; ++q) {
-                const int c = wg * (DK / 2) + 16 * q;
+            for (int q = 0; q < DK / 64; ++q) {
+                const int c = wg * (DK / 4) + 16 * q;
                 float v[16];
                 tc::tmem_ld16(tl + A1 + c, v);
                 const uint4 u0 = tile16(L::B, c), u1 = tile16(L::B, c + 8);
@@ -397,8 +461,8 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             // ---- dx and db
             const float skip = p.D ? p.D[h] : 0.f;
 #pragma unroll 1
-            for (int q = 0; q < DV / 32; ++q) {
-                const int c = wg * (DV / 2) + 16 * q;
+            for (int q = 0; q < DV / 64; ++q) {
+                const int c = wg * (DV / 4) + 16 * q;
                 float v[16];
                 tc::tmem_ld16(tl + A0 + c, v);
                 const uint4 u0 = tile16(L::DY, c), u1 = tile16(L::DY, c + 8);
@@ -437,8 +501,8 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         };
         if (ok) {
 #pragma unroll 1
-            for (int q = 0; q < DK / 32; ++q) {
-                const int c = wg * (DK / 2) + 16 * q;
+            for (int q = 0; q < DK / 64; ++q) {
+                const int c = wg * (DK / 4) + 16 * q;
                 float v[16];
                 tc::tmem_ld16(tl + A1 + c, v);
                 tc::tmem_ld_wait();
@@ -459,16 +523,15 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             tc::fence_after_sync();
             // ---- scores [i][j], j <= i
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-                const int b = 2 * k + wg;
+            for (int b = wg; b < 8; b += 4) {
                 uint32_t w2[8];
-                if (k > wq) {
+                if (b > 2 * wq + 1) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) w2[e] = 0;
                 } else {
                     float s2[16], wt[16];
                     tc::tmem_ld16(tl + T1 + 16 * b, s2);
-                    if (k == wq) {
+                    if (b >= 2 * wq) {
                         const float d = (f->bh[rb] - f->bh[b]) + (f->bl[rb] - f->bl[b]) + f->l[r];
                         const float4* lp = reinterpret_cast<const float4*>(f->l + 16 * b);
                         const float4* sp = reinterpret_cast<const float4*>(f->st + 16 * b);
@@ -516,8 +579,8 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             const float e1 = ex2f(f->bh[rb] + f->l[r] + f->bl[rb]);
             const float2 e2 = make_float2(e1, e1);
 #pragma unroll 1
-            for (int q = 0; q < DK / 32; ++q) {
-                const int c = wg * (DK / 2) + 16 * q;
+            for (int q = 0; q < DK / 64; ++q) {
+                const int c = wg * (DK / 4) + 16 * q;
                 float v[16];
                 tc::tmem_ld16(tl + A0 + c, v);
                 const uint4 u0 = tile16(L::C, c), u1 = tile16(L::C, c + 8);
@@ -541,8 +604,8 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         if (ok) {
             tc::fence_after_sync();
 #pragma unroll 1
-            for (int q = 0; q < DK / 32; ++q) {
-                const int c = wg * (DK / 2) + 16 * q;
+            for (int q = 0; q < DK / 64; ++q) {
+                const int c = wg * (DK / 4) + 16 * q;
                 float v[16];
                 tc::tmem_ld16(tl + A0 + c, v);
                 tc::tmem_ld_wait();
@@ -554,7 +617,7 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 8) tc::tmem_dealloc(tmem, 512);
+    if (warp == 16) tc::tmem_dealloc(tmem, 512);
 }
 
 // db and dc of the groups: the heads' fp32 shares summed in order, rounded once.  8 channels a
