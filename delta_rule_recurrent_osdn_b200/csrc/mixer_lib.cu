@@ -296,7 +296,7 @@ osdn_status_t check_ssm(int32_t H, int32_t G, int32_t Dk, int32_t Dv) {
 // the gradients behind each chunk as images of bf16 terms, the heads' dc and db when heads share
 // rows of b and c.  Both: the sums that the step gradient is made of.
 struct SsmBwdWorkspace {
-    size_t dch, dbh, ckpt, ckpt_r, gs, pos, ri, rn, vk, part, total;
+    size_t dch, dbh, ckpt, ckpt_r, gs, pos, ri, rn, wd, vk, part, total;
 };
 SsmBwdWorkspace ssm_bwd_workspace(int64_t rows, int64_t N, int32_t H, int32_t G, int32_t Dk,
                                   int32_t Dv, osdn_dtype_t io) {
@@ -319,6 +319,7 @@ SsmBwdWorkspace ssm_bwd_workspace(int64_t rows, int64_t N, int32_t H, int32_t G,
     w.pos = take(shares * th * 4);
     w.ri = take(shares * th * 4);
     w.rn = take(tc ? shares * th * 4 : 0);
+    w.wd = take(tc ? th * 4 : 0);
     w.vk = take(th * 4);
     w.part = take((size_t)3 * slots * H * 4);
     w.total = off;
@@ -335,14 +336,14 @@ struct SsmBwdCall {
 // ddt of every token, then dA, dD and ddt_bias.
 template <int BLOCK>
 osdn_status_t launch_ssm_gates(const SsmBwdCall& k, const SsmBwdWorkspace& w, const float* rn,
-                               int shares, int nslice) {
+                               const float* wd, int shares, int nslice) {
     auto f32 = [&](size_t at) { return reinterpret_cast<float*>(k.ws + at); };
     const int64_t slots = ssm_slots(k.rows, k.N, BLOCK), units = slots * k.H;
     const int64_t blocks = ceil_div(units, SSM_GATE_WARPS);
     if (blocks > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
     if (k.N > 0) {
         ssm_gate_kernel<BLOCK><<<dim3((unsigned)blocks), dim3(32 * SSM_GATE_WARPS), 0, k.stream>>>(
-            f32(w.pos), f32(w.ri), rn, shares, f32(w.gs), nslice, k.dD ? f32(w.vk) : nullptr, k.dt, k.A,
+            f32(w.pos), f32(w.ri), rn, shares, wd, f32(w.gs), nslice, k.dD ? f32(w.vk) : nullptr, k.dt, k.A,
             k.dt_bias, k.softplus, k.ddt, f32(w.part), k.cu, (int)k.N, k.T, k.H, k.rows);
         const osdn_status_t st = launch_status();
         if (st != OSDN_OK) return st;
@@ -381,7 +382,7 @@ osdn_status_t launch_ssm_bwd_f32(const SsmBwdCall& k) {
         st = launch_status();
         if (st != OSDN_OK) return st;
     }
-    return launch_ssm_gates<SSM_BLOCK>(k, w, nullptr, 1, k.Dk / SSM_BV);
+    return launch_ssm_gates<SSM_BLOCK>(k, w, nullptr, nullptr, 1, k.Dk / SSM_BV);
 }
 
 // bf16 tokens: the chains of states in both directions, then all chunks at once.
@@ -407,7 +408,7 @@ template <int DK, int DV> osdn_status_t launch_ssm_bwd_tc(const SsmBwdCall& k) {
         g.dbh = f32(w.dbh);
         g.dch = f32(w.dch);
     }
-    g.pos = f32(w.pos); g.ri = f32(w.ri); g.rn = f32(w.rn); g.gs = f32(w.gs); g.vk = k.dD ? f32(w.vk) : nullptr;
+    g.pos = f32(w.pos); g.ri = f32(w.ri); g.rn = f32(w.rn); g.gs = f32(w.gs); g.wd = f32(w.wd); g.vk = k.dD ? f32(w.vk) : nullptr;
     g.cu = k.cu; g.rows = k.rows; g.N = (int)k.N; g.T = k.T; g.H = k.H; g.G = k.G;
     g.slots = ssm_slots(k.rows, k.N, TCS_L);
     if (g.slots * k.H > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
@@ -428,7 +429,7 @@ template <int DK, int DV> osdn_status_t launch_ssm_bwd_tc(const SsmBwdCall& k) {
         st = launch_status();
         if (st != OSDN_OK) return st;
     }
-    return launch_ssm_gates<TCS_L>(k, w, g.rn, 4, 16);
+    return launch_ssm_gates<TCS_L>(k, w, g.rn, g.wd, 4, 16);
 }
 
 }  // namespace

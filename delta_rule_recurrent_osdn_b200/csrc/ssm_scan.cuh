@@ -306,18 +306,19 @@ ssm_group_kernel(const float* __restrict__ dch, const float* __restrict__ dbh,
 
 // ddt of every token, and per (sequence, head) the sums that dA, dD and ddt_bias are made of.
 // Within a block of BLOCK tokens (gs its <G, S> term, nslice shares of it; pos, ri and rn have
-// `shares` shares each, rn may be null for 0):
+// `shares` shares each; rn and wd may be null for 0):
 //   d(log a_t) = sum_{i >= t} (pos_i - step_i ri_i) + sum_{j < t} step_j rn_j + gs
-//   dstep_t = ri_t + rn_t + A d(log a_t)
-// A warp per (block, head); part: the block's sums for dA, dD and ddt_bias, [3][slots][H].
+//   dstep_t = ri_t + wd_t + rn_t + A d(log a_t)
+// The sums that nearly cancel run in 64 bits.  A warp per (block, head); part: the block's sums for dA, dD and ddt_bias, [3][slots][H].
 constexpr int SSM_GATE_WARPS = 8;
 template <int BLOCK>
 __global__ void __launch_bounds__(32 * SSM_GATE_WARPS)
 ssm_gate_kernel(const float* __restrict__ pos, const float* __restrict__ ri,
-                const float* __restrict__ rn, int shares, const float* __restrict__ gs, int nslice,
-                const float* __restrict__ vk, const float* __restrict__ dt,
-                const float* __restrict__ A, const float* __restrict__ dt_bias, int softplus,
-                float* __restrict__ ddt, float* __restrict__ part, const int32_t* __restrict__ cu,
+                const float* __restrict__ rn, int shares, const float* __restrict__ wd,
+                const float* __restrict__ gs, int nslice, const float* __restrict__ vk,
+                const float* __restrict__ dt, const float* __restrict__ A,
+                const float* __restrict__ dt_bias, int softplus, float* __restrict__ ddt,
+                float* __restrict__ part, const int32_t* __restrict__ cu,
                 int N, int T, int H, int64_t rows) {
     constexpr int PT = BLOCK / 32;  // neighbouring tokens of a lane
     const int64_t slots = ssm_slots(rows, N, BLOCK), share = (int64_t)H * rows;
@@ -340,8 +341,8 @@ ssm_gate_kernel(const float* __restrict__ pos, const float* __restrict__ ri,
         const float Ah = A[h], bias = dt_bias ? dt_bias[h] : 0.f;
         float edge = 0.f;
         for (int s = 0; s < nslice; ++s) edge += gs[(s * slots + slot) * H + h];
-        float raw[PT], step[PT], r[PT], back[PT], fore[PT];
-        float own_b = 0.f, own_f = 0.f;
+        float raw[PT], step[PT], r[PT];
+        double back[PT], fore[PT], own_b = 0.0, own_f = 0.0;
 #pragma unroll
         for (int e = 0; e < PT; ++e) {
             const int64_t t = t0 + lane * PT + e, at = h * rows + first + t;
@@ -354,23 +355,23 @@ ssm_gate_kernel(const float* __restrict__ pos, const float* __restrict__ ri,
                 a += ri[s * share + at];
                 if (rn) b += rn[s * share + at];
             }
-            r[e] = a + b;
-            back[e] = ps - step[e] * a;
-            fore[e] = step[e] * b;
+            r[e] = a + b + (wd && live ? wd[at] : 0.f);
+            back[e] = (double)ps - (double)step[e] * (double)a;
+            fore[e] = (double)step[e] * (double)b;
             own_b += back[e];
             own_f += fore[e];
             if (vk && live) sD += vk[at];
         }
-        float sum_b = own_b, sum_f = own_f;  // over this lane and the later (earlier) ones
+        double sum_b = own_b, sum_f = own_f;  // over this lane and the later (earlier) ones
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const float o = __shfl_down_sync(0xffffffffu, sum_b, off);
+            const double o = __shfl_down_sync(0xffffffffu, sum_b, off);
             if (lane + off < 32) sum_b += o;
-            const float u = __shfl_up_sync(0xffffffffu, sum_f, off);
+            const double u = __shfl_up_sync(0xffffffffu, sum_f, off);
             if (lane >= off) sum_f += u;
         }
-        float after = sum_b - own_b, before = sum_f - own_f;
-        float dla[PT];
+        double after = sum_b - own_b, before = sum_f - own_f;
+        double dla[PT];
 #pragma unroll
         for (int e = PT - 1; e >= 0; --e) {
             after += back[e];
@@ -382,10 +383,10 @@ ssm_gate_kernel(const float* __restrict__ pos, const float* __restrict__ ri,
             before += fore[e];
             const int64_t t = t0 + lane * PT + e;
             if (t < count) {
-                float d = fmaf(Ah, dla[e], r[e]);
+                float d = fmaf(Ah, (float)dla[e], r[e]);
                 if (softplus) d *= 1.f / (1.f + expf(-raw[e]));
                 if (OSDN_IN_BOUNDS(first + t, rows)) ddt[(first + t) * H + h] = d;
-                sA = fmaf(step[e], dla[e], sA);
+                sA = fmaf(step[e], (float)dla[e], sA);
                 sb += d;
             }
         }

@@ -7,10 +7,10 @@
 //   db_j = step_j [ sum_i (x_j.dy_i) L_ij c_i + 2^(cum_L - cum_j) R^T x_j ]
 //   dc_i = sum_j (dy_i.x_j) L_ij step_j b_j + 2^cum_i S^T dy_i
 // and for the steps, with W_ij = (c_i.b_j)(dy_i.x_j) L_ij in fp32:
-//   pos_i = sum_j W_ij step_j + 2^cum_i c_i.(S^T dy_i),   ri_j = sum_i W_ij,
+//   pos_i = sum_{j < i} W_ij step_j + 2^cum_i c_i.(S^T dy_i),   ri_j = sum_{i > j} W_ij,
 //   rn_j = 2^(cum_L - cum_j) b_j.(R^T x_j)
 //   d(log a_t) = sum_{i >= t} (pos_i - step_i ri_i) + sum_{j < t} step_j rn_j + 2^cum_L <R, S>
-//   dstep_t = ri_t + rn_t + A d(log a_t)       (sums over the chunk; see ssm_gate_kernel)
+//   dstep_t = ri_t + W_tt + rn_t + A d(log a_t)   (sums over the chunk; see ssm_gate_kernel)
 // The pairs inside the chunk enter both sums as one and the same W_ij, summed over rows by each
 // thread and over columns across them, so what cancels between the sums does so to fp32 (two
 // evaluations of W, each good to 2^-22, left dA wrong by up to 1e-5); what crosses the chunk's
@@ -44,6 +44,7 @@ struct TcgArgs {
     float *pos, *ri, *rn;          // [4][H][rows], a share from each warpgroup
     float* gs;                     // 2^cum_L <R, S> [16][slots][H], a share from each warp
     float* vk;                     // dy . x [H][rows], or null
+    float* wd;                     // W_tt [H][rows]
     const int32_t* cu;
     int64_t rows, slots;
     int N, T, H, G, softplus;
@@ -382,6 +383,8 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                         }
                     }
                     tc::tmem_ld_wait();
+                    const int own = b == rb ? r & 15 : -1;  // the diagonal's column
+                    float diag = 0.f;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float2 t = make_float2(wt[2 * e], wt[2 * e + 1]);
@@ -389,12 +392,16 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                         const float2 v = __fmul2_rn(t, make_float2(s2[2 * e], s2[2 * e + 1]));
                         w1[e] = pack2_rn(u.x, u.y);
                         w2[e] = pack2_rn(v.x, v.y);
-                        const float2 x = __fmul2_rn(u, make_float2(s2[2 * e], s2[2 * e + 1]));  // W
+                        float2 x = __fmul2_rn(u, make_float2(s2[2 * e], s2[2 * e + 1]));  // W
+                        if (own == 2 * e) { diag = x.x; x.x = 0.f; }
+                        if (own == 2 * e + 1) { diag = x.y; x.y = 0.f; }
                         ri += x.x;
                         ri += x.y;
                         s1[2 * e] = sj * x.x;
                         s1[2 * e + 1] = sj * x.y;
                     }
+                    if (own >= 0 && live && OSDN_IN_BOUNDS(row, p.rows)) p.wd[h * p.rows + row] = diag;
+                    __syncwarp();
                     // 16 columns summed over the warp's 32 rows: each step halves the columns a
                     // lane keeps and doubles the rows that they stand for
 #pragma unroll
