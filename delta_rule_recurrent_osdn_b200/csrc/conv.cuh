@@ -15,7 +15,9 @@
 namespace osdn {
 
 constexpr int CONV_THREADS = 128;
-constexpr int CONV_UNROLL = 8;  // tokens loaded before the first is used
+template <typename IO> constexpr int CONV_MAX_V = 4;  // channels of a thread
+constexpr int CONV_BWD_MAX_V = 2;
+constexpr int CONV_UNROLL = 4;  // tokens of a group; the next group's loads are in flight meanwhile
 
 // One row of a sequence at position pos (< 0: a row of the initial state) as fp32.
 template <int V, int W, typename IO>
@@ -35,19 +37,36 @@ template <int V, int W>
 __device__ __forceinline__ void conv_weights(const float* __restrict__ weight,
                                              const float* __restrict__ bias, int c, float (*wt)[V],
                                              float* bs) {
+    if constexpr (V > 1 && V * W % 4 == 0) {  // V * W neighbouring floats, 16-byte aligned
+        float flat[V * W];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+        for (int i = 0; i < V * W; i += 4) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(weight + (int64_t)c * W + i));
+            flat[i] = f.x; flat[i + 1] = f.y; flat[i + 2] = f.z; flat[i + 3] = f.w;
+        }
 #pragma unroll
-        for (int w = 0; w < W; ++w) wt[w][v] = __ldg(weight + (int64_t)(c + v) * W + w);
-        bs[v] = bias ? __ldg(bias + c + v) : 0.f;
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int w = 0; w < W; ++w) wt[w][v] = flat[v * W + w];
+        if (bias) {
+            vec_io<V, float>::load(bias + c, bs);
+            return;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int w = 0; w < W; ++w) wt[w][v] = __ldg(weight + (int64_t)(c + v) * W + w);
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v) bs[v] = bias ? __ldg(bias + c + v) : 0.f;
 }
 
 // blockIdx.x: channels; blockIdx.y < strips: a strip of `strip` rows; the blocks behind them
 // write one sequence's final state each (the last W - 1 rows of [state0; x], oldest first) and
 // check its offsets.
 template <int V, int W, typename IO>
-__global__ void __launch_bounds__(CONV_THREADS)
+__global__ void __launch_bounds__(CONV_THREADS, V * sizeof(IO) == 16 ? 5 : 8)
 conv_fwd_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
                 const float* __restrict__ bias, const IO* __restrict__ state0, int silu,
                 IO* __restrict__ y, IO* __restrict__ stateT, const int32_t* __restrict__ cu, int N,
@@ -81,11 +100,15 @@ conv_fwd_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
             conv_row<V, W>(x, state0, n, a, row - a - (W - 1) + j, C, c, win[j]);
+        raw_io<V, IO> in[CONV_UNROLL], next[CONV_UNROLL];
+#pragma unroll
+        for (int u = 0; u < CONV_UNROLL; ++u)
+            if (row + u < stop) in[u].load(x + (row + u) * C + c);
+#pragma unroll 1
         for (; row < stop; row += CONV_UNROLL) {
-            float in[CONV_UNROLL][V];
 #pragma unroll
             for (int u = 0; u < CONV_UNROLL; ++u)
-                if (row + u < stop) vec_io<V, IO>::load(x + (row + u) * C + c, in[u]);
+                if (row + CONV_UNROLL + u < stop) next[u].load(x + (row + CONV_UNROLL + u) * C + c);
 #pragma unroll
             for (int u = 0; u < CONV_UNROLL; ++u) {
                 if (row + u < stop) {
@@ -95,7 +118,7 @@ conv_fwd_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
                         float s = bs[v];
 #pragma unroll
                         for (int w = 0; w < W - 1; ++w) s = fmaf(wt[w][v], win[w][v], s);
-                        s = fmaf(wt[W - 1][v], in[u][v], s);
+                        s = fmaf(wt[W - 1][v], in[u].get(v), s);
                         z[v] = silu ? silu_f(s) : s;
                     }
                     if (OSDN_IN_BOUNDS(row + u, rows))
@@ -104,10 +127,12 @@ conv_fwd_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
                     for (int v = 0; v < V; ++v) {
 #pragma unroll
                         for (int w = 0; w + 1 < W - 1; ++w) win[w][v] = win[w + 1][v];
-                        win[W - 2][v] = in[u][v];
+                        win[W - 2][v] = in[u].get(v);
                     }
                 }
             }
+#pragma unroll
+            for (int u = 0; u < CONV_UNROLL; ++u) in[u] = next[u];
         }
         row = stop;
     }
@@ -149,9 +174,10 @@ conv_step_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
 // dweight and dbias are summed over the strips it walks in registers, over its rows of threads
 // in shared memory, and over the blocks by conv_reduce_kernel, each in a fixed order.
 constexpr int CONV_BWD_STRIPS = 8;
+constexpr int CONV_BWD_UNROLL = 4;  // tokens loaded before the first is used
 
 template <int V, int W, typename IO, typename GO>
-__global__ void __launch_bounds__(32 * CONV_BWD_STRIPS)
+__global__ void __launch_bounds__(32 * CONV_BWD_STRIPS, 3)
 conv_bwd_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
                 const float* __restrict__ bias, const IO* __restrict__ state0, int silu,
                 const GO* __restrict__ dy, const float* __restrict__ dstateT, IO* __restrict__ dx,
@@ -205,16 +231,18 @@ conv_bwd_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
 #pragma unroll
                     for (int v = 0; v < V; ++v) dz[j][v] = 0.f;
                 // dz_t from x and dy, then dx_{t - W + 1}, whose last contribution dz_t is
-                for (int64_t t0 = p0; t0 < p1 + W - 1; t0 += 4) {
-                    float in[4][V], g[4][V];
+#pragma unroll 1
+                for (int64_t t0 = p0; t0 < p1 + W - 1; t0 += CONV_BWD_UNROLL) {
+                    raw_io<V, IO> in[CONV_BWD_UNROLL];
+                    raw_io<V, GO> g[CONV_BWD_UNROLL];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
+                    for (int u = 0; u < CONV_BWD_UNROLL; ++u)
                         if (t0 + u < p1 + W - 1 && t0 + u < b) {
-                            vec_io<V, IO>::load(x + (t0 + u) * C + c, in[u]);
-                            vec_io<V, GO>::load(dy + (t0 + u) * C + c, g[u]);
+                            in[u].load(x + (t0 + u) * C + c);
+                            g[u].load(dy + (t0 + u) * C + c);
                         }
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
+                    for (int u = 0; u < CONV_BWD_UNROLL; ++u) {
                         const int64_t t = t0 + u;
                         if (t >= p1 + W - 1) break;
                         const bool live = t < b;
@@ -225,10 +253,10 @@ conv_bwd_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
                                 win[w][v] = win[w + 1][v];
                                 dz[w][v] = dz[w + 1][v];
                             }
-                            win[W - 1][v] = live ? in[u][v] : 0.f;
+                            win[W - 1][v] = live ? in[u].get(v) : 0.f;
                             float d = 0.f;
                             if (live) {
-                                d = g[u][v];
+                                d = g[u].get(v);
                                 if (silu) {
                                     float z = bs[v];
 #pragma unroll

@@ -12,7 +12,7 @@ namespace osdn {
 // V consecutive io elements <-> fp32 registers, as accesses of up to 16 bytes (V * sizeof(IO)
 // bytes, at least 16 at a time where V allows it).  V == 1 makes no assumption on alignment.
 template <int V, typename IO> struct vec_io {
-    static_assert(V % 4 == 0, "vectors of 4 or 8 elements");
+    static_assert(V % 4 == 0, "vectors of 4 or 8 elements (2 and 1 below)");
     static __device__ __forceinline__ void load(const IO* p, float* x) {
         if constexpr (V == 8 && sizeof(IO) == 2) {
             const uint4 r = __ldg(reinterpret_cast<const uint4*>(p));
@@ -46,6 +46,15 @@ template <int V, typename IO> struct vec_io {
         }
     }
 };
+template <typename IO> struct vec_io<2, IO> {
+    static __device__ __forceinline__ void load(const IO* p, float* x) {
+        const float2 v = load2<IO>(p);
+        x[0] = v.x; x[1] = v.y;
+    }
+    static __device__ __forceinline__ void store(IO* p, const float* x) {
+        store2<IO>(p, make_float2(x[0], x[1]));
+    }
+};
 template <typename IO> struct vec_io<1, IO> {
     static __device__ __forceinline__ void load(const IO* p, float* x) {
         x[0] = io_traits<IO>::to_f32(*p);
@@ -53,6 +62,34 @@ template <typename IO> struct vec_io<1, IO> {
     static __device__ __forceinline__ void store(IO* p, const float* x) {
         *p = io_traits<IO>::from_f32(x[0]);
     }
+};
+
+// V consecutive io elements as they lie in memory: loads that are in flight hold half (bf16) the
+// registers of their fp32 values.
+template <int V, typename IO> struct raw_io {
+    static constexpr int WORDS = V * (int)sizeof(IO) / 4;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const IO* p) {
+        if constexpr (WORDS == 4) {
+            const uint4 r = __ldg(reinterpret_cast<const uint4*>(p));
+            w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
+        } else if constexpr (WORDS == 1) {
+            w[0] = __ldg(reinterpret_cast<const unsigned int*>(p));
+        } else {
+            static_assert(WORDS == 2, "4, 8 or 16 bytes");
+            const uint2 r = __ldg(reinterpret_cast<const uint2*>(p));
+            w[0] = r.x; w[1] = r.y;
+        }
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(IO) == 4) return __uint_as_float(w[i]);
+        return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+};
+template <typename IO> struct raw_io<1, IO> {
+    IO v;
+    __device__ __forceinline__ void load(const IO* p) { v = *p; }
+    __device__ __forceinline__ float get(int) const { return io_traits<IO>::to_f32(v); }
 };
 
 // 1 / (1 + e^-z).  e^-z overflows to inf for z < -88, where the quotient is 0 as it should be.

@@ -63,20 +63,17 @@ osdn_status_t check_workspace(const void* ws, size_t have, size_t need) {
     return (reinterpret_cast<uintptr_t>(ws) & 255u) ? OSDN_ERR_ALIGNMENT : OSDN_OK;
 }
 
-// Runs f(constant V, constant W) for the vector width and filter length of a convolution.
-template <typename IO, typename F> osdn_status_t conv_dispatch(int C, int W, bool narrow, F f) {
-    // 16 bytes per access where C keeps rows that aligned, 4 elements where it keeps them 4 apart
-    const int V = C % 8 == 0 && sizeof(IO) == 2 && !narrow ? 8 : C % 4 == 0 ? 4 : 1;
-    auto width = [&](auto v) {
-        switch (W) {
-            case 2: return f(v, std::integral_constant<int, 2>{});
-            case 3: return f(v, std::integral_constant<int, 3>{});
-            default: return f(v, std::integral_constant<int, 4>{});
-        }
-    };
-    if constexpr (sizeof(IO) == 2)
-        if (V == 8) return width(std::integral_constant<int, 8>{});
-    return V == 4 ? width(std::integral_constant<int, 4>{}) : width(std::integral_constant<int, 1>{});
+// Runs f(constant V, constant W) for the channels of a thread and the filter length: the widest V
+// of MAX, MAX / 2, .. 2 that divides C (rows stay aligned to V elements then), else 1.
+template <int MAX, typename F> osdn_status_t conv_dispatch(int C, int W, F f) {
+    if constexpr (MAX > 1)
+        if (C % MAX != 0) return conv_dispatch<MAX / 2>(C, W, f);
+    using v = std::integral_constant<int, MAX>;
+    switch (W) {
+        case 2: return f(v{}, std::integral_constant<int, 2>{});
+        case 3: return f(v{}, std::integral_constant<int, 3>{});
+        default: return f(v{}, std::integral_constant<int, 4>{});
+    }
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -86,7 +83,7 @@ osdn_status_t launch_conv_fwd(const void* x, const float* weight, const float* b
                               const void* state0, int silu, void* y, void* stateT,
                               const int32_t* cu, int N, int T, int C, int W, int64_t rows,
                               cudaStream_t stream) {
-    return conv_dispatch<IO>(C, W, false, [&](auto v, auto w) -> osdn_status_t {
+    return conv_dispatch<CONV_MAX_V<IO>>(C, W, [&](auto v, auto w) -> osdn_status_t {
         constexpr int V = decltype(v)::value, WW = decltype(w)::value;
         const int64_t gx = ceil_div(C, (int64_t)V * CONV_THREADS);
         // strips of as many tokens as still leave about 1024 threads for every SM
@@ -110,7 +107,7 @@ osdn_status_t launch_conv_fwd(const void* x, const float* weight, const float* b
 template <typename IO>
 osdn_status_t launch_conv_step(const void* x, const float* weight, const float* bias, void* state,
                                int silu, void* y, int N, int C, int W, cudaStream_t stream) {
-    return conv_dispatch<IO>(C, W, false, [&](auto v, auto w) -> osdn_status_t {
+    return conv_dispatch<CONV_MAX_V<IO>>(C, W, [&](auto v, auto w) -> osdn_status_t {
         constexpr int V = decltype(v)::value, WW = decltype(w)::value;
         const int64_t gx = ceil_div(C, (int64_t)V * CONV_THREADS);
         conv_step_kernel<V, WW, IO><<<dim3((unsigned)gx, (unsigned)(N < 32768 ? N : 32768)),
@@ -126,12 +123,12 @@ osdn_status_t launch_conv_step(const void* x, const float* weight, const float* 
 struct ConvBwdPlan { int64_t gx; int strip, row_blocks; };
 ConvBwdPlan conv_bwd_plan(int64_t rows, int C) {
     ConvBwdPlan pl;
-    const int V = C % 4 == 0 ? 4 : 1;
+    const int V = C % 2 == 0 ? CONV_BWD_MAX_V : 1;
     const int sms = 148;  // a constant, so that the workspace's size does not need a device
     pl.gx = ceil_div(C, 32 * V);
     pl.strip = 64;
-    while (pl.strip > 8 && ceil_div(rows, CONV_BWD_STRIPS * pl.strip) * pl.gx < 3 * sms) pl.strip /= 2;
-    int64_t most = ceil_div(4 * sms, pl.gx);
+    while (pl.strip > 8 && ceil_div(rows, CONV_BWD_STRIPS * pl.strip) * pl.gx < 6 * sms) pl.strip /= 2;
+    int64_t most = ceil_div(6 * sms, pl.gx);
     int64_t rb = ceil_div(rows, CONV_BWD_STRIPS * pl.strip);
     pl.row_blocks = (int)(rb < 1 ? 1 : rb > most ? most : rb);
     return pl;
@@ -145,16 +142,13 @@ osdn_status_t launch_conv_bwd(const void* x, const float* weight, const float* b
                               cudaStream_t stream) {
     const ConvBwdPlan pl = conv_bwd_plan(rows, C);
     const int64_t tail = cu || dstate0 ? ceil_div(N < 4096 ? N : 4096, CONV_BWD_STRIPS) : 0;
-    const osdn_status_t st = conv_dispatch<IO>(C, W, true, [&](auto v, auto w) -> osdn_status_t {
+    const osdn_status_t st = conv_dispatch<CONV_BWD_MAX_V>(C, W, [&](auto v, auto w) -> osdn_status_t {
         constexpr int V = decltype(v)::value, WW = decltype(w)::value;
-        if constexpr (V <= 4) {
-            conv_bwd_kernel<V, WW, IO, GO>
-                <<<dim3((unsigned)pl.gx, (unsigned)(pl.row_blocks + tail)),
-                   dim3(32, CONV_BWD_STRIPS), 0, stream>>>(
-                    static_cast<const IO*>(x), weight, bias, static_cast<const IO*>(state0), silu,
-                    static_cast<const GO*>(dy), dstateT, static_cast<IO*>(dx), dstate0, part, cu, N,
-                    T, C, rows, pl.row_blocks, pl.strip);
-        }
+        conv_bwd_kernel<V, WW, IO, GO>
+            <<<dim3((unsigned)pl.gx, (unsigned)(pl.row_blocks + tail)), dim3(32, CONV_BWD_STRIPS), 0,
+               stream>>>(static_cast<const IO*>(x), weight, bias, static_cast<const IO*>(state0), silu,
+                         static_cast<const GO*>(dy), dstateT, static_cast<IO*>(dx), dstate0, part, cu, N,
+                         T, C, rows, pl.row_blocks, pl.strip);
         return launch_status();
     });
     if (st != OSDN_OK) return st;

@@ -9,6 +9,7 @@ raises, and a non-OK status raises :class:`OsdnError`.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Optional
@@ -371,55 +372,73 @@ def osdn_rho_geomean(rho, cu_seqlens=None, q_geo=None, stream=None):
 # ------------------------------------------------------------------------------------------
 # Layer operators around the mixer: the short causal convolution, the selective scan, the norm.
 
-class _On:
-    """Makes a tensor's device current, and `stream` (default: that device's current stream) the
-    stream that the call launches on and that its outputs and workspace are allocated for."""
+# A call launches on the current stream of its tensors' device, and a decoder makes thousands of
+# them a second: the checks below look at each tensor once, and pointers go to ctypes as integers.
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, t, stream):
+
+def _placed(fn):
+    """Runs an entry point with its first tensor's device current and, when `stream` is given, that
+    stream: outputs and workspace are then allocated for the stream that the call launches on."""
+    @functools.wraps(fn)
+    def call(t, *args, stream=None, **kw):
         if not t.is_cuda:
             raise ValueError("tensors must be CUDA tensors")
-        self.device = t.device
-        self.stream = stream
-        self.inner = []
-        if t.device.index != torch.cuda.current_device():
-            self.inner.append(torch.cuda.device(t.device))
-        if stream is not None:
-            if stream.device != t.device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
-            self.inner.append(torch.cuda.stream(stream))
+        if stream is None and t.device.index == _current_device():
+            return fn(t, *args, **kw)
+        if stream is not None and stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+        with torch.cuda.device(t.device), torch.cuda.stream(stream):
+            return fn(t, *args, **kw)
+    return call
 
-    def __enter__(self):
-        for c in self.inner:
-            c.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream()
-        self.handle = ctypes.c_void_p(s.cuda_stream)
-        return self
 
-    def __exit__(self, *exc):
-        for c in reversed(self.inner):
-            c.__exit__(*exc)
+def _refuse(t, name, dtype, shape, device):
+    _req(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
-    def need(self, t, name, dtype=None, shape=None):
-        if t is not None:
-            _req(t, name, dtype, shape)
-            if t.device != self.device:
-                raise ValueError(f"{name} is on {t.device}, expected {self.device}")
 
-    def out(self, t, name, dtype, shape):
-        """The caller's output tensor, checked, or a new one."""
-        if t is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        self.need(t, name, dtype, shape)
-        return t
+def _ptr(t, name, dtype, shape, device):
+    """Address of a tensor (None for None) after checking its type, shape, device and layout."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _refuse(t, name, dtype, shape, device)
+    return t.data_ptr()
 
-    def workspace(self, t, need):
-        """(tensor, bytes) of the caller's workspace or of a new one; (None, 0) for no bytes."""
-        if t is None:
-            if need == 0:
-                return None, 0
-            t = torch.empty(need, dtype=torch.uint8, device=self.device)
-        self.need(t, "workspace")
-        return t, t.numel() * t.element_size()
+
+def _out(t, name, dtype, shape, device):
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _ptr(t, name, dtype, shape, device)
+    return t
+
+
+def _packed(cu_seqlens, B, device):
+    """(address, num_seqs, N) of packed offsets, or (None, 0, B)."""
+    if cu_seqlens is None:
+        return None, 0, B
+    n = cu_seqlens.numel() - 1
+    return _ptr(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), device), n, n
+
+
+def _scratch(t, need, device):
+    """(tensor, address, bytes) of the caller's workspace or of a new one."""
+    if t is None:
+        if need == 0:
+            return None, None, 0
+        t = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _req(t, "workspace")
+        if t.device != device:
+            raise ValueError(f"workspace is on {t.device}, expected {device}")
+    return t, t.data_ptr(), t.numel() * t.element_size()
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _silu_flag(activation):
@@ -429,102 +448,96 @@ def _silu_flag(activation):
 
 
 def _conv_dims(x, weight, lead):
-    """(leading sizes, C, W) of a convolution's input [*lead, ...channels] and filters [C, W]."""
+    """(C, W) of a convolution's input [lead sizes, ...channels] and filters [C, W]."""
     if x.dim() < lead + 1:
         raise ValueError(f"x has shape {tuple(x.shape)}, expected {lead} leading sizes and channels")
     if weight.dim() != 2:
         raise ValueError(f"weight has shape {tuple(weight.shape)}, expected [C, W]")
-    head, tail = x.shape[:lead], x.shape[lead:]
-    return head, tail.numel(), weight.shape[1]
+    C = x.shape[lead]
+    for n in x.shape[lead + 1:]:
+        C *= n
+    return C, weight.shape[1]
 
 
+@_placed
 def osdn_conv_fwd(x, weight, bias=None, state0=None, activation: Optional[str] = "silu",
-                  cu_seqlens=None, y=None, stateT=None, return_state: bool = True, stream=None):
+                  cu_seqlens=None, y=None, stateT=None, return_state: bool = True):
     """Short causal convolution over each channel's last W tokens: returns ``(y, stateT)``
     (``stateT`` None when ``return_state`` is False).  x: [B, T, C], or [B, T, H, D] with
     C = H * D (q, k or v as the mixer takes them); weight: [C, W] float32, W in 2..4; bias: [C]
     float32; state0, stateT: [N, W - 1, C] in x's dtype, the last inputs, oldest first;
-    activation: "silu" or None."""
-    with _On(x, stream) as on:
-        (B, T), C, W = _conv_dims(x, weight, 2)
-        io = _io(x)
-        on.need(x, "x")
-        on.need(weight, "weight", torch.float32, (C, W))
-        on.need(bias, "bias", torch.float32, (C,))
-        on.need(cu_seqlens, "cu_seqlens", torch.int32)
-        num_seqs, N = _seqs(cu_seqlens, B)
-        on.need(state0, "state0", x.dtype, (N, W - 1, C))
-        y = on.out(y, "y", x.dtype, x.shape)
-        if stateT is not None or return_state:
-            stateT = on.out(stateT, "stateT", x.dtype, (N, W - 1, C))
-        _check(LIB.osdn_conv_fwd(_p(x), _p(weight), _p(bias), _p(state0), _silu_flag(activation),
-                                 _p(y), _p(stateT), _p(cu_seqlens), num_seqs, B, T, C, W, io,
-                                 on.handle), "osdn_conv_fwd")
+    activation: "silu" or None; stream: where to launch (default: the current stream)."""
+    C, W = _conv_dims(x, weight, 2)
+    io, dev, dt = _io(x), x.device, x.dtype
+    B, T = x.shape[0], x.shape[1]
+    cu, num_seqs, N = _packed(cu_seqlens, B, dev)
+    y = torch.empty_like(x) if y is None else _out(y, "y", dt, x.shape, dev)
+    if stateT is not None or return_state:
+        stateT = _out(stateT, "stateT", dt, (N, W - 1, C), dev)
+    _check(LIB.osdn_conv_fwd(_ptr(x, "x", dt, x.shape, dev),
+                             _ptr(weight, "weight", torch.float32, (C, W), dev),
+                             _ptr(bias, "bias", torch.float32, (C,), dev),
+                             _ptr(state0, "state0", dt, (N, W - 1, C), dev),
+                             _silu_flag(activation), y.data_ptr(), _addr(stateT), cu, num_seqs, B, T,
+                             C, W, io, _raw_stream(dev.index)), "osdn_conv_fwd")
     return y, stateT
 
 
-def osdn_conv_step(x, weight, state, bias=None, activation: Optional[str] = "silu", y=None,
-                   stream=None):
+@_placed
+def osdn_conv_step(x, weight, state, bias=None, activation: Optional[str] = "silu", y=None):
     """One token per sequence of :func:`osdn_conv_fwd`: x [N, C] (or [N, H, D]); state
     [N, W - 1, C] in x's dtype, moved on by one token in place.  Returns y of x's shape."""
-    with _On(x, stream) as on:
-        (N,), C, W = _conv_dims(x, weight, 1)
-        io = _io(x)
-        on.need(x, "x")
-        on.need(weight, "weight", torch.float32, (C, W))
-        on.need(bias, "bias", torch.float32, (C,))
-        if state is None:
-            raise ValueError("state is required")
-        on.need(state, "state", x.dtype, (N, W - 1, C))
-        y = on.out(y, "y", x.dtype, x.shape)
-        _check(LIB.osdn_conv_step(_p(x), _p(weight), _p(bias), _p(state), _silu_flag(activation),
-                                  _p(y), N, C, W, io, on.handle), "osdn_conv_step")
+    C, W = _conv_dims(x, weight, 1)
+    io, dev, dt, N = _io(x), x.device, x.dtype, x.shape[0]
+    if state is None:
+        raise ValueError("state is required")
+    y = torch.empty_like(x) if y is None else _out(y, "y", dt, x.shape, dev)
+    _check(LIB.osdn_conv_step(_ptr(x, "x", dt, x.shape, dev),
+                              _ptr(weight, "weight", torch.float32, (C, W), dev),
+                              _ptr(bias, "bias", torch.float32, (C,), dev),
+                              _ptr(state, "state", dt, (N, W - 1, C), dev), _silu_flag(activation),
+                              y.data_ptr(), N, C, W, io, _raw_stream(dev.index)), "osdn_conv_step")
     return y
 
 
+@_placed
 def osdn_conv_bwd(x, weight, dy, bias=None, state0=None, dstateT=None,
-                  activation: Optional[str] = "silu", cu_seqlens=None, workspace=None,
-                  stream=None):
+                  activation: Optional[str] = "silu", cu_seqlens=None, workspace=None):
     """Gradients of :func:`osdn_conv_fwd` given dy (x's shape; x's dtype or float32, as
     :func:`osdn_bwd` returns for q, k and v) and optionally dstateT [N, W - 1, C] float32.
     Returns a dict: dx in x's dtype; dweight, dbias (None without bias) and dstate0 (None without
     state0) in float32."""
-    with _On(x, stream) as on:
-        (B, T), C, W = _conv_dims(x, weight, 2)
-        io = _io(x)
-        on.need(x, "x")
-        on.need(weight, "weight", torch.float32, (C, W))
-        on.need(bias, "bias", torch.float32, (C,))
-        on.need(dy, "dy", None, x.shape)
-        if dy.dtype not in (x.dtype, torch.float32):
-            raise TypeError(f"dy must be {x.dtype} or torch.float32, got {dy.dtype}")
-        on.need(cu_seqlens, "cu_seqlens", torch.int32)
-        num_seqs, N = _seqs(cu_seqlens, B)
-        on.need(state0, "state0", x.dtype, (N, W - 1, C))
-        on.need(dstateT, "dstateT", torch.float32, (N, W - 1, C))
-        f32 = dict(dtype=torch.float32, device=x.device)
-        g = {"dx": torch.empty_like(x), "dweight": torch.empty((C, W), **f32),
-             "dbias": None if bias is None else torch.empty((C,), **f32),
-             "dstate0": None if state0 is None else torch.empty((N, W - 1, C), **f32)}
-        ws, ws_bytes = on.workspace(workspace, LIB.osdn_conv_bwd_workspace_bytes(B, T, C, W))
-        _check(LIB.osdn_conv_bwd(_p(x), _p(weight), _p(bias), _p(state0), _silu_flag(activation),
-                                 _p(dy), _io(dy), _p(dstateT), _p(g["dx"]), _p(g["dweight"]),
-                                 _p(g["dbias"]), _p(g["dstate0"]), _p(cu_seqlens), num_seqs, B, T,
-                                 C, W, io, _p(ws), ws_bytes, on.handle), "osdn_conv_bwd")
+    C, W = _conv_dims(x, weight, 2)
+    io, dev, dt = _io(x), x.device, x.dtype
+    B, T = x.shape[0], x.shape[1]
+    f32 = torch.float32
+    if dy.dtype not in (dt, f32):
+        raise TypeError(f"dy must be {dt} or torch.float32, got {dy.dtype}")
+    cu, num_seqs, N = _packed(cu_seqlens, B, dev)
+    g = {"dx": torch.empty_like(x), "dweight": torch.empty((C, W), dtype=f32, device=dev),
+         "dbias": None if bias is None else torch.empty((C,), dtype=f32, device=dev),
+         "dstate0": None if state0 is None else torch.empty((N, W - 1, C), dtype=f32, device=dev)}
+    ws, ws_ptr, ws_bytes = _scratch(workspace, LIB.osdn_conv_bwd_workspace_bytes(B, T, C, W), dev)
+    _check(LIB.osdn_conv_bwd(_ptr(x, "x", dt, x.shape, dev), _ptr(weight, "weight", f32, (C, W), dev),
+                             _ptr(bias, "bias", f32, (C,), dev),
+                             _ptr(state0, "state0", dt, (N, W - 1, C), dev), _silu_flag(activation),
+                             _ptr(dy, "dy", dy.dtype, x.shape, dev), _io(dy),
+                             _ptr(dstateT, "dstateT", f32, (N, W - 1, C), dev), g["dx"].data_ptr(),
+                             g["dweight"].data_ptr(), _addr(g["dbias"]), _addr(g["dstate0"]), cu,
+                             num_seqs, B, T, C, W, io, ws_ptr, ws_bytes, _raw_stream(dev.index)),
+           "osdn_conv_bwd")
     return g
 
 
-def _ssm_check(on, x, dt, A, b, c, D, dt_bias, lead):
-    """Checks the scan's common inputs; returns (H, G, Dk, Dv)."""
+def _ssm_args(x, dt, A, b, c, D, dt_bias, lead, dev):
+    """Addresses of the scan's common inputs after their checks, and (H, G, Dk, Dv)."""
     H, Dv = x.shape[-2:]
     G, Dk = b.shape[-2:]
-    on.need(x, "x", None, (*lead, H, Dv))
-    on.need(b, "b", x.dtype, (*lead, G, Dk))
-    on.need(c, "c", x.dtype, (*lead, G, Dk))
-    on.need(dt, "dt", torch.float32, (*lead, H))
-    for name, t in (("A", A), ("D", D), ("dt_bias", dt_bias)):
-        on.need(t, name, torch.float32, (H,))
-    return H, G, Dk, Dv
+    f32, io = torch.float32, x.dtype
+    return (_ptr(x, "x", io, (*lead, H, Dv), dev), _ptr(dt, "dt", f32, (*lead, H), dev),
+            _ptr(A, "A", f32, (H,), dev), _ptr(b, "b", io, (*lead, G, Dk), dev),
+            _ptr(c, "c", io, (*lead, G, Dk), dev), _ptr(D, "D", f32, (H,), dev),
+            _ptr(dt_bias, "dt_bias", f32, (H,), dev)), H, G, Dk, Dv
 
 
 def osdn_ssm_fwd_workspace_bytes(B: int, T: int, H: int, Dk: int, Dv: int, dtype=torch.bfloat16,
@@ -533,77 +546,70 @@ def osdn_ssm_fwd_workspace_bytes(B: int, T: int, H: int, Dk: int, Dv: int, dtype
     return int(LIB.osdn_ssm_fwd_workspace_bytes(num_seqs, B, T, H, Dk, Dv, io))
 
 
+@_placed
 def osdn_ssm_fwd(x, dt, A, b, c, D=None, dt_bias=None, softplus: bool = True, S0=None,
-                 cu_seqlens=None, y=None, ST=None, workspace=None, return_ST: bool = True,
-                 stream=None):
+                 cu_seqlens=None, y=None, ST=None, workspace=None, return_ST: bool = True):
     """Selective state-space scan: S_t = exp(step_t A) S_{t-1} + step_t x_t b_t^T and
     y_t = S_t c_t + D x_t with step = softplus(dt + dt_bias) (softplus False: dt + dt_bias).
     x: [B, T, H, Dv]; b, c: [B, T, G, Dk], shared by H / G heads each; dt: [B, T, H] float32;
     A, D, dt_bias: [H] float32; S0, ST: [N, H, Dv, Dk] float32, the mixer's state layout.
     Returns ``(y, ST)`` (``ST`` None when ``return_ST`` is False)."""
-    with _On(x, stream) as on:
-        B, T = x.shape[:2]
-        H, G, Dk, Dv = _ssm_check(on, x, dt, A, b, c, D, dt_bias, (B, T))
-        io = _io(x)
-        on.need(cu_seqlens, "cu_seqlens", torch.int32)
-        num_seqs, N = _seqs(cu_seqlens, B)
-        on.need(S0, "S0", torch.float32, (N, H, Dv, Dk))
-        y = on.out(y, "y", x.dtype, x.shape)
-        if ST is not None or return_ST:
-            ST = on.out(ST, "ST", torch.float32, (N, H, Dv, Dk))
-        ws, ws_bytes = on.workspace(
-            workspace, LIB.osdn_ssm_fwd_workspace_bytes(num_seqs, B, T, H, Dk, Dv, io))
-        _check(LIB.osdn_ssm_fwd(_p(x), _p(dt), _p(A), _p(b), _p(c), _p(D), _p(dt_bias),
-                                int(softplus), _p(S0), _p(y), _p(ST), _p(cu_seqlens), num_seqs, B,
-                                T, H, G, Dk, Dv, io, _p(ws), ws_bytes, on.handle), "osdn_ssm_fwd")
+    io, dev = _io(x), x.device
+    B, T = x.shape[0], x.shape[1]
+    args, H, G, Dk, Dv = _ssm_args(x, dt, A, b, c, D, dt_bias, (B, T), dev)
+    cu, num_seqs, N = _packed(cu_seqlens, B, dev)
+    y = torch.empty_like(x) if y is None else _out(y, "y", x.dtype, x.shape, dev)
+    if ST is not None or return_ST:
+        ST = _out(ST, "ST", torch.float32, (N, H, Dv, Dk), dev)
+    ws, ws_ptr, ws_bytes = _scratch(
+        workspace, LIB.osdn_ssm_fwd_workspace_bytes(num_seqs, B, T, H, Dk, Dv, io), dev)
+    _check(LIB.osdn_ssm_fwd(*args, int(softplus),
+                            _ptr(S0, "S0", torch.float32, (N, H, Dv, Dk), dev), y.data_ptr(), _addr(ST),
+                            cu, num_seqs, B, T, H, G, Dk, Dv, io, ws_ptr, ws_bytes,
+                            _raw_stream(dev.index)), "osdn_ssm_fwd")
     return y, ST
 
 
-def osdn_ssm_step(x, dt, A, b, c, S, D=None, dt_bias=None, softplus: bool = True, y=None,
-                  stream=None):
+@_placed
+def osdn_ssm_step(x, dt, A, b, c, S, D=None, dt_bias=None, softplus: bool = True, y=None):
     """One token per sequence of :func:`osdn_ssm_fwd` (the decode path): x [N, H, Dv]; b, c
     [N, G, Dk]; dt [N, H] float32; S [N, H, Dv, Dk] float32, updated in place.  Returns y."""
-    with _On(x, stream) as on:
-        N = x.shape[0]
-        H, G, Dk, Dv = _ssm_check(on, x, dt, A, b, c, D, dt_bias, (N,))
-        io = _io(x)
-        if S is None:
-            raise ValueError("S is required")
-        on.need(S, "S", torch.float32, (N, H, Dv, Dk))
-        y = on.out(y, "y", x.dtype, x.shape)
-        _check(LIB.osdn_ssm_step(_p(x), _p(dt), _p(A), _p(b), _p(c), _p(D), _p(dt_bias),
-                                 int(softplus), _p(S), _p(y), N, H, G, Dk, Dv, io, on.handle),
-               "osdn_ssm_step")
+    io, dev, N = _io(x), x.device, x.shape[0]
+    args, H, G, Dk, Dv = _ssm_args(x, dt, A, b, c, D, dt_bias, (N,), dev)
+    if S is None:
+        raise ValueError("S is required")
+    y = torch.empty_like(x) if y is None else _out(y, "y", x.dtype, x.shape, dev)
+    _check(LIB.osdn_ssm_step(*args, int(softplus), _ptr(S, "S", torch.float32, (N, H, Dv, Dk), dev),
+                             y.data_ptr(), N, H, G, Dk, Dv, io, _raw_stream(dev.index)),
+           "osdn_ssm_step")
     return y
 
 
+@_placed
 def osdn_ssm_bwd(x, dt, A, b, c, dy, D=None, dt_bias=None, softplus: bool = True, S0=None,
-                 dST=None, cu_seqlens=None, workspace=None, stream=None):
+                 dST=None, cu_seqlens=None, workspace=None):
     """Gradients of :func:`osdn_ssm_fwd` given dy (x's shape and dtype) and optionally dST.
     Returns a dict: dx, db, dc in x's dtype; ddt, dA, dD, ddt_bias and dS0 in float32 (the last
     three None where their input is)."""
-    with _On(x, stream) as on:
-        B, T = x.shape[:2]
-        H, G, Dk, Dv = _ssm_check(on, x, dt, A, b, c, D, dt_bias, (B, T))
-        io = _io(x)
-        on.need(dy, "dy", x.dtype, x.shape)
-        on.need(cu_seqlens, "cu_seqlens", torch.int32)
-        num_seqs, N = _seqs(cu_seqlens, B)
-        on.need(S0, "S0", torch.float32, (N, H, Dv, Dk))
-        on.need(dST, "dST", torch.float32, (N, H, Dv, Dk))
+    io, dev, f32 = _io(x), x.device, torch.float32
+    B, T = x.shape[0], x.shape[1]
+    args, H, G, Dk, Dv = _ssm_args(x, dt, A, b, c, D, dt_bias, (B, T), dev)
+    cu, num_seqs, N = _packed(cu_seqlens, B, dev)
 
-        def like(t):
-            return None if t is None else torch.empty_like(t)
+    def like(t):
+        return None if t is None else torch.empty_like(t)
 
-        g = {"dx": like(x), "ddt": like(dt), "dA": like(A), "db": like(b), "dc": like(c),
-             "dD": like(D), "ddt_bias": like(dt_bias), "dS0": like(S0)}
-        ws, ws_bytes = on.workspace(
-            workspace, LIB.osdn_ssm_bwd_workspace_bytes(num_seqs, B, T, H, Dk, Dv, io))
-        _check(LIB.osdn_ssm_bwd(_p(x), _p(dt), _p(A), _p(b), _p(c), _p(D), _p(dt_bias),
-                                int(softplus), _p(S0), _p(dy), _p(dST), _p(g["dx"]), _p(g["ddt"]),
-                                _p(g["dA"]), _p(g["db"]), _p(g["dc"]), _p(g["dD"]),
-                                _p(g["ddt_bias"]), _p(g["dS0"]), _p(cu_seqlens), num_seqs, B, T, H,
-                                G, Dk, Dv, io, _p(ws), ws_bytes, on.handle), "osdn_ssm_bwd")
+    g = {"dx": like(x), "ddt": like(dt), "dA": like(A), "db": like(b), "dc": like(c),
+         "dD": like(D), "ddt_bias": like(dt_bias), "dS0": like(S0)}
+    ws, ws_ptr, ws_bytes = _scratch(
+        workspace, LIB.osdn_ssm_bwd_workspace_bytes(num_seqs, B, T, H, Dk, Dv, io), dev)
+    _check(LIB.osdn_ssm_bwd(*args, int(softplus), _ptr(S0, "S0", f32, (N, H, Dv, Dk), dev),
+                            _ptr(dy, "dy", x.dtype, x.shape, dev),
+                            _ptr(dST, "dST", f32, (N, H, Dv, Dk), dev),
+                            *(_addr(g[k]) for k in ("dx", "ddt", "dA", "db", "dc", "dD", "ddt_bias",
+                                                    "dS0")),
+                            cu, num_seqs, B, T, H, G, Dk, Dv, io, ws_ptr, ws_bytes,
+                            _raw_stream(dev.index)), "osdn_ssm_bwd")
     return g
 
 
@@ -613,67 +619,61 @@ def _gate_act(gate_act):
     return int(gate_act == "sigmoid")
 
 
-def _norm_check(on, f, x, gate, w_post, w_next):
-    """Checks the norm's common inputs; returns (R, D)."""
-    D = f.shape[-1]
-    on.need(f, "f")
-    for name, t in (("x", x), ("gate", gate)):
-        on.need(t, name, f.dtype, f.shape)
-    for name, t in (("w_post", w_post), ("w_next", w_next)):
-        on.need(t, name, torch.float32, (D,))
-    return (f.numel() // D if D else 0), D
+def _norm_args(f, x, gate, w_post, w_next, dev):
+    """Addresses of the norm's common inputs after their checks, and (R, D)."""
+    D, dt, shape = f.shape[-1], f.dtype, f.shape
+    return (_ptr(f, "f", dt, shape, dev), _ptr(x, "x", dt, shape, dev),
+            _ptr(gate, "gate", dt, shape, dev), _ptr(w_post, "w_post", torch.float32, (D,), dev),
+            _ptr(w_next, "w_next", torch.float32, (D,), dev)), (f.numel() // D if D else 0), D
 
 
+@_placed
 def osdn_norm_fwd(f, x=None, gate=None, w_post=None, w_next=None, gate_act: str = "silu",
                   gate_first: bool = False, scale: float = 1.0, eps: float = 1e-5, x_out=None,
-                  h=None, return_x_out: bool = True, stream=None):
+                  h=None, return_x_out: bool = True):
     """Block norm over the last dimension of f: u = rmsnorm(f) * w_post * act(gate) (gate_first:
     rmsnorm(f * act(gate)) * w_post), x_out = x + scale * u, h = rmsnorm(x_out) * w_next.  Every
     part is optional: w_post, gate, x (no residual), w_next (h is None then).  x, gate: f's shape
     and dtype; w_post, w_next: [D] float32.  Returns ``(x_out, h)``; ``return_x_out`` False (with
     w_next) skips x_out."""
-    with _On(f, stream) as on:
-        R, D = _norm_check(on, f, x, gate, w_post, w_next)
-        io = _io(f)
-        if x_out is not None or return_x_out or w_next is None:
-            x_out = on.out(x_out, "x_out", f.dtype, f.shape)
-        if w_next is not None:
-            h = on.out(h, "h", f.dtype, f.shape)
-        elif h is not None:
-            raise ValueError("h needs w_next")
-        _check(LIB.osdn_norm_fwd(_p(f), _p(x), _p(gate), _p(w_post), _p(w_next),
-                                 _gate_act(gate_act), int(gate_first), float(scale), float(eps),
-                                 _p(x_out), _p(h), R, D, io, on.handle), "osdn_norm_fwd")
+    io, dev = _io(f), f.device
+    args, R, D = _norm_args(f, x, gate, w_post, w_next, dev)
+    if x_out is not None or return_x_out or w_next is None:
+        x_out = torch.empty_like(f) if x_out is None else _out(x_out, "x_out", f.dtype, f.shape, dev)
+    if w_next is not None:
+        h = torch.empty_like(f) if h is None else _out(h, "h", f.dtype, f.shape, dev)
+    elif h is not None:
+        raise ValueError("h needs w_next")
+    _check(LIB.osdn_norm_fwd(*args, _gate_act(gate_act), int(gate_first), scale, eps, _addr(x_out),
+                             _addr(h), R, D, io, _raw_stream(dev.index)), "osdn_norm_fwd")
     return x_out, h
 
 
+@_placed
 def osdn_norm_bwd(f, dx_out=None, dh=None, x=None, gate=None, w_post=None, w_next=None,
                   gate_act: str = "silu", gate_first: bool = False, scale: float = 1.0,
-                  eps: float = 1e-5, workspace=None, stream=None):
+                  eps: float = 1e-5, workspace=None):
     """Gradients of :func:`osdn_norm_fwd` from its inputs, given dx_out (or None for 0) and dh
     (exactly when w_next is given).  Returns a dict: df, dx, dgate in f's dtype, dw_post, dw_next
     in float32; None where the input is."""
-    with _On(f, stream) as on:
-        R, D = _norm_check(on, f, x, gate, w_post, w_next)
-        io = _io(f)
-        for name, t in (("dx_out", dx_out), ("dh", dh)):
-            on.need(t, name, f.dtype, f.shape)
-        if (dh is None) != (w_next is None):
-            raise ValueError("dh is given exactly when w_next is")
-        if dh is None and dx_out is None:
-            raise ValueError("dx_out or dh is required")
+    io, dev = _io(f), f.device
+    args, R, D = _norm_args(f, x, gate, w_post, w_next, dev)
+    if (dh is None) != (w_next is None):
+        raise ValueError("dh is given exactly when w_next is")
+    if dh is None and dx_out is None:
+        raise ValueError("dx_out or dh is required")
 
-        def like(t):
-            return None if t is None else torch.empty_like(t)
+    def like(t):
+        return None if t is None else torch.empty_like(t)
 
-        g = {"df": like(f), "dx": like(x), "dgate": like(gate), "dw_post": like(w_post),
-             "dw_next": like(w_next)}
-        ws, ws_bytes = on.workspace(workspace, LIB.osdn_norm_bwd_workspace_bytes(R, D))
-        _check(LIB.osdn_norm_bwd(_p(f), _p(x), _p(gate), _p(w_post), _p(w_next),
-                                 _gate_act(gate_act), int(gate_first), float(scale), float(eps),
-                                 _p(dx_out), _p(dh), _p(g["df"]), _p(g["dx"]), _p(g["dgate"]),
-                                 _p(g["dw_post"]), _p(g["dw_next"]), R, D, io, _p(ws), ws_bytes,
-                                 on.handle), "osdn_norm_bwd")
+    g = {"df": like(f), "dx": like(x), "dgate": like(gate), "dw_post": like(w_post),
+         "dw_next": like(w_next)}
+    ws, ws_ptr, ws_bytes = _scratch(workspace, LIB.osdn_norm_bwd_workspace_bytes(R, D), dev)
+    _check(LIB.osdn_norm_bwd(*args, _gate_act(gate_act), int(gate_first), scale, eps,
+                             _ptr(dx_out, "dx_out", f.dtype, f.shape, dev),
+                             _ptr(dh, "dh", f.dtype, f.shape, dev),
+                             *(_addr(g[k]) for k in ("df", "dx", "dgate", "dw_post", "dw_next")),
+                             R, D, io, ws_ptr, ws_bytes, _raw_stream(dev.index)), "osdn_norm_bwd")
     return g
 
 
