@@ -16,7 +16,7 @@ namespace osdn {
 
 constexpr int CONV_THREADS = 128;
 template <typename IO> constexpr int CONV_MAX_V = 4;  // channels of a thread
-constexpr int CONV_BWD_MAX_V = 2;
+constexpr int CONV_BWD_MAX_V = 4;
 constexpr int CONV_UNROLL = 4;  // tokens of a group; the next group's loads are in flight meanwhile
 
 // One row of a sequence at position pos (< 0: a row of the initial state) as fp32.
@@ -35,8 +35,8 @@ __device__ __forceinline__ void conv_row(const IO* __restrict__ x, const IO* __r
 
 template <int V, int W>
 __device__ __forceinline__ void conv_weights(const float* __restrict__ weight,
-                                             const float* __restrict__ bias, int c, float (*wt)[V],
-                                             float* bs) {
+                                             const float* __restrict__ bias, int c, fvec<V>* wt,
+                                             fvec<V>& bs) {
     if constexpr (V > 1 && V * W % 4 == 0) {  // V * W neighbouring floats, 16-byte aligned
         float flat[V * W];
 #pragma unroll
@@ -49,7 +49,7 @@ __device__ __forceinline__ void conv_weights(const float* __restrict__ weight,
 #pragma unroll
             for (int w = 0; w < W; ++w) wt[w][v] = flat[v * W + w];
         if (bias) {
-            vec_io<V, float>::load(bias + c, bs);
+            vec_io<V, float>::load(bias + c, bs.x);
             return;
         }
     } else {
@@ -87,7 +87,7 @@ conv_fwd_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
         return;
     }
     if (c >= C) return;
-    float wt[W][V], bs[V];
+    fvec<V> wt[W], bs;
     conv_weights<V, W>(weight, bias, c, wt, bs);
     int64_t row = (int64_t)blockIdx.y * strip;
     const int64_t end = row + strip < rows ? row + strip : rows;
@@ -96,43 +96,41 @@ conv_fwd_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
         int64_t a, b;
         if (!row_sequence(cu, N, T, row, n, a, b)) { ++row; continue; }
         const int64_t stop = b < end ? b : end;
-        float win[W - 1][V];  // the W - 1 inputs before `row`, oldest first
+        constexpr int U = CONV_UNROLL;
+        fvec<V> win[W - 1 + U];  // the W - 1 inputs before a group of tokens, oldest first, then it
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
-            conv_row<V, W>(x, state0, n, a, row - a - (W - 1) + j, C, c, win[j]);
-        raw_io<V, IO> in[CONV_UNROLL], next[CONV_UNROLL];
+            conv_row<V, W>(x, state0, n, a, row - a - (W - 1) + j, C, c, win[j].x);
+        int left = (int)(stop - row);
+        const IO* px = x + row * C + c;
+        IO* py = y + row * C + c;
+        raw_io<V, IO> in[U];
 #pragma unroll
-        for (int u = 0; u < CONV_UNROLL; ++u)
-            if (row + u < stop) in[u].load(x + (row + u) * C + c);
+        for (int u = 0; u < U; ++u)
+            if (u < left) in[u].load(px + (int64_t)u * C);
 #pragma unroll 1
-        for (; row < stop; row += CONV_UNROLL) {
+        for (; left > 0; left -= U) {
 #pragma unroll
-            for (int u = 0; u < CONV_UNROLL; ++u)
-                if (row + CONV_UNROLL + u < stop) next[u].load(x + (row + CONV_UNROLL + u) * C + c);
+            for (int u = 0; u < U; ++u) in[u].to(win[W - 1 + u].x);
+            px += (int64_t)U * C;
 #pragma unroll
-            for (int u = 0; u < CONV_UNROLL; ++u) {
-                if (row + u < stop) {
-                    float z[V];
+            for (int u = 0; u < U; ++u)
+                if (U + u < left) in[u].load(px + (int64_t)u * C);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        float s = bs[v];
+            for (int u = 0; u < U; ++u) {
+                fvec<V> z = bs;
 #pragma unroll
-                        for (int w = 0; w < W - 1; ++w) s = fmaf(wt[w][v], win[w][v], s);
-                        s = fmaf(wt[W - 1][v], in[u].get(v), s);
-                        z[v] = silu ? silu_f(s) : s;
-                    }
-                    if (OSDN_IN_BOUNDS(row + u, rows))
-                        vec_io<V, IO>::store(y + (row + u) * C + c, z);
+                for (int w = 0; w < W; ++w) z = fma_v(wt[w], win[u + w], z);
+                if (silu) {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-#pragma unroll
-                        for (int w = 0; w + 1 < W - 1; ++w) win[w][v] = win[w + 1][v];
-                        win[W - 2][v] = in[u].get(v);
-                    }
+                    for (int v = 0; v < V; ++v) z[v] = silu_f(z[v]);
                 }
+                if (u < left && OSDN_IN_BOUNDS(stop - left + u, rows))
+                    vec_io<V, IO>::store(py + (int64_t)u * C, z.x);
             }
+            py += (int64_t)U * C;
 #pragma unroll
-            for (int u = 0; u < CONV_UNROLL; ++u) in[u] = next[u];
+            for (int j = 0; j < W - 1; ++j) win[j] = win[U + j];
         }
         row = stop;
     }
@@ -149,22 +147,22 @@ conv_step_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
     if (c >= C) return;
     for (int n = blockIdx.y; n < N; n += gridDim.y) {
         IO* st = state + (int64_t)n * (W - 1) * C + c;
-        float in[W][V], wt[W][V], bs[V], z[V];
+        fvec<V> in[W], wt[W], bs;
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) vec_io<V, IO>::load(st + (int64_t)j * C, in[j]);
-        vec_io<V, IO>::load(x + (int64_t)n * C + c, in[W - 1]);
+        for (int j = 0; j < W - 1; ++j) vec_io<V, IO>::load(st + (int64_t)j * C, in[j].x);
+        vec_io<V, IO>::load(x + (int64_t)n * C + c, in[W - 1].x);
         conv_weights<V, W>(weight, bias, c, wt, bs);
+        fvec<V> z = bs;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float s = bs[v];
+        for (int w = 0; w < W; ++w) z = fma_v(wt[w], in[w], z);
+        if (silu) {
 #pragma unroll
-            for (int w = 0; w < W; ++w) s = fmaf(wt[w][v], in[w][v], s);
-            z[v] = silu ? silu_f(s) : s;
+            for (int v = 0; v < V; ++v) z[v] = silu_f(z[v]);
         }
         if (OSDN_IN_BOUNDS(n, N)) {
-            vec_io<V, IO>::store(y + (int64_t)n * C + c, z);
+            vec_io<V, IO>::store(y + (int64_t)n * C + c, z.x);
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) vec_io<V, IO>::store(st + (int64_t)j * C, in[j + 1]);
+            for (int j = 0; j < W - 1; ++j) vec_io<V, IO>::store(st + (int64_t)j * C, in[j + 1].x);
         }
     }
 }
@@ -177,7 +175,7 @@ constexpr int CONV_BWD_STRIPS = 8;
 constexpr int CONV_BWD_UNROLL = 4;  // tokens loaded before the first is used
 
 template <int V, int W, typename IO, typename GO>
-__global__ void __launch_bounds__(32 * CONV_BWD_STRIPS, 3)
+__global__ void __launch_bounds__(32 * CONV_BWD_STRIPS, 2)
 conv_bwd_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
                 const float* __restrict__ bias, const IO* __restrict__ state0, int silu,
                 const GO* __restrict__ dy, const float* __restrict__ dstateT, IO* __restrict__ dx,
@@ -203,13 +201,9 @@ conv_bwd_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
         }
         return;
     }
-    float wt[W][V], bs[V], dw[W][V], db[V];
+    fvec<V> wt[W], bs, dw[W], db = zero_v<V>();
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        db[v] = 0.f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) dw[w][v] = 0.f;
-    }
+    for (int w = 0; w < W; ++w) dw[w] = zero_v<V>();
     if (on) {
         conv_weights<V, W>(weight, bias, c, wt, bs);
         const int64_t hop = (int64_t)row_blocks * CONV_BWD_STRIPS * strip;
@@ -222,65 +216,65 @@ conv_bwd_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
                 int64_t a, b;
                 if (!row_sequence(cu, N, T, row, n, a, b)) { ++row; continue; }
                 const int64_t p0 = row, p1 = b < end ? b : end, len = b - a;
-                float win[W][V], dz[W][V];  // x and dz of the last W tokens, oldest first
+                constexpr int U = CONV_BWD_UNROLL;
+                // x and dz of the last W - 1 tokens, oldest first, then a group's
+                fvec<V> win[W - 1 + U], dz[W - 1 + U];
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j)
-                    conv_row<V, W>(x, state0, n, a, p0 - a - (W - 1) + j, C, c, win[j + 1]);
+                for (int j = 0; j < W - 1; ++j) {
+                    conv_row<V, W>(x, state0, n, a, p0 - a - (W - 1) + j, C, c, win[j].x);
+                    dz[j] = zero_v<V>();
+                }
+                // dz_t of token u of a group
+                auto grad = [&](int u, const raw_io<V, GO>& g) {
+                    fvec<V> d;
+                    g.to(d.x);
+                    if (silu) {
+                        fvec<V> z = bs;
 #pragma unroll
-                for (int j = 0; j < W; ++j)
+                        for (int w = 0; w < W; ++w) z = fma_v(wt[w], win[u + w], z);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) dz[j][v] = 0.f;
-                // dz_t from x and dy, then dx_{t - W + 1}, whose last contribution dz_t is
-#pragma unroll 1
-                for (int64_t t0 = p0; t0 < p1 + W - 1; t0 += CONV_BWD_UNROLL) {
-                    raw_io<V, IO> in[CONV_BWD_UNROLL];
-                    raw_io<V, GO> g[CONV_BWD_UNROLL];
+                        for (int v = 0; v < V; ++v) d[v] *= silu_grad_f(z[v]);
+                    }
+                    dz[W - 1 + u] = d;
+                };
+                auto sums = [&](int u) {
+                    db = add_v(db, dz[W - 1 + u]);
 #pragma unroll
-                    for (int u = 0; u < CONV_BWD_UNROLL; ++u)
-                        if (t0 + u < p1 + W - 1 && t0 + u < b) {
-                            in[u].load(x + (t0 + u) * C + c);
-                            g[u].load(dy + (t0 + u) * C + c);
-                        }
+                    for (int w = 0; w < W; ++w) dw[w] = fma_v(dz[W - 1 + u], win[u + w], dw[w]);
+                };
+                // dx_p, p = t - (W - 1), whose last contribution dz_t is: dz[u + w] is dz_{p + w}
+                auto give = [&](int u) {
+                    fvec<V> r = zero_v<V>();
 #pragma unroll
-                    for (int u = 0; u < CONV_BWD_UNROLL; ++u) {
-                        const int64_t t = t0 + u;
-                        if (t >= p1 + W - 1) break;
-                        const bool live = t < b;
+                    for (int w = 0; w < W; ++w) r = fma_v(wt[W - 1 - w], dz[u + w], r);
+                    return r;
+                };
+                auto shift = [&](int k) {
 #pragma unroll
-                        for (int v = 0; v < V; ++v) {
-#pragma unroll
-                            for (int w = 0; w < W - 1; ++w) {
-                                win[w][v] = win[w + 1][v];
-                                dz[w][v] = dz[w + 1][v];
-                            }
-                            win[W - 1][v] = live ? in[u].get(v) : 0.f;
-                            float d = 0.f;
-                            if (live) {
-                                d = g[u].get(v);
-                                if (silu) {
-                                    float z = bs[v];
-#pragma unroll
-                                    for (int w = 0; w < W; ++w) z = fmaf(wt[w][v], win[w][v], z);
-                                    d *= silu_grad_f(z);
-                                }
-                                if (t < p1) {
-                                    db[v] += d;
-#pragma unroll
-                                    for (int w = 0; w < W; ++w)
-                                        dw[w][v] = fmaf(d, win[w][v], dw[w][v]);
-                                }
-                            }
-                            dz[W - 1][v] = d;
-                        }
-                        const int64_t p = t - (W - 1);  // dz[w] is dz_{p + w}
-                        if (p < p0 && (p0 > a || !dstate0)) continue;
-                        float r[V];
-#pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            r[v] = 0.f;
-#pragma unroll
-                            for (int w = 0; w < W; ++w) r[v] = fmaf(wt[W - 1 - w][v], dz[w][v], r[v]);
-                        }
+                    for (int j = 0; j < W - 1; ++j) {
+                        win[j] = k == 1 ? win[j + 1] : win[j + U];
+                        dz[j] = k == 1 ? dz[j + 1] : dz[j + U];
+                    }
+                };
+                // one token near a piece's ends: before its first own dx is complete (t < p0 + W - 1;
+                // what is complete there belongs to the initial state or to the piece before), or
+                // behind its last token (dz of the next piece's tokens again, 0 behind the sequence)
+                auto edge = [&](int64_t t) {
+                    const bool live = t < b;
+                    win[W - 1] = zero_v<V>();
+                    dz[W - 1] = zero_v<V>();
+                    if (live) {
+                        raw_io<V, IO> i;
+                        raw_io<V, GO> g;
+                        i.load(x + t * C + c);
+                        g.load(dy + t * C + c);
+                        i.to(win[W - 1].x);
+                        grad(0, g);
+                        if (t < p1) sums(0);
+                    }
+                    const int64_t p = t - (W - 1);
+                    if (p >= p0 || (p0 == a && dstate0)) {
+                        fvec<V> r = give(0);
                         const int64_t j = p - a - len + (W - 1);  // p's row of the final state
                         if (dstateT && j >= 0) {
                             const float* e = dstateT + ((int64_t)n * (W - 1) + j) * C + c;
@@ -288,13 +282,52 @@ conv_bwd_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
                             for (int v = 0; v < V; ++v) r[v] += e[v];
                         }
                         if (p >= p0) {
-                            if (OSDN_IN_BOUNDS(p, rows)) vec_io<V, IO>::store(dx + p * C + c, r);
+                            if (OSDN_IN_BOUNDS(p, rows)) vec_io<V, IO>::store(dx + p * C + c, r.x);
                         } else if (OSDN_IN_BOUNDS(n, N)) {
                             vec_io<V, float>::store(
-                                dstate0 + ((int64_t)n * (W - 1) + (p - a) + (W - 1)) * C + c, r);
+                                dstate0 + ((int64_t)n * (W - 1) + (p - a) + (W - 1)) * C + c, r.x);
                         }
                     }
+                    shift(1);
+                };
+                int64_t t = p0;
+#pragma unroll 1
+                for (; t < p0 + W - 1 && t < p1; ++t) edge(t);
+                int groups = (int)((p1 - t) / U);
+                raw_io<V, IO> in[U];
+                raw_io<V, GO> g[U];
+                const IO* px = x + t * C + c;
+                const GO* pg = dy + t * C + c;
+                IO* po = dx + (t - (W - 1)) * C + c;
+                if (groups > 0) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        in[u].load(px + (int64_t)u * C);
+                        g[u].load(pg + (int64_t)u * C);
+                    }
                 }
+                t += (int64_t)groups * U;
+#pragma unroll 1
+                for (; groups > 0; --groups) {
+                    px += (int64_t)U * C;
+                    pg += (int64_t)U * C;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        in[u].to(win[W - 1 + u].x);
+                        grad(u, g[u]);
+                        if (groups > 1) {  // the next group's, in flight from here
+                            in[u].load(px + (int64_t)u * C);
+                            g[u].load(pg + (int64_t)u * C);
+                        }
+                        sums(u);
+                        const fvec<V> r = give(u);
+                        if (OSDN_IN_BOUNDS(p1 - 1, rows)) vec_io<V, IO>::store(po + (int64_t)u * C, r.x);
+                    }
+                    po += (int64_t)U * C;
+                    shift(U);
+                }
+#pragma unroll 1
+                for (; t < p1 + W - 1; ++t) edge(t);
                 row = p1;
             }
         }

@@ -85,16 +85,74 @@ template <int V, typename IO> struct raw_io {
         if constexpr (sizeof(IO) == 4) return __uint_as_float(w[i]);
         return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
     }
+    __device__ __forceinline__ void to(float* x) const {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = get(i);
+    }
 };
 template <typename IO> struct raw_io<1, IO> {
     IO v;
     __device__ __forceinline__ void load(const IO* p) { v = *p; }
     __device__ __forceinline__ float get(int) const { return io_traits<IO>::to_f32(v); }
+    __device__ __forceinline__ void to(float* x) const { x[0] = get(0); }
 };
 
+// V fp32 values; products and sums two at a time (one instruction per pair).
+template <int V> struct fvec {
+    float x[V];
+    __device__ __forceinline__ float operator[](int i) const { return x[i]; }
+    __device__ __forceinline__ float& operator[](int i) { return x[i]; }
+};
+template <int V> __device__ __forceinline__ fvec<V> fma_v(const fvec<V>& a, const fvec<V>& b, const fvec<V>& c) {
+    fvec<V> r;
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const float2 t = __ffma2_rn(make_float2(a.x[i], a.x[i + 1]), make_float2(b.x[i], b.x[i + 1]),
+                                        make_float2(c.x[i], c.x[i + 1]));
+            r.x[i] = t.x;
+            r.x[i + 1] = t.y;
+        }
+    } else {
+        r.x[0] = fmaf(a.x[0], b.x[0], c.x[0]);
+    }
+    return r;
+}
+template <int V> __device__ __forceinline__ fvec<V> add_v(const fvec<V>& a, const fvec<V>& b) {
+    fvec<V> r;
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const float2 t = __fadd2_rn(make_float2(a.x[i], a.x[i + 1]), make_float2(b.x[i], b.x[i + 1]));
+            r.x[i] = t.x;
+            r.x[i + 1] = t.y;
+        }
+    } else {
+        r.x[0] = a.x[0] + b.x[0];
+    }
+    return r;
+}
+template <int V> __device__ __forceinline__ fvec<V> zero_v() {
+    fvec<V> r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.x[i] = 0.f;
+    return r;
+}
+
+// 2^x and 1 / x, each one instruction, good to about 2^-22 (subnormal results are 0).
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcpf(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // 1 / (1 + e^-z).  e^-z overflows to inf for z < -88, where the quotient is 0 as it should be.
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
-__device__ __forceinline__ float silu_f(float z) { return __fdividef(z, 1.f + __expf(-z)); }
+__device__ __forceinline__ float sigmoid_f(float z) { return rcpf(1.f + ex2f(z * -1.4426950408889634f)); }
+__device__ __forceinline__ float silu_f(float z) { return z * sigmoid_f(z); }
 // d silu(z) / dz = s (1 + z (1 - s)), s = sigmoid(z)
 __device__ __forceinline__ float silu_grad_f(float z) {
     const float s = sigmoid_f(z);

@@ -123,12 +123,12 @@ osdn_status_t launch_conv_step(const void* x, const float* weight, const float* 
 struct ConvBwdPlan { int64_t gx; int strip, row_blocks; };
 ConvBwdPlan conv_bwd_plan(int64_t rows, int C) {
     ConvBwdPlan pl;
-    const int V = C % 2 == 0 ? CONV_BWD_MAX_V : 1;
+    const int V = C % 4 == 0 ? 4 : C % 2 == 0 ? 2 : 1;  // as conv_dispatch picks it
     const int sms = 148;  // a constant, so that the workspace's size does not need a device
     pl.gx = ceil_div(C, 32 * V);
     pl.strip = 64;
-    while (pl.strip > 8 && ceil_div(rows, CONV_BWD_STRIPS * pl.strip) * pl.gx < 6 * sms) pl.strip /= 2;
-    int64_t most = ceil_div(6 * sms, pl.gx);
+    while (pl.strip > 8 && ceil_div(rows, CONV_BWD_STRIPS * pl.strip) * pl.gx < 4 * sms) pl.strip /= 2;
+    int64_t most = ceil_div(4 * sms, pl.gx);
     int64_t rb = ceil_div(rows, CONV_BWD_STRIPS * pl.strip);
     pl.row_blocks = (int)(rb < 1 ? 1 : rb > most ? most : rb);
     return pl;

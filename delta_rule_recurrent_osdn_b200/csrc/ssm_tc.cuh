@@ -97,12 +97,6 @@ struct TcsGate {
 };
 static_assert(sizeof(TcsGate) <= TcsSmem<128, TCS_FWD>::GATE_BYTES, "gate arrays");
 
-__device__ __forceinline__ float ex2f(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Two fp32 values as packed bf16 pairs hi + lo, both rounded to nearest (2^-18 off at most).
 __device__ __forceinline__ void split2_rn(float a, float b, uint32_t& hi, uint32_t& lo) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
