@@ -16,7 +16,9 @@ namespace osdn {
 
 constexpr int CONV_THREADS = 128;
 template <typename IO> constexpr int CONV_MAX_V = 4;  // channels of a thread
-constexpr int CONV_BWD_MAX_V = 4;
+constexpr int CONV_BWD_MAX_V = 2;  // (4 spills: 340M backward 62 us, 2: 40 us)
+// resident blocks of the forward kernel on an SM, by the bytes of a thread's access
+constexpr int conv_per_sm(int bytes) { return bytes == 16 ? 5 : 7; }
 constexpr int CONV_UNROLL = 4;  // tokens of a group; the next group's loads are in flight meanwhile
 
 // One row of a sequence at position pos (< 0: a row of the initial state) as fp32.
@@ -66,7 +68,7 @@ __device__ __forceinline__ void conv_weights(const float* __restrict__ weight,
 // write one sequence's final state each (the last W - 1 rows of [state0; x], oldest first) and
 // check its offsets.
 template <int V, int W, typename IO>
-__global__ void __launch_bounds__(CONV_THREADS, V * sizeof(IO) == 16 ? 5 : 8)
+__global__ void __launch_bounds__(CONV_THREADS, conv_per_sm(V * sizeof(IO)))
 conv_fwd_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
                 const float* __restrict__ bias, const IO* __restrict__ state0, int silu,
                 IO* __restrict__ y, IO* __restrict__ stateT, const int32_t* __restrict__ cu, int N,
@@ -171,11 +173,11 @@ conv_step_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
 // A block is 32 channel lanes (V channels each) x CONV_BWD_STRIPS strips at a time; its partial
 // dweight and dbias are summed over the strips it walks in registers, over its rows of threads
 // in shared memory, and over the blocks by conv_reduce_kernel, each in a fixed order.
-constexpr int CONV_BWD_STRIPS = 8;
+constexpr int CONV_BWD_STRIPS = 8, CONV_BWD_PER_SM = 3;
 constexpr int CONV_BWD_UNROLL = 4;  // tokens loaded before the first is used
 
 template <int V, int W, typename IO, typename GO>
-__global__ void __launch_bounds__(32 * CONV_BWD_STRIPS, 2)
+__global__ void __launch_bounds__(32 * CONV_BWD_STRIPS, CONV_BWD_PER_SM)
 conv_bwd_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
                 const float* __restrict__ bias, const IO* __restrict__ state0, int silu,
                 const GO* __restrict__ dy, const float* __restrict__ dstateT, IO* __restrict__ dx,

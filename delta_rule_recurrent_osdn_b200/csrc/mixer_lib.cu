@@ -78,6 +78,17 @@ template <int MAX, typename F> osdn_status_t conv_dispatch(int C, int W, F f) {
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Tokens of a strip, so that `per_sm` blocks on each of 148 SMs (a constant, so that the backward
+// workspace's size does not need a device), `gx` blocks side by side per strip, share the rows in
+// whole rounds: no round is left half empty.  At most `most` tokens, and 8 at least (a strip
+// re-reads the W - 1 tokens before it).
+int64_t conv_strip(int64_t rows, int64_t gx, int per_sm, int64_t most) {
+    const int64_t side = 148LL * per_sm / gx, lanes = side < 1 ? 1 : side;
+    const int64_t rounds = ceil_div(ceil_div(rows, lanes), most);
+    const int64_t strip = ceil_div(rows, lanes * (rounds < 1 ? 1 : rounds));
+    return strip < 8 ? 8 : strip;
+}
+
 template <typename IO>
 osdn_status_t launch_conv_fwd(const void* x, const float* weight, const float* bias,
                               const void* state0, int silu, void* y, void* stateT,
@@ -86,9 +97,7 @@ osdn_status_t launch_conv_fwd(const void* x, const float* weight, const float* b
     return conv_dispatch<CONV_MAX_V<IO>>(C, W, [&](auto v, auto w) -> osdn_status_t {
         constexpr int V = decltype(v)::value, WW = decltype(w)::value;
         const int64_t gx = ceil_div(C, (int64_t)V * CONV_THREADS);
-        // strips of as many tokens as still leave about 1024 threads for every SM
-        int64_t strip = rows * gx * CONV_THREADS / (1024LL * sm_count()) / CONV_UNROLL * CONV_UNROLL;
-        strip = strip < CONV_UNROLL ? CONV_UNROLL : strip > 64 ? 64 : strip;
+        int64_t strip = conv_strip(rows, gx, conv_per_sm(V * sizeof(IO)), 64);
         const int64_t least = ceil_div(rows, 32768);
         strip = strip < least ? least : strip;
         const int64_t strips = ceil_div(rows, strip);
@@ -123,14 +132,13 @@ osdn_status_t launch_conv_step(const void* x, const float* weight, const float* 
 struct ConvBwdPlan { int64_t gx; int strip, row_blocks; };
 ConvBwdPlan conv_bwd_plan(int64_t rows, int C) {
     ConvBwdPlan pl;
-    const int V = C % 4 == 0 ? 4 : C % 2 == 0 ? 2 : 1;  // as conv_dispatch picks it
-    const int sms = 148;  // a constant, so that the workspace's size does not need a device
+    int V = CONV_BWD_MAX_V;  // as conv_dispatch picks it
+    while (C % V != 0) V /= 2;
     pl.gx = ceil_div(C, 32 * V);
-    pl.strip = 64;
-    while (pl.strip > 8 && ceil_div(rows, CONV_BWD_STRIPS * pl.strip) * pl.gx < 4 * sms) pl.strip /= 2;
-    int64_t most = ceil_div(4 * sms, pl.gx);
-    int64_t rb = ceil_div(rows, CONV_BWD_STRIPS * pl.strip);
-    pl.row_blocks = (int)(rb < 1 ? 1 : rb > most ? most : rb);
+    pl.strip = (int)conv_strip(rows, pl.gx, CONV_BWD_PER_SM * CONV_BWD_STRIPS, 128);
+    const int64_t need = ceil_div(rows, CONV_BWD_STRIPS * pl.strip);
+    const int64_t side = 148LL * CONV_BWD_PER_SM / pl.gx, most = side < 1 ? 1 : side;
+    pl.row_blocks = (int)(need < 1 ? 1 : need > most ? most : need);
     return pl;
 }
 
