@@ -16,7 +16,7 @@ namespace osdn {
 
 constexpr int CONV_THREADS = 128;
 template <typename IO> constexpr int CONV_MAX_V = 4;  // channels of a thread
-constexpr int CONV_BWD_MAX_V = 2;  // (4 spills: 340M backward 62 us, 2: 40 us)
+constexpr int CONV_BWD_MAX_V = 4;
 // resident blocks of the forward kernel on an SM, by the bytes of a thread's access
 constexpr int conv_per_sm(int bytes) { return bytes == 16 ? 5 : 7; }
 constexpr int CONV_UNROLL = 4;  // tokens of a group; the next group's loads are in flight meanwhile
@@ -173,7 +173,7 @@ conv_step_kernel(const IO* __restrict__ x, const float* __restrict__ weight,
 // A block is 32 channel lanes (V channels each) x CONV_BWD_STRIPS strips at a time; its partial
 // dweight and dbias are summed over the strips it walks in registers, over its rows of threads
 // in shared memory, and over the blocks by conv_reduce_kernel, each in a fixed order.
-constexpr int CONV_BWD_STRIPS = 8, CONV_BWD_PER_SM = 3;
+constexpr int CONV_BWD_STRIPS = 4, CONV_BWD_PER_SM = 4;
 constexpr int CONV_BWD_UNROLL = 4;  // tokens loaded before the first is used
 
 template <int V, int W, typename IO, typename GO>

@@ -70,9 +70,12 @@ template <int V, typename IO> struct raw_io {
     static constexpr int WORDS = V * (int)sizeof(IO) / 4;
     uint32_t w[WORDS];
     __device__ __forceinline__ void load(const IO* p) {
-        if constexpr (WORDS == 4) {
-            const uint4 r = __ldg(reinterpret_cast<const uint4*>(p));
-            w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
+        if constexpr (WORDS >= 4) {
+#pragma unroll
+            for (int i = 0; i < WORDS; i += 4) {
+                const uint4 r = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+                w[i] = r.x; w[i + 1] = r.y; w[i + 2] = r.z; w[i + 3] = r.w;
+            }
         } else if constexpr (WORDS == 1) {
             w[0] = __ldg(reinterpret_cast<const unsigned int*>(p));
         } else {

@@ -172,26 +172,24 @@ osdn_status_t launch_conv_bwd(const void* x, const float* weight, const float* b
 template <typename F> osdn_status_t norm_dispatch(int D, F f) {
     const int need = (D + NORM_V - 1) / NORM_V;
     auto vec = [&](auto tpr) {
-        return D % NORM_V == 0 ? f(std::true_type{}, tpr) : f(std::false_type{}, tpr);
+        return D % 8 == 0 ? f(std::true_type{}, tpr) : f(std::false_type{}, tpr);
     };
+    if (need <= 4) return vec(std::integral_constant<int, 4>{});
     if (need <= 8) return vec(std::integral_constant<int, 8>{});
     if (need <= 16) return vec(std::integral_constant<int, 16>{});
     if (need <= 32) return vec(std::integral_constant<int, 32>{});
     if (need <= 64) return vec(std::integral_constant<int, 64>{});
     if (need <= 128) return vec(std::integral_constant<int, 128>{});
     if (need <= 256) return vec(std::integral_constant<int, 256>{});
-    if (need <= 512) return vec(std::integral_constant<int, 512>{});
-    return vec(std::integral_constant<int, 1024>{});
+    return vec(std::integral_constant<int, 512>{});
 }
 
-// Blocks of the backward pass (each leaves one partial row of dw_post and dw_next): 1024 threads
+// Blocks of the backward pass (each leaves one partial row of dw_post and dw_next): 512 threads
 // for every SM, or one block per set of rows.
 int64_t norm_bwd_blocks(int64_t R, int D) {
-    const int need = (D + NORM_V - 1) / NORM_V;
-    int tpr = 8;
-    while (tpr < need) tpr *= 2;
-    const int rows = tpr > 32 ? 1 : 128 / tpr, threads = tpr > 32 ? tpr : 128;
-    const int64_t most = 148LL * (1024 / threads), have = ceil_div(R, rows);
+    int tpr = 4;
+    while (tpr * NORM_V < D) tpr *= 2;
+    const int64_t most = 148LL * (512 / norm_threads(tpr)), have = ceil_div(R, norm_rows(tpr));
     return have < most ? have : most;
 }
 
@@ -687,10 +685,10 @@ osdn_status_t osdn_norm_fwd(const void* f, const void* x, const void* gate, cons
         using IO = decltype(zero);
         return norm_dispatch(D, [&](auto vec, auto tpr) {
             constexpr int TPR = decltype(tpr)::value;
-            constexpr int ROWS = TPR > 32 ? 1 : 128 / TPR, THREADS = TPR > 32 ? TPR : 128;
-            const int64_t need = ceil_div(R, ROWS), cap = 64LL * sm_count();
+            // 512 threads an SM that walk the rows with the next one's loads in flight
+            const int64_t need = ceil_div(R, norm_rows(TPR)), cap = (int64_t)(512 / norm_threads(TPR)) * sm_count();
             norm_fwd_kernel<decltype(vec)::value, TPR, IO>
-                <<<dim3((unsigned)(need < cap ? need : cap)), dim3(THREADS), 0, s>>>(
+                <<<dim3((unsigned)(need < cap ? need : cap)), dim3(norm_threads(TPR)), 0, s>>>(
                     static_cast<const IO*>(f), static_cast<const IO*>(x),
                     static_cast<const IO*>(gate), w_post, w_next, gate_act, gate_first, scale, eps,
                     static_cast<IO*>(x_out), static_cast<IO*>(h), R, D);
@@ -738,7 +736,7 @@ osdn_status_t osdn_norm_bwd(const void* f, const void* x, const void* gate, cons
             return norm_dispatch(D, [&](auto vec, auto tpr) {
                 constexpr int TPR = decltype(tpr)::value;
                 norm_bwd_kernel<decltype(vec)::value, TPR, IO>
-                    <<<dim3((unsigned)blocks), dim3(TPR > 32 ? TPR : 128), 0, s>>>(
+                    <<<dim3((unsigned)blocks), dim3(norm_threads(TPR)), 0, s>>>(
                         static_cast<const IO*>(f), static_cast<const IO*>(x),
                         static_cast<const IO*>(gate), w_post, w_next, gate_act, gate_first, scale,
                         eps, static_cast<const IO*>(dx_out), static_cast<const IO*>(dh),

@@ -8,131 +8,189 @@
 // and its gradients, which recompute all of this from the inputs.  With n = v / rms(v), the norm
 // n * w has d v = (dn - n * mean(dn * n)) / rms(v), dn = dout * w, and dw = sum over rows dout * n.
 //
-// A few operations per element: bound by HBM, each input read and each output written once.  A
-// row is held in the registers of TPR threads, 8 values each, so one pass suffices; sums over a
-// row go by shuffles, and through shared memory when a row takes several warps.
+// Some 20 operations per element and two to four sums over the row: bound by HBM if those stay
+// cheap, so a row is held in the registers of TPR threads, 16 values each, sums go by shuffles
+// (and through shared memory when a row takes several warps), and the next row's loads are in
+// flight while one is worked on.  (8 values a thread spent as much on the sums as on the rest:
+// 16384 rows of 2048, everything on: 98 us forward, 259 us backward.)
 #pragma once
 
 #include "mixer_common.cuh"
 
 namespace osdn {
 
-constexpr int NORM_V = 8;             // values per thread
-constexpr int NORM_MAX_D = 1024 * NORM_V;
+constexpr int NORM_V = 16;            // values per thread
+constexpr int NORM_MAX_D = 512 * NORM_V;
 
 enum { NORM_ACT_SILU = 0, NORM_ACT_SIGMOID = 1 };
 
-__device__ __forceinline__ float norm_act(float g, int act) {
-    return act == NORM_ACT_SILU ? silu_f(g) : sigmoid_f(g);
-}
-__device__ __forceinline__ float norm_act_grad(float g, int act) {
-    if (act == NORM_ACT_SILU) return silu_grad_f(g);
-    const float s = sigmoid_f(g);
-    return s * (1.f - s);
-}
-
-// The 8 values of a row that lane `i` of its TPR threads holds: 8 neighbours when VEC (D a
-// multiple of 8 and the rows 16-byte aligned), else every TPR-th, so that a warp's accesses stay
-// together in either case.
-template <bool VEC, int TPR, typename IO>
-__device__ __forceinline__ void norm_load(const IO* __restrict__ p, int i, int D, float* x) {
-    if constexpr (VEC) {
-        if (i * NORM_V < D) {
-            vec_io<NORM_V, IO>::load(p + i * NORM_V, x);
-            return;
-        }
+// The 16 values of a row that lane `i` of its TPR threads holds: twice 8 neighbours, TPR * 8
+// apart, when VEC (D a multiple of 8: the rows are 16-byte aligned), else every TPR-th; a warp's
+// accesses stay together in either case.  Values past D are 0.
+template <bool VEC, int TPR, typename IO> struct norm_row {
+    raw_io<8, IO> r[2];
+    __device__ __forceinline__ void load(const IO* __restrict__ p, int i, int D) {
 #pragma unroll
-        for (int e = 0; e < NORM_V; ++e) x[e] = 0.f;
-    } else {
+        for (int k = 0; k < 2; ++k) {
+            const int c = (k * TPR + i) * 8;
+            if (c < D) {
+                r[k].load(p + c);
+            } else {
+#pragma unroll
+                for (int e = 0; e < raw_io<8, IO>::WORDS; ++e) r[k].w[e] = 0;
+            }
+        }
+    }
+    __device__ __forceinline__ void to(float* x) const {
+        r[0].to(x);
+        r[1].to(x + 8);
+    }
+    static __device__ __forceinline__ void store(IO* __restrict__ p, int i, int D, const float* x) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c = (k * TPR + i) * 8;
+            if (c < D) vec_io<8, IO>::store(p + c, x + 8 * k);
+        }
+    }
+};
+template <int TPR, typename IO> struct norm_row<false, TPR, IO> {
+    IO v[NORM_V];
+    __device__ __forceinline__ void load(const IO* __restrict__ p, int i, int D) {
 #pragma unroll
         for (int e = 0; e < NORM_V; ++e)
-            x[e] = e * TPR + i < D ? io_traits<IO>::to_f32(p[e * TPR + i]) : 0.f;
+            v[e] = e * TPR + i < D ? p[e * TPR + i] : io_traits<IO>::from_f32(0.f);
     }
-}
-template <bool VEC, int TPR, typename IO>
-__device__ __forceinline__ void norm_store(IO* __restrict__ p, int i, int D, const float* x) {
-    if constexpr (VEC) {
-        if (i * NORM_V < D) vec_io<NORM_V, IO>::store(p + i * NORM_V, x);
-    } else {
+    __device__ __forceinline__ void to(float* x) const {
+#pragma unroll
+        for (int e = 0; e < NORM_V; ++e) x[e] = io_traits<IO>::to_f32(v[e]);
+    }
+    static __device__ __forceinline__ void store(IO* __restrict__ p, int i, int D, const float* x) {
 #pragma unroll
         for (int e = 0; e < NORM_V; ++e)
             if (e * TPR + i < D) p[e * TPR + i] = io_traits<IO>::from_f32(x[e]);
     }
-}
+};
 
-// Sum over the TPR threads of a row.  `red` holds 2 x 32 floats per row slot and alternates by
-// `flip`, so one barrier per sum suffices.
+// Sum over the TPR threads of a row.  `red` holds 2 x 32 floats and alternates by `flip`, so one
+// barrier per sum suffices.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float s, float* red, int& flip) {
     constexpr int W = TPR < 32 ? TPR : 32;
 #pragma unroll
     for (int off = W / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    if constexpr (TPR > 32) {
-        const int warp = threadIdx.x >> 5;                 // one row per block then
+    if constexpr (TPR > 32) {  // one row per block then
         float* r = red + 32 * flip;
-        if ((threadIdx.x & 31) == 0) r[warp] = s;
+        if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = s;
         __syncthreads();
-        s = (threadIdx.x & 31) < TPR / 32 ? r[threadIdx.x & 31] : 0.f;
+        s = r[0];
 #pragma unroll
-        for (int off = TPR / 64; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s = __shfl_sync(0xffffffffu, s, 0);
+        for (int k = 1; k < TPR / 32; ++k) s += r[k];
         flip ^= 1;
     }
     return s;
 }
 
+// sum of a[e] * b[e], two at a time
+__device__ __forceinline__ float norm_dot(const float* a, const float* b) {
+    float2 s = make_float2(0.f, 0.f), t = s;
+#pragma unroll
+    for (int e = 0; e < NORM_V; e += 4) {
+        s = __ffma2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]), s);
+        t = __ffma2_rn(make_float2(a[e + 2], a[e + 3]), make_float2(b[e + 2], b[e + 3]), t);
+    }
+    return (s.x + s.y) + (t.x + t.y);
+}
+// x[e] = a[e] * b[e] (* k), two at a time
+__device__ __forceinline__ void norm_mul(float* x, const float* a, const float* b, float k) {
+#pragma unroll
+    for (int e = 0; e < NORM_V; e += 2) {
+        const float2 t = __fmul2_rn(__fmul2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1])),
+                                    make_float2(k, k));
+        x[e] = t.x;
+        x[e + 1] = t.y;
+    }
+}
+// x[e] = k * a[e] + b[e]
+__device__ __forceinline__ void norm_axpy(float* x, float k, const float* a, const float* b) {
+#pragma unroll
+    for (int e = 0; e < NORM_V; e += 2) {
+        const float2 t = __ffma2_rn(make_float2(k, k), make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
+        x[e] = t.x;
+        x[e + 1] = t.y;
+    }
+}
+__device__ __forceinline__ void norm_scale(float* x, float k) {
+#pragma unroll
+    for (int e = 0; e < NORM_V; e += 2) {
+        const float2 t = __fmul2_rn(make_float2(k, k), make_float2(x[e], x[e + 1]));
+        x[e] = t.x;
+        x[e + 1] = t.y;
+    }
+}
+
+constexpr int norm_threads(int TPR) { return TPR > 32 ? TPR : 128; }
+constexpr int norm_rows(int TPR) { return TPR > 32 ? 1 : 128 / TPR; }
+
 template <bool VEC, int TPR, typename IO>
-__global__ void __launch_bounds__(TPR > 32 ? TPR : 128)
+__global__ void __launch_bounds__(norm_threads(TPR))
 norm_fwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __restrict__ gate,
                 const float* __restrict__ w_post, const float* __restrict__ w_next, int act,
                 int gate_first, float scale, float eps, IO* __restrict__ x_out,
                 IO* __restrict__ h, int64_t R, int D) {
-    constexpr int ROWS = TPR > 32 ? 1 : 128 / TPR;
+    using row_t = norm_row<VEC, TPR, IO>;
+    using wrow_t = norm_row<VEC, TPR, float>;
+    constexpr int ROWS = norm_rows(TPR);
     __shared__ float red[64];
     int flip = 0;
     const int i = threadIdx.x % TPR;
-    float wp[NORM_V], wn[NORM_V];
-    if (w_post) norm_load<VEC, TPR, float>(w_post, i, D, wp);
-    if (w_next) norm_load<VEC, TPR, float>(w_next, i, D, wn);
     const float inv_d = 1.f / (float)D;
-    for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < R; r0 += (int64_t)gridDim.x * ROWS) {
-        const int64_t row = r0 + threadIdx.x / TPR;
+    row_t rf, rg, rx;
+    auto fetch = [&](int64_t r0) {
+        int64_t row = r0 + threadIdx.x / TPR;
+        row = row < R ? row : R - 1;  // a row that is not there repeats the last
+        rf.load(f + row * D, i, D);
+        if (gate) rg.load(gate + row * D, i, D);
+        if (x) rx.load(x + row * D, i, D);
+    };
+    const int64_t hop = (int64_t)gridDim.x * ROWS;
+    int64_t r0 = (int64_t)blockIdx.x * ROWS;
+    if (r0 < R) fetch(r0);
+    for (; r0 < R; r0 += hop) {
+        const int64_t row = r0 + threadIdx.x / TPR, at = row * D;
         const bool live = row < R;
-        const int64_t at = (live ? row : R - 1) * D;  // a row that is not there repeats the last
         float u[NORM_V], a[NORM_V], xr[NORM_V];
-        norm_load<VEC, TPR, IO>(f + at, i, D, u);
-        if (gate) norm_load<VEC, TPR, IO>(gate + at, i, D, a);
-        if (x) norm_load<VEC, TPR, IO>(x + at, i, D, xr);
+        rf.to(u);
         if (gate) {
+            rg.to(a);
 #pragma unroll
             for (int e = 0; e < NORM_V; ++e) {
-                a[e] = norm_act(a[e], act);
-                if (gate_first) u[e] *= a[e];
+                const float s = sigmoid_f(a[e]);
+                a[e] = act == NORM_ACT_SILU ? a[e] * s : s;
             }
         }
+        if (x) rx.to(xr);
+        if (r0 + hop < R) fetch(r0 + hop);
+        if (gate && gate_first) norm_mul(u, u, a, 1.f);
         if (w_post) {
-            float s = 0.f;
-#pragma unroll
-            for (int e = 0; e < NORM_V; ++e) s = fmaf(u[e], u[e], s);
-            const float rs = rsqrtf(fmaf(row_sum<TPR>(s, red, flip), inv_d, eps));
-#pragma unroll
-            for (int e = 0; e < NORM_V; ++e) u[e] *= rs * wp[e];
+            const float rs = rsqrtf(fmaf(row_sum<TPR>(norm_dot(u, u), red, flip), inv_d, eps));
+            wrow_t w;
+            float wf[NORM_V];
+            w.load(w_post, i, D);
+            w.to(wf);
+            norm_mul(u, u, wf, rs);
         }
-#pragma unroll
-        for (int e = 0; e < NORM_V; ++e) {
-            if (gate && !gate_first) u[e] *= a[e];
-            u[e] = x ? fmaf(scale, u[e], xr[e]) : scale * u[e];
-        }
-        if (x_out && live && OSDN_IN_BOUNDS(row, R)) norm_store<VEC, TPR, IO>(x_out + at, i, D, u);
+        if (gate && !gate_first) norm_mul(u, u, a, 1.f);
+        if (x) norm_axpy(u, scale, u, xr);
+        else norm_scale(u, scale);
+        if (x_out && live && OSDN_IN_BOUNDS(row, R)) row_t::store(x_out + at, i, D, u);
         if (w_next) {
-            float s = 0.f;
-#pragma unroll
-            for (int e = 0; e < NORM_V; ++e)
-                if (VEC ? i * NORM_V < D : e * TPR + i < D) s = fmaf(u[e], u[e], s);
-            const float rs = rsqrtf(fmaf(row_sum<TPR>(s, red, flip), inv_d, eps));
-#pragma unroll
-            for (int e = 0; e < NORM_V; ++e) u[e] *= rs * wn[e];
-            if (live && OSDN_IN_BOUNDS(row, R)) norm_store<VEC, TPR, IO>(h + at, i, D, u);
+            const float rs = rsqrtf(fmaf(row_sum<TPR>(norm_dot(u, u), red, flip), inv_d, eps));
+            wrow_t w;
+            float wf[NORM_V];
+            w.load(w_next, i, D);
+            w.to(wf);
+            norm_mul(u, u, wf, rs);
+            if (live && OSDN_IN_BOUNDS(row, R)) row_t::store(h + at, i, D, u);
         }
     }
 }
@@ -141,110 +199,130 @@ norm_fwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __
 // in registers, adds its row slots' in shared memory and writes one partial row per weight to
 // `part` ([2][gridDim.x][D]); norm_reduce_kernel adds the blocks in a fixed order.
 template <bool VEC, int TPR, typename IO>
-__global__ void __launch_bounds__(TPR > 32 ? TPR : 128)
+__global__ void __launch_bounds__(norm_threads(TPR))
 norm_bwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __restrict__ gate,
                 const float* __restrict__ w_post, const float* __restrict__ w_next, int act,
                 int gate_first, float scale, float eps, const IO* __restrict__ dx_out,
                 const IO* __restrict__ dh, IO* __restrict__ df, IO* __restrict__ dx,
                 IO* __restrict__ dgate, float* __restrict__ part, int64_t R, int D) {
-    constexpr int ROWS = TPR > 32 ? 1 : 128 / TPR;
-    __shared__ float red[TPR > 32 ? 64 : ROWS * TPR * NORM_V];
+    using row_t = norm_row<VEC, TPR, IO>;
+    using wrow_t = norm_row<VEC, TPR, float>;
+    constexpr int ROWS = norm_rows(TPR);
+    __shared__ float red[TPR > 32 ? 64 : norm_threads(TPR) * NORM_V];
     int flip = 0;
     const int i = threadIdx.x % TPR;
     float dwp[NORM_V], dwn[NORM_V];
 #pragma unroll
     for (int e = 0; e < NORM_V; ++e) dwp[e] = dwn[e] = 0.f;
     const float inv_d = 1.f / (float)D;
-    for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < R; r0 += (int64_t)gridDim.x * ROWS) {
+    const int64_t hop = (int64_t)gridDim.x * ROWS;
+    for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < R; r0 += hop) {
         const int64_t row = r0 + threadIdx.x / TPR;
         const bool live = row < R;
-        const int64_t at = (live ? row : R - 1) * D;
-        float v[NORM_V], a[NORM_V], d[NORM_V], w[NORM_V], xo[NORM_V];
-        norm_load<VEC, TPR, IO>(f + at, i, D, v);
-        if (gate) norm_load<VEC, TPR, IO>(gate + at, i, D, a);
-        if (x) norm_load<VEC, TPR, IO>(x + at, i, D, xo);
+        const int64_t at = (live ? row : R - 1) * D;  // a row that is not there repeats the last
+        row_t rf, rg, rx, rd, rh;
+        rf.load(f + at, i, D);
+        if (gate) rg.load(gate + at, i, D);
+        if (x && w_next) rx.load(x + at, i, D);  // x' matters to the second norm alone
+        if (dx_out) rd.load(dx_out + at, i, D);
+        if (w_next) rh.load(dh + at, i, D);
+        float v[NORM_V], s[NORM_V], d[NORM_V], w[NORM_V];  // s: sigmoid of the gate
+        rf.to(v);
+        if (gate) {
+            rg.to(s);
+#pragma unroll
+            for (int e = 0; e < NORM_V; ++e) s[e] = sigmoid_f(s[e]);
+        }
+        // the gate's factor of element e
+        auto factor = [&](const float* g, int e) { return act == NORM_ACT_SILU ? g[e] * s[e] : s[e]; };
+        float rs = 1.f;
+        if (gate && gate_first) {
+            float g[NORM_V];
+            rg.to(g);
+#pragma unroll
+            for (int e = 0; e < NORM_V; ++e) v[e] *= factor(g, e);
+        }
+        if (w_post) {
+            rs = rsqrtf(fmaf(row_sum<TPR>(norm_dot(v, v), red, flip), inv_d, eps));
+            wrow_t wr;
+            wr.load(w_post, i, D);
+            wr.to(w);
+            norm_scale(v, rs);  // the norm's output before its weight
+        }
         if (dx_out) {
-            norm_load<VEC, TPR, IO>(dx_out + at, i, D, d);
+            rd.to(d);
         } else {
 #pragma unroll
             for (int e = 0; e < NORM_V; ++e) d[e] = 0.f;
         }
-        // forward: v = the norm's input, rs its 1 / rms, u = the branch before scale
-        float rs = 1.f;
-        if (gate && gate_first) {
-#pragma unroll
-            for (int e = 0; e < NORM_V; ++e) v[e] *= norm_act(a[e], act);
-        }
-        if (w_post) {
-            float s = 0.f;
-#pragma unroll
-            for (int e = 0; e < NORM_V; ++e) s = fmaf(v[e], v[e], s);
-            rs = rsqrtf(fmaf(row_sum<TPR>(s, red, flip), inv_d, eps));
-            norm_load<VEC, TPR, float>(w_post, i, D, w);
-        } else {
-#pragma unroll
-            for (int e = 0; e < NORM_V; ++e) w[e] = 1.f;
-        }
         if (w_next) {
-            float g[NORM_V], s = 0.f;
-            norm_load<VEC, TPR, IO>(dh + at, i, D, g);
-#pragma unroll
-            for (int e = 0; e < NORM_V; ++e) {
-                float u = v[e] * rs * w[e];
-                if (gate && !gate_first) u *= norm_act(a[e], act);
-                u = x ? fmaf(scale, u, xo[e]) : scale * u;
-                xo[e] = u;
-                if (VEC ? i * NORM_V < D : e * TPR + i < D) s = fmaf(u, u, s);
-            }
-            const float rn = rsqrtf(fmaf(row_sum<TPR>(s, red, flip), inv_d, eps));
-            float wn[NORM_V], dot = 0.f;
-            norm_load<VEC, TPR, float>(w_next, i, D, wn);
-#pragma unroll
-            for (int e = 0; e < NORM_V; ++e) {
-                xo[e] *= rn;                                   // n
-                if (live) dwn[e] = fmaf(g[e], xo[e], dwn[e]);
-                g[e] *= wn[e];                                 // dn
-                if (VEC ? i * NORM_V < D : e * TPR + i < D) dot = fmaf(g[e], xo[e], dot);
-            }
-            dot = row_sum<TPR>(dot, red, flip) * inv_d;
-#pragma unroll
-            for (int e = 0; e < NORM_V; ++e) d[e] += rn * (g[e] - xo[e] * dot);
-        }
-        if (dx && live && OSDN_IN_BOUNDS(row, R)) norm_store<VEC, TPR, IO>(dx + at, i, D, d);
-        float dg[NORM_V];
-#pragma unroll
-        for (int e = 0; e < NORM_V; ++e) {
-            d[e] *= scale;
+            float n[NORM_V], g[NORM_V];
+            if (w_post) norm_mul(n, v, w, scale);
+            else norm_axpy(n, scale - 1.f, v, v);
             if (gate && !gate_first) {
-                dg[e] = d[e] * (v[e] * rs * w[e]) * norm_act_grad(a[e], act);
-                d[e] *= norm_act(a[e], act);
+                rg.to(g);
+#pragma unroll
+                for (int e = 0; e < NORM_V; ++e) n[e] *= factor(g, e);
+            }
+            if (x) {
+                rx.to(g);
+                norm_axpy(n, 1.f, n, g);
+            }
+            const float rn = rsqrtf(fmaf(row_sum<TPR>(norm_dot(n, n), red, flip), inv_d, eps));
+            norm_scale(n, rn);
+            rh.to(g);
+            if (live) {
+#pragma unroll
+                for (int e = 0; e < NORM_V; ++e) dwn[e] = fmaf(g[e], n[e], dwn[e]);
+            }
+            wrow_t wr;
+            float wn[NORM_V];
+            wr.load(w_next, i, D);
+            wr.to(wn);
+            norm_mul(g, g, wn, 1.f);
+            const float dot = row_sum<TPR>(norm_dot(g, n), red, flip) * inv_d;
+            norm_axpy(g, -dot, n, g);
+            norm_axpy(d, rn, g, d);
+        }
+        if (dx && live && OSDN_IN_BOUNDS(row, R)) row_t::store(dx + at, i, D, d);
+        norm_scale(d, scale);
+        // d of the gate: d * (what it multiplies) * act'; act' = s (1 + g (1 - s)) or s (1 - s)
+        auto gate_grad = [&](const float* m) {
+            float g[NORM_V], dg[NORM_V];
+            rg.to(g);
+#pragma unroll
+            for (int e = 0; e < NORM_V; ++e) {
+                const float one = 1.f - s[e];
+                const float ds = act == NORM_ACT_SILU ? s[e] * fmaf(g[e], one, 1.f) : s[e] * one;
+                dg[e] = d[e] * m[e] * ds;
+                d[e] *= factor(g, e);
+            }
+            if (live && OSDN_IN_BOUNDS(row, R)) row_t::store(dgate + at, i, D, dg);
+        };
+        if (gate && !gate_first) {
+            if (w_post) {
+                float m[NORM_V];
+                norm_mul(m, v, w, 1.f);
+                gate_grad(m);
+            } else {
+                gate_grad(v);
             }
         }
         if (w_post) {
-            float dot = 0.f;
+            if (live) {
 #pragma unroll
-            for (int e = 0; e < NORM_V; ++e) {
-                v[e] *= rs;                                    // n
-                if (live) dwp[e] = fmaf(d[e], v[e], dwp[e]);
-                d[e] *= w[e];                                  // dn
-                if (VEC ? i * NORM_V < D : e * TPR + i < D) dot = fmaf(d[e], v[e], dot);
+                for (int e = 0; e < NORM_V; ++e) dwp[e] = fmaf(d[e], v[e], dwp[e]);
             }
-            dot = row_sum<TPR>(dot, red, flip) * inv_d;
-#pragma unroll
-            for (int e = 0; e < NORM_V; ++e) d[e] = rs * (d[e] - v[e] * dot);
+            norm_mul(d, d, w, 1.f);
+            const float dot = row_sum<TPR>(norm_dot(d, v), red, flip) * inv_d;
+            norm_axpy(d, -dot, v, d);
+            norm_scale(d, rs);
         }
         if (gate && gate_first) {
-            norm_load<VEC, TPR, IO>(f + at, i, D, v);
-#pragma unroll
-            for (int e = 0; e < NORM_V; ++e) {
-                dg[e] = d[e] * v[e] * norm_act_grad(a[e], act);
-                d[e] *= norm_act(a[e], act);
-            }
+            rf.to(v);
+            gate_grad(v);
         }
-        if (live && OSDN_IN_BOUNDS(row, R)) {
-            norm_store<VEC, TPR, IO>(df + at, i, D, d);
-            if (gate) norm_store<VEC, TPR, IO>(dgate + at, i, D, dg);
-        }
+        if (live && OSDN_IN_BOUNDS(row, R)) row_t::store(df + at, i, D, d);
     }
     // one partial row per weight and block
 #pragma unroll
@@ -263,10 +341,10 @@ norm_bwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __
                     dw[e] = 0.f;
                     for (int q = 0; q < ROWS; ++q) dw[e] += red[(q * TPR + i) * NORM_V + e];
                 }
-                norm_store<VEC, TPR, float>(out, i, D, dw);
+                wrow_t::store(out, i, D, dw);
             }
         } else {
-            norm_store<VEC, TPR, float>(out, i, D, dw);
+            wrow_t::store(out, i, D, dw);
         }
     }
 }
