@@ -167,29 +167,22 @@ osdn_status_t launch_conv_bwd(const void* x, const float* weight, const float* b
 }
 
 // ---------------------------------------------------------------- block norm
-// Runs f(constant VEC, constant TPR) for rows of D values: TPR threads of NORM_V values each,
-// the smallest power of two that holds a row.
-template <typename F> osdn_status_t norm_dispatch(int D, F f) {
-    const int need = (D + NORM_V - 1) / NORM_V;
-    auto vec = [&](auto tpr) {
-        return D % 8 == 0 ? f(std::true_type{}, tpr) : f(std::false_type{}, tpr);
-    };
-    if (need <= 4) return vec(std::integral_constant<int, 4>{});
-    if (need <= 8) return vec(std::integral_constant<int, 8>{});
-    if (need <= 16) return vec(std::integral_constant<int, 16>{});
-    if (need <= 32) return vec(std::integral_constant<int, 32>{});
-    if (need <= 64) return vec(std::integral_constant<int, 64>{});
-    if (need <= 128) return vec(std::integral_constant<int, 128>{});
-    if (need <= 256) return vec(std::integral_constant<int, 256>{});
-    return vec(std::integral_constant<int, 512>{});
+// Runs f(constant VEC, constant TPR) for rows of D values: TPR threads of V values each, the
+// smallest power of two that holds a row.
+template <int V, int TPR = 4, typename F> osdn_status_t norm_dispatch(int D, F f) {
+    using tpr = std::integral_constant<int, TPR>;
+    if constexpr (TPR * V < NORM_MAX_D)
+        if (D > TPR * V) return norm_dispatch<V, 2 * TPR>(D, f);
+    return D % 8 == 0 ? f(std::true_type{}, tpr{}) : f(std::false_type{}, tpr{});
 }
 
-// Blocks of the backward pass (each leaves one partial row of dw_post and dw_next): 512 threads
-// for every SM, or one block per set of rows.
-int64_t norm_bwd_blocks(int64_t R, int D) {
+// Blocks of the backward pass (each leaves one partial row of dw_post and dw_next): as many as
+// are resident on 148 SMs (a constant, so that the workspace's size does not need a device), or
+// one per set of rows.
+int64_t norm_bwd_blocks(int64_t R, int D, bool next) {
     int tpr = 4;
-    while (tpr * NORM_V < D) tpr *= 2;
-    const int64_t most = 148LL * (512 / norm_threads(tpr)), have = ceil_div(R, norm_rows(tpr));
+    while (tpr * NORM_BWD_V < D) tpr *= 2;
+    const int64_t most = 148LL * norm_bwd_per_sm(tpr, next), have = ceil_div(R, norm_rows(tpr));
     return have < most ? have : most;
 }
 
@@ -683,7 +676,7 @@ osdn_status_t osdn_norm_fwd(const void* f, const void* x, const void* gate, cons
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto go = [&](auto zero) {
         using IO = decltype(zero);
-        return norm_dispatch(D, [&](auto vec, auto tpr) {
+        return norm_dispatch<NORM_FWD_V>(D, [&](auto vec, auto tpr) {
             constexpr int TPR = decltype(tpr)::value;
             // 512 threads an SM that walk the rows with the next one's loads in flight
             const int64_t need = ceil_div(R, norm_rows(TPR)), cap = (int64_t)(512 / norm_threads(TPR)) * sm_count();
@@ -700,7 +693,7 @@ osdn_status_t osdn_norm_fwd(const void* f, const void* x, const void* gate, cons
 
 size_t osdn_norm_bwd_workspace_bytes(int64_t R, int32_t D) {
     if (R < 0 || D < 1 || D > NORM_MAX_D) return 0;
-    return up256((size_t)2 * norm_bwd_blocks(R, D) * D * 4);
+    return up256((size_t)2 * norm_bwd_blocks(R, D, false) * D * 4);  // the larger of the two
 }
 
 osdn_status_t osdn_norm_bwd(const void* f, const void* x, const void* gate, const float* w_post,
@@ -729,19 +722,19 @@ osdn_status_t osdn_norm_bwd(const void* f, const void* x, const void* gate, cons
     if (st != OSDN_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     float* part = static_cast<float*>(workspace);
-    const int64_t blocks = norm_bwd_blocks(R, D);
+    const int64_t blocks = norm_bwd_blocks(R, D, w_next != nullptr);
     if (blocks > 0) {
         auto go = [&](auto zero) {
             using IO = decltype(zero);
-            return norm_dispatch(D, [&](auto vec, auto tpr) {
+            return norm_dispatch<NORM_BWD_V>(D, [&](auto vec, auto tpr) {
                 constexpr int TPR = decltype(tpr)::value;
-                norm_bwd_kernel<decltype(vec)::value, TPR, IO>
-                    <<<dim3((unsigned)blocks), dim3(norm_threads(TPR)), 0, s>>>(
-                        static_cast<const IO*>(f), static_cast<const IO*>(x),
-                        static_cast<const IO*>(gate), w_post, w_next, gate_act, gate_first, scale,
-                        eps, static_cast<const IO*>(dx_out), static_cast<const IO*>(dh),
-                        static_cast<IO*>(df), static_cast<IO*>(dx), static_cast<IO*>(dgate), part, R,
-                        D);
+                auto kern = w_next ? norm_bwd_kernel<decltype(vec)::value, TPR, true, IO>
+                                   : norm_bwd_kernel<decltype(vec)::value, TPR, false, IO>;
+                kern<<<dim3((unsigned)blocks), dim3(norm_threads(TPR)), 0, s>>>(
+                    static_cast<const IO*>(f), static_cast<const IO*>(x), static_cast<const IO*>(gate),
+                    w_post, w_next, gate_act, gate_first, scale, eps, static_cast<const IO*>(dx_out),
+                    static_cast<const IO*>(dh), static_cast<IO*>(df), static_cast<IO*>(dx),
+                    static_cast<IO*>(dgate), part, R, D);
                 return launch_status();
             });
         };

@@ -9,29 +9,28 @@
 // n * w has d v = (dn - n * mean(dn * n)) / rms(v), dn = dout * w, and dw = sum over rows dout * n.
 //
 // Some 20 operations per element and two to four sums over the row: bound by HBM if those stay
-// cheap, so a row is held in the registers of TPR threads, 16 values each, sums go by shuffles
-// (and through shared memory when a row takes several warps), and the next row's loads are in
-// flight while one is worked on.  (8 values a thread spent as much on the sums as on the rest:
-// 16384 rows of 2048, everything on: 98 us forward, 259 us backward.)
+// cheap, so a row is held in the registers of TPR threads, sums go by shuffles (and through shared
+// memory when a row takes several warps), and the forward pass has the next row's loads in flight
+// while it works on one.
 #pragma once
 
 #include "mixer_common.cuh"
 
 namespace osdn {
 
-constexpr int NORM_V = 16;            // values per thread
-constexpr int NORM_MAX_D = 512 * NORM_V;
+constexpr int NORM_FWD_V = 16, NORM_BWD_V = 8;  // values per thread (backward: registers)
+constexpr int NORM_MAX_D = 8192;
 
 enum { NORM_ACT_SILU = 0, NORM_ACT_SIGMOID = 1 };
 
-// The 16 values of a row that lane `i` of its TPR threads holds: twice 8 neighbours, TPR * 8
+// The V values of a row that lane `i` of its TPR threads holds: V / 8 times 8 neighbours, TPR * 8
 // apart, when VEC (D a multiple of 8: the rows are 16-byte aligned), else every TPR-th; a warp's
 // accesses stay together in either case.  Values past D are 0.
-template <bool VEC, int TPR, typename IO> struct norm_row {
-    raw_io<8, IO> r[2];
+template <bool VEC, int TPR, int V, typename IO> struct norm_row {
+    raw_io<8, IO> r[V / 8];
     __device__ __forceinline__ void load(const IO* __restrict__ p, int i, int D) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < V / 8; ++k) {
             const int c = (k * TPR + i) * 8;
             if (c < D) {
                 r[k].load(p + c);
@@ -42,31 +41,31 @@ template <bool VEC, int TPR, typename IO> struct norm_row {
         }
     }
     __device__ __forceinline__ void to(float* x) const {
-        r[0].to(x);
-        r[1].to(x + 8);
+#pragma unroll
+        for (int k = 0; k < V / 8; ++k) r[k].to(x + 8 * k);
     }
     static __device__ __forceinline__ void store(IO* __restrict__ p, int i, int D, const float* x) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < V / 8; ++k) {
             const int c = (k * TPR + i) * 8;
             if (c < D) vec_io<8, IO>::store(p + c, x + 8 * k);
         }
     }
 };
-template <int TPR, typename IO> struct norm_row<false, TPR, IO> {
-    IO v[NORM_V];
+template <int TPR, int V, typename IO> struct norm_row<false, TPR, V, IO> {
+    IO v[V];
     __device__ __forceinline__ void load(const IO* __restrict__ p, int i, int D) {
 #pragma unroll
-        for (int e = 0; e < NORM_V; ++e)
+        for (int e = 0; e < V; ++e)
             v[e] = e * TPR + i < D ? p[e * TPR + i] : io_traits<IO>::from_f32(0.f);
     }
     __device__ __forceinline__ void to(float* x) const {
 #pragma unroll
-        for (int e = 0; e < NORM_V; ++e) x[e] = io_traits<IO>::to_f32(v[e]);
+        for (int e = 0; e < V; ++e) x[e] = io_traits<IO>::to_f32(v[e]);
     }
     static __device__ __forceinline__ void store(IO* __restrict__ p, int i, int D, const float* x) {
 #pragma unroll
-        for (int e = 0; e < NORM_V; ++e)
+        for (int e = 0; e < V; ++e)
             if (e * TPR + i < D) p[e * TPR + i] = io_traits<IO>::from_f32(x[e]);
     }
 };
@@ -91,19 +90,19 @@ __device__ __forceinline__ float row_sum(float s, float* red, int& flip) {
 }
 
 // sum of a[e] * b[e], two at a time
-__device__ __forceinline__ float norm_dot(const float* a, const float* b) {
+template <int V> __device__ __forceinline__ float norm_dot(const float (&a)[V], const float (&b)[V]) {
     float2 s = make_float2(0.f, 0.f), t = s;
 #pragma unroll
-    for (int e = 0; e < NORM_V; e += 4) {
+    for (int e = 0; e < V; e += 4) {
         s = __ffma2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]), s);
         t = __ffma2_rn(make_float2(a[e + 2], a[e + 3]), make_float2(b[e + 2], b[e + 3]), t);
     }
     return (s.x + s.y) + (t.x + t.y);
 }
 // x[e] = a[e] * b[e] (* k), two at a time
-__device__ __forceinline__ void norm_mul(float* x, const float* a, const float* b, float k) {
+template <int V> __device__ __forceinline__ void norm_mul(float (&x)[V], const float (&a)[V], const float (&b)[V], float k) {
 #pragma unroll
-    for (int e = 0; e < NORM_V; e += 2) {
+    for (int e = 0; e < V; e += 2) {
         const float2 t = __fmul2_rn(__fmul2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1])),
                                     make_float2(k, k));
         x[e] = t.x;
@@ -111,17 +110,17 @@ __device__ __forceinline__ void norm_mul(float* x, const float* a, const float* 
     }
 }
 // x[e] = k * a[e] + b[e]
-__device__ __forceinline__ void norm_axpy(float* x, float k, const float* a, const float* b) {
+template <int V> __device__ __forceinline__ void norm_axpy(float (&x)[V], float k, const float (&a)[V], const float (&b)[V]) {
 #pragma unroll
-    for (int e = 0; e < NORM_V; e += 2) {
+    for (int e = 0; e < V; e += 2) {
         const float2 t = __ffma2_rn(make_float2(k, k), make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
         x[e] = t.x;
         x[e + 1] = t.y;
     }
 }
-__device__ __forceinline__ void norm_scale(float* x, float k) {
+template <int V> __device__ __forceinline__ void norm_scale(float (&x)[V], float k) {
 #pragma unroll
-    for (int e = 0; e < NORM_V; e += 2) {
+    for (int e = 0; e < V; e += 2) {
         const float2 t = __fmul2_rn(make_float2(k, k), make_float2(x[e], x[e + 1]));
         x[e] = t.x;
         x[e + 1] = t.y;
@@ -130,6 +129,13 @@ __device__ __forceinline__ void norm_scale(float* x, float k) {
 
 constexpr int norm_threads(int TPR) { return TPR > 32 ? TPR : 128; }
 constexpr int norm_rows(int TPR) { return TPR > 32 ? 1 : 128 / TPR; }
+// Resident blocks of the backward kernel: 640 threads an SM, 512 with the second norm's registers.
+// (131072 rows of 128: 512 threads 50 us, 640 46 us; 8192 rows of 1001 with the second norm: 60
+// us, 83 us.)
+constexpr int norm_bwd_per_sm(int TPR, bool next) {
+    const int threads = norm_threads(TPR);
+    return threads >= 512 ? 1 : (next ? 512 : 640) / threads;
+}
 
 template <bool VEC, int TPR, typename IO>
 __global__ void __launch_bounds__(norm_threads(TPR))
@@ -137,8 +143,9 @@ norm_fwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __
                 const float* __restrict__ w_post, const float* __restrict__ w_next, int act,
                 int gate_first, float scale, float eps, IO* __restrict__ x_out,
                 IO* __restrict__ h, int64_t R, int D) {
-    using row_t = norm_row<VEC, TPR, IO>;
-    using wrow_t = norm_row<VEC, TPR, float>;
+    constexpr int V = NORM_FWD_V;
+    using row_t = norm_row<VEC, TPR, V, IO>;
+    using wrow_t = norm_row<VEC, TPR, V, float>;
     constexpr int ROWS = norm_rows(TPR);
     __shared__ float red[64];
     int flip = 0;
@@ -158,12 +165,12 @@ norm_fwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __
     for (; r0 < R; r0 += hop) {
         const int64_t row = r0 + threadIdx.x / TPR, at = row * D;
         const bool live = row < R;
-        float u[NORM_V], a[NORM_V], xr[NORM_V];
+        float u[V], a[V], xr[V];
         rf.to(u);
         if (gate) {
             rg.to(a);
 #pragma unroll
-            for (int e = 0; e < NORM_V; ++e) {
+            for (int e = 0; e < V; ++e) {
                 const float s = sigmoid_f(a[e]);
                 a[e] = act == NORM_ACT_SILU ? a[e] * s : s;
             }
@@ -174,7 +181,7 @@ norm_fwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __
         if (w_post) {
             const float rs = rsqrtf(fmaf(row_sum<TPR>(norm_dot(u, u), red, flip), inv_d, eps));
             wrow_t w;
-            float wf[NORM_V];
+            float wf[V];
             w.load(w_post, i, D);
             w.to(wf);
             norm_mul(u, u, wf, rs);
@@ -186,7 +193,7 @@ norm_fwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __
         if (w_next) {
             const float rs = rsqrtf(fmaf(row_sum<TPR>(norm_dot(u, u), red, flip), inv_d, eps));
             wrow_t w;
-            float wf[NORM_V];
+            float wf[V];
             w.load(w_next, i, D);
             w.to(wf);
             norm_mul(u, u, wf, rs);
@@ -196,51 +203,62 @@ norm_fwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __
 }
 
 // Gradients.  Each block keeps its threads' sums of dw_post and dw_next over the rows it walks
-// in registers, adds its row slots' in shared memory and writes one partial row per weight to
+// in registers (NEXT: with w_next), adds its row slots' in shared memory and writes one partial row per weight to
 // `part` ([2][gridDim.x][D]); norm_reduce_kernel adds the blocks in a fixed order.
-template <bool VEC, int TPR, typename IO>
-__global__ void __launch_bounds__(norm_threads(TPR))
+template <bool VEC, int TPR, bool NEXT, typename IO>
+__global__ void __launch_bounds__(norm_threads(TPR), norm_bwd_per_sm(TPR, NEXT))
 norm_bwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __restrict__ gate,
                 const float* __restrict__ w_post, const float* __restrict__ w_next, int act,
                 int gate_first, float scale, float eps, const IO* __restrict__ dx_out,
                 const IO* __restrict__ dh, IO* __restrict__ df, IO* __restrict__ dx,
                 IO* __restrict__ dgate, float* __restrict__ part, int64_t R, int D) {
-    using row_t = norm_row<VEC, TPR, IO>;
-    using wrow_t = norm_row<VEC, TPR, float>;
+    constexpr int V = NORM_BWD_V;
+    using row_t = norm_row<VEC, TPR, V, IO>;
+    using wrow_t = norm_row<VEC, TPR, V, float>;
     constexpr int ROWS = norm_rows(TPR);
-    __shared__ float red[TPR > 32 ? 64 : norm_threads(TPR) * NORM_V];
+    __shared__ float red[TPR > 32 ? 64 : norm_threads(TPR) * V];
     int flip = 0;
     const int i = threadIdx.x % TPR;
-    float dwp[NORM_V], dwn[NORM_V];
+    float dwp[V], dwn[V];
 #pragma unroll
-    for (int e = 0; e < NORM_V; ++e) dwp[e] = dwn[e] = 0.f;
+    for (int e = 0; e < V; ++e) dwp[e] = dwn[e] = 0.f;
     const float inv_d = 1.f / (float)D;
+    // the next row's loads are in flight while one is worked on, where registers allow it
+    constexpr bool AHEAD = TPR < 1024;
+    row_t nf, ng, nx, nd, nh;
+    auto fetch = [&](int64_t r0) {
+        int64_t row = r0 + threadIdx.x / TPR;
+        const int64_t at = (row < R ? row : R - 1) * D;  // a row that is not there repeats the last
+        nf.load(f + at, i, D);
+        if (gate) ng.load(gate + at, i, D);
+        if (NEXT && x) nx.load(x + at, i, D);  // x' matters to the second norm alone
+        if (dx_out) nd.load(dx_out + at, i, D);
+        if (NEXT) nh.load(dh + at, i, D);
+    };
     const int64_t hop = (int64_t)gridDim.x * ROWS;
-    for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < R; r0 += hop) {
-        const int64_t row = r0 + threadIdx.x / TPR;
+    int64_t r0 = (int64_t)blockIdx.x * ROWS;
+    if (AHEAD && r0 < R) fetch(r0);
+    for (; r0 < R; r0 += hop) {
+        const int64_t row = r0 + threadIdx.x / TPR, at = row * D;
         const bool live = row < R;
-        const int64_t at = (live ? row : R - 1) * D;  // a row that is not there repeats the last
-        row_t rf, rg, rx, rd, rh;
-        rf.load(f + at, i, D);
-        if (gate) rg.load(gate + at, i, D);
-        if (x && w_next) rx.load(x + at, i, D);  // x' matters to the second norm alone
-        if (dx_out) rd.load(dx_out + at, i, D);
-        if (w_next) rh.load(dh + at, i, D);
-        float v[NORM_V], s[NORM_V], d[NORM_V], w[NORM_V];  // s: sigmoid of the gate
+        if (!AHEAD) fetch(r0);
+        const row_t rf = nf, rg = ng, rx = nx, rd = nd, rh = nh;
+        if (AHEAD && r0 + hop < R) fetch(r0 + hop);
+        float v[V], s[V], d[V], w[V];  // s: sigmoid of the gate
         rf.to(v);
         if (gate) {
             rg.to(s);
 #pragma unroll
-            for (int e = 0; e < NORM_V; ++e) s[e] = sigmoid_f(s[e]);
+            for (int e = 0; e < V; ++e) s[e] = sigmoid_f(s[e]);
         }
         // the gate's factor of element e
-        auto factor = [&](const float* g, int e) { return act == NORM_ACT_SILU ? g[e] * s[e] : s[e]; };
+        auto factor = [&](const float (&g)[V], int e) { return act == NORM_ACT_SILU ? g[e] * s[e] : s[e]; };
         float rs = 1.f;
         if (gate && gate_first) {
-            float g[NORM_V];
+            float g[V];
             rg.to(g);
 #pragma unroll
-            for (int e = 0; e < NORM_V; ++e) v[e] *= factor(g, e);
+            for (int e = 0; e < V; ++e) v[e] *= factor(g, e);
         }
         if (w_post) {
             rs = rsqrtf(fmaf(row_sum<TPR>(norm_dot(v, v), red, flip), inv_d, eps));
@@ -253,16 +271,16 @@ norm_bwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __
             rd.to(d);
         } else {
 #pragma unroll
-            for (int e = 0; e < NORM_V; ++e) d[e] = 0.f;
+            for (int e = 0; e < V; ++e) d[e] = 0.f;
         }
-        if (w_next) {
-            float n[NORM_V], g[NORM_V];
+        if constexpr (NEXT) {
+            float n[V], g[V];
             if (w_post) norm_mul(n, v, w, scale);
             else norm_axpy(n, scale - 1.f, v, v);
             if (gate && !gate_first) {
                 rg.to(g);
 #pragma unroll
-                for (int e = 0; e < NORM_V; ++e) n[e] *= factor(g, e);
+                for (int e = 0; e < V; ++e) n[e] *= factor(g, e);
             }
             if (x) {
                 rx.to(g);
@@ -273,10 +291,10 @@ norm_bwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __
             rh.to(g);
             if (live) {
 #pragma unroll
-                for (int e = 0; e < NORM_V; ++e) dwn[e] = fmaf(g[e], n[e], dwn[e]);
+                for (int e = 0; e < V; ++e) dwn[e] = fmaf(g[e], n[e], dwn[e]);
             }
             wrow_t wr;
-            float wn[NORM_V];
+            float wn[V];
             wr.load(w_next, i, D);
             wr.to(wn);
             norm_mul(g, g, wn, 1.f);
@@ -287,11 +305,11 @@ norm_bwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __
         if (dx && live && OSDN_IN_BOUNDS(row, R)) row_t::store(dx + at, i, D, d);
         norm_scale(d, scale);
         // d of the gate: d * (what it multiplies) * act'; act' = s (1 + g (1 - s)) or s (1 - s)
-        auto gate_grad = [&](const float* m) {
-            float g[NORM_V], dg[NORM_V];
+        auto gate_grad = [&](const float (&m)[V]) {
+            float g[V], dg[V];
             rg.to(g);
 #pragma unroll
-            for (int e = 0; e < NORM_V; ++e) {
+            for (int e = 0; e < V; ++e) {
                 const float one = 1.f - s[e];
                 const float ds = act == NORM_ACT_SILU ? s[e] * fmaf(g[e], one, 1.f) : s[e] * one;
                 dg[e] = d[e] * m[e] * ds;
@@ -301,7 +319,7 @@ norm_bwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __
         };
         if (gate && !gate_first) {
             if (w_post) {
-                float m[NORM_V];
+                float m[V];
                 norm_mul(m, v, w, 1.f);
                 gate_grad(m);
             } else {
@@ -311,7 +329,7 @@ norm_bwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __
         if (w_post) {
             if (live) {
 #pragma unroll
-                for (int e = 0; e < NORM_V; ++e) dwp[e] = fmaf(d[e], v[e], dwp[e]);
+                for (int e = 0; e < V; ++e) dwp[e] = fmaf(d[e], v[e], dwp[e]);
             }
             norm_mul(d, d, w, 1.f);
             const float dot = row_sum<TPR>(norm_dot(d, v), red, flip) * inv_d;
@@ -333,13 +351,13 @@ norm_bwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __
         if constexpr (ROWS > 1) {
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < NORM_V; ++e) red[threadIdx.x * NORM_V + e] = dw[e];
+            for (int e = 0; e < V; ++e) red[threadIdx.x * V + e] = dw[e];
             __syncthreads();
             if (threadIdx.x < TPR) {
 #pragma unroll
-                for (int e = 0; e < NORM_V; ++e) {
+                for (int e = 0; e < V; ++e) {
                     dw[e] = 0.f;
-                    for (int q = 0; q < ROWS; ++q) dw[e] += red[(q * TPR + i) * NORM_V + e];
+                    for (int q = 0; q < ROWS; ++q) dw[e] += red[(q * TPR + i) * V + e];
                 }
                 wrow_t::store(out, i, D, dw);
             }
