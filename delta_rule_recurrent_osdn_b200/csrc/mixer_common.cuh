@@ -198,4 +198,21 @@ __device__ __forceinline__ bool row_sequence(const int32_t* __restrict__ cu, int
     return a >= 0 && a <= row && row < b && b <= T;
 }
 
+// Blocks of `len` tokens of all sequences are numbered so that sequence n's start at
+// first / len + n: no two share a number, some have none.  The sequence and the block in it that
+// `number` may stand for; false if none (the caller checks the block against the length).
+__device__ __forceinline__ bool token_block(const int32_t* __restrict__ cu, int N, int T, int len,
+                                            int64_t number, int& n, int& block) {
+    int lo = 0, hi = N - 1;  // the last n whose numbers start at or before this one
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        const int64_t first = cu ? (int64_t)__ldg(cu + mid) : (int64_t)mid * T;
+        if (first / len + mid <= number) lo = mid; else hi = mid - 1;
+    }
+    const int64_t first = cu ? (int64_t)__ldg(cu + lo) : (int64_t)lo * T;
+    n = lo;
+    block = (int)(number - (first / len + lo));
+    return block >= 0;
+}
+
 }  // namespace osdn

@@ -187,21 +187,55 @@ int64_t norm_bwd_blocks(int64_t R, int D, bool next) {
 }
 
 // ---------------------------------------------------------------- selective scan
-template <int MODE, typename IO>
-osdn_status_t launch_ssm_scan(const SsmArgs& a, int DQ, int DV, cudaStream_t stream) {
-    const int64_t ctas = (int64_t)a.N * a.H * (DV / SSM_BV);
+// How the fp32 scan cuts sequences into segments (see ssm_scan.cuh): tokens of one (INT_MAX: no
+// cuts), how many numbers they take, and the bytes they need.  About 4 CTAs for each of 148 SMs (a
+// constant, so that the workspace's size does not need a device), of 128 tokens at least, and only
+// where a sequence gives two: the first launch re-reads k and v and costs about 2/3 of a token's
+// time per token.
+struct SsmSegments { int seg; int64_t slots; size_t state, decay, bytes; };
+SsmSegments ssm_f32_segments(int64_t rows, int64_t N, int64_t T, int H, int Dk, int Dv) {
+    SsmSegments s = {INT_MAX, N, 0, 0, 0};
+    const int64_t most = Dk > Dv ? Dk : Dv;  // rows of the state, in either orientation
+    const int64_t len = ceil_div(ceil_div(rows * H * (most / SSM_BV), 4 * 148), SSM_BLOCK) * SSM_BLOCK;
+    const int64_t tokens = len < 128 ? 128 : len;
+    if (2 * tokens <= T && tokens < INT_MAX) {
+        s.seg = (int)tokens;
+        s.slots = rows / tokens + N;
+        s.decay = up256((size_t)s.slots * H * Dv * Dk * 4);
+        s.bytes = s.decay + up256((size_t)s.slots * H * 4);
+    }
+    return s;
+}
+
+template <int MODE, bool SEG>
+osdn_status_t launch_ssm_scan_one(const SsmArgs& a, int64_t slots, int DQ, int DV, cudaStream_t stream) {
+    const int64_t ctas = slots * a.H * (DV / SSM_BV);
     if (ctas == 0) return OSDN_OK;
     if (ctas > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)ctas), block(SSM_THREADS);
     if (DQ == 128 && DV == 128)
-        ssm_scan_kernel<128, 128, MODE, IO><<<grid, block, 0, stream>>>(a);
+        ssm_scan_kernel<128, 128, MODE, SEG, float><<<grid, block, 0, stream>>>(a);
     else if (DQ == 128)
-        ssm_scan_kernel<128, 64, MODE, IO><<<grid, block, 0, stream>>>(a);
+        ssm_scan_kernel<128, 64, MODE, SEG, float><<<grid, block, 0, stream>>>(a);
     else if (DV == 128)
-        ssm_scan_kernel<64, 128, MODE, IO><<<grid, block, 0, stream>>>(a);
+        ssm_scan_kernel<64, 128, MODE, SEG, float><<<grid, block, 0, stream>>>(a);
     else
-        ssm_scan_kernel<64, 64, MODE, IO><<<grid, block, 0, stream>>>(a);
+        ssm_scan_kernel<64, 64, MODE, SEG, float><<<grid, block, 0, stream>>>(a);
     return launch_status();
+}
+
+// One scan of a mode, its segments' launch first.  ws: the segments' workspace.
+template <int MODE>
+osdn_status_t launch_ssm_scan(SsmArgs a, const SsmSegments& sg, uint8_t* ws, int DQ, int DV,
+                              cudaStream_t stream) {
+    a.seg = sg.seg;
+    if (sg.seg != INT_MAX) {
+        a.seg_state = reinterpret_cast<float*>(ws + sg.state);
+        a.seg_decay = reinterpret_cast<float*>(ws + sg.decay);
+        const osdn_status_t st = launch_ssm_scan_one<MODE, true>(a, sg.slots, DQ, DV, stream);
+        if (st != OSDN_OK) return st;
+    }
+    return launch_ssm_scan_one<MODE, false>(a, sg.slots, DQ, DV, stream);
 }
 
 // 3-D bf16 view [rows][heads][D] of a token tensor; boxes of 64 channels x 1 head x 128 tokens,
@@ -226,7 +260,6 @@ bool make_chunk_map(CUtensorMap* m, const void* base, int D, int heads, int64_t 
 //   a chunk's time per chunk: two segments win from about 8 chunks on).
 //   Packed sequences, whose lengths the host does not know: twice the tokens that an even split
 //   of the whole would give a CTA, so only sequences far above the average are cut.
-struct SsmSegments { int seg; int64_t slots; size_t state, decay, bytes; };
 SsmSegments ssm_segments(bool packed, int64_t rows, int64_t N, int64_t T, int H, int Dk, int Dv) {
     const int64_t nvt = Dv / TCS_BV, chunks = ceil_div(packed ? rows : T, TCS_L), sms = 148;
     SsmSegments s = {INT_MAX, N, 0, 0, 0};
@@ -289,10 +322,10 @@ osdn_status_t check_ssm(int32_t H, int32_t G, int32_t Dk, int32_t Dv) {
 // the gradients behind each chunk as images of bf16 terms, the heads' dc and db when heads share
 // rows of b and c.  Both: the sums that the step gradient is made of.
 struct SsmBwdWorkspace {
-    size_t dch, dbh, ckpt, ckpt_r, gs, pos, ri, rn, wd, vk, part, total;
+    size_t seg, dch, dbh, ckpt, ckpt_r, gs, pos, ri, rn, wd, vk, part, total;
 };
-SsmBwdWorkspace ssm_bwd_workspace(int64_t rows, int64_t N, int32_t H, int32_t G, int32_t Dk,
-                                  int32_t Dv, osdn_dtype_t io) {
+SsmBwdWorkspace ssm_bwd_workspace(int64_t rows, int64_t N, int64_t T, int32_t H, int32_t G,
+                                  int32_t Dk, int32_t Dv, osdn_dtype_t io) {
     SsmBwdWorkspace w;
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -304,6 +337,7 @@ SsmBwdWorkspace ssm_bwd_workspace(int64_t rows, int64_t N, int32_t H, int32_t G,
     const size_t th = (size_t)rows * H, slots = (size_t)ssm_slots(rows, N, tc ? TCS_L : SSM_BLOCK);
     const size_t heads = !tc || G < H ? th * Dk * 4 : 0, shares = tc ? 4 : 1;
     const size_t image = slots * H * Dk * Dv * (tc ? TCS_TERMS * 2 : 4);
+    w.seg = take(tc ? 0 : ssm_f32_segments(rows, N, T, H, Dk, Dv).bytes);
     w.dch = take(heads);
     w.dbh = take(heads);
     w.ckpt = take(image);
@@ -348,7 +382,7 @@ osdn_status_t launch_ssm_gates(const SsmBwdCall& k, const SsmBwdWorkspace& w, co
 
 // fp32 tokens, and calls without tokens: three scans token by token.
 osdn_status_t launch_ssm_bwd_f32(const SsmBwdCall& k) {
-    const SsmBwdWorkspace w = ssm_bwd_workspace(k.rows, k.N, k.H, k.G, k.Dk, k.Dv, OSDN_F32);
+    const SsmBwdWorkspace w = ssm_bwd_workspace(k.rows, k.N, k.T, k.H, k.G, k.Dk, k.Dv, OSDN_F32);
     auto f32 = [&](size_t at) { return reinterpret_cast<float*>(k.ws + at); };
     SsmArgs a = {};
     a.dt = k.dt; a.A = k.A; a.D = k.D; a.dt_bias = k.dt_bias; a.softplus = k.softplus;
@@ -360,9 +394,10 @@ osdn_status_t launch_ssm_bwd_f32(const SsmBwdCall& k) {
     dcp.vk = k.dD ? f32(w.vk) : nullptr;
     dxp.q = k.b; dxp.k = k.c; dxp.v = k.dy; dxp.S_in = k.dST; dxp.out = k.dx; dxp.S_out = k.dS0;
     dbp.q = k.x; dbp.k = k.dy; dbp.v = k.c; dbp.S_in = k.dST; dbp.out = f32(w.dbh);
-    osdn_status_t st = launch_ssm_scan<SSM_DC, float>(dcp, k.Dv, k.Dk, k.stream);
-    if (st == OSDN_OK) st = launch_ssm_scan<SSM_DX, float>(dxp, k.Dk, k.Dv, k.stream);
-    if (st == OSDN_OK) st = launch_ssm_scan<SSM_DB, float>(dbp, k.Dv, k.Dk, k.stream);
+    const SsmSegments sg = ssm_f32_segments(k.rows, k.N, k.T, k.H, k.Dk, k.Dv);
+    osdn_status_t st = launch_ssm_scan<SSM_DC>(dcp, sg, k.ws + w.seg, k.Dv, k.Dk, k.stream);
+    if (st == OSDN_OK) st = launch_ssm_scan<SSM_DX>(dxp, sg, k.ws + w.seg, k.Dk, k.Dv, k.stream);
+    if (st == OSDN_OK) st = launch_ssm_scan<SSM_DB>(dbp, sg, k.ws + w.seg, k.Dv, k.Dk, k.stream);
     if (st != OSDN_OK) return st;
     if (k.rows > 0) {
         const int64_t need = ceil_div(k.rows * k.G, 8), cap = 16LL * sm_count();
@@ -381,7 +416,7 @@ osdn_status_t launch_ssm_bwd_f32(const SsmBwdCall& k) {
 // bf16 tokens: the chains of states in both directions, then all chunks at once.
 template <int DK, int DV> osdn_status_t launch_ssm_bwd_tc(const SsmBwdCall& k) {
     using bf16 = __nv_bfloat16;
-    const SsmBwdWorkspace w = ssm_bwd_workspace(k.rows, k.N, k.H, k.G, DK, DV, OSDN_BF16);
+    const SsmBwdWorkspace w = ssm_bwd_workspace(k.rows, k.N, k.T, k.H, k.G, DK, DV, OSDN_BF16);
     auto f32 = [&](size_t at) { return reinterpret_cast<float*>(k.ws + at); };
     TcsArgs a = {};
     a.dt = k.dt; a.A = k.A; a.dt_bias = k.dt_bias; a.softplus = k.softplus; a.cu = k.cu;
@@ -564,15 +599,18 @@ osdn_status_t osdn_ssm_fwd(const void* x, const float* dt, const float* A, const
         return Dk == 128 ? launch_tc_fwd<128>(c, b, x, t, sg.slots, s)
                          : launch_tc_fwd<64>(c, b, x, t, sg.slots, s);
     }
-    return launch_ssm_scan<SSM_FWD, float>(a, Dk, Dv, s);
+    return launch_ssm_scan<SSM_FWD>(a, ssm_f32_segments(rows, N, T, H, Dk, Dv),
+                                    static_cast<uint8_t*>(workspace), Dk, Dv, s);
 }
 
 size_t osdn_ssm_fwd_workspace_bytes(int32_t num_seqs, int32_t B, int32_t T, int32_t H, int32_t Dk,
                                     int32_t Dv, osdn_dtype_t io) {
     if (B < 0 || T < 0 || H < 1 || num_seqs < 0 || (Dk != 64 && Dk != 128) ||
-        (Dv != 64 && Dv != 128) || io != OSDN_BF16 || (int64_t)B * T == 0)
+        (Dv != 64 && Dv != 128) || (io != OSDN_BF16 && io != OSDN_F32) || (int64_t)B * T == 0)
         return 0;
-    return ssm_segments(num_seqs > 0, (int64_t)B * T, num_seqs > 0 ? num_seqs : B, T, H, Dk, Dv).bytes;
+    const int64_t rows = (int64_t)B * T, N = num_seqs > 0 ? num_seqs : B;
+    return io == OSDN_BF16 ? ssm_segments(num_seqs > 0, rows, N, T, H, Dk, Dv).bytes
+                           : ssm_f32_segments(rows, N, T, H, Dk, Dv).bytes;
 }
 
 osdn_status_t osdn_ssm_step(const void* x, const float* dt, const float* A, const void* b,
@@ -619,7 +657,7 @@ size_t osdn_ssm_bwd_workspace_bytes(int32_t num_seqs, int32_t B, int32_t T, int3
         return 0;
     // enough for heads that share rows of b and c, and for a call without tokens
     const int64_t rows = (int64_t)B * T, N = num_seqs > 0 ? num_seqs : B;
-    return ssm_bwd_workspace(rows, N, H, 1, Dk, Dv, rows > 0 ? io : OSDN_F32).total;
+    return ssm_bwd_workspace(rows, N, T, H, 1, Dk, Dv, rows > 0 ? io : OSDN_F32).total;
 }
 
 osdn_status_t osdn_ssm_bwd(const void* x, const float* dt, const float* A, const void* b,
@@ -637,7 +675,7 @@ osdn_status_t osdn_ssm_bwd(const void* x, const float* dt, const float* A, const
     if (!A || !dA || (rows > 0 && (!x || !dt || !b || !c || !dy || !dx || !ddt || !db || !dc)))
         return OSDN_ERR_INVALID_ARG;
     const osdn_dtype_t path = rows > 0 ? io : OSDN_F32;
-    const size_t need = ssm_bwd_workspace(rows, N, H, G, Dk, Dv, path).total;
+    const size_t need = ssm_bwd_workspace(rows, N, T, H, G, Dk, Dv, path).total;
     st = check_workspace(workspace, workspace_bytes, need);
     if (st != OSDN_OK) return st;
     if (N * H > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;

@@ -17,10 +17,16 @@
 //
 // One kernel serves all four: a CTA holds 32 rows of the state (DV channels of v) in registers,
 // 4 threads a row, each with DQ / 4 columns, and walks the tokens; tiles of q, k, v are staged in
-// shared memory, the next tile's loads in flight while one is used.  3 fp32 operations per state
+// shared memory, the loads of the tile after the next in flight while one is used.  3 fp32 operations per state
 // element and token (2 packed FMA-pipe instructions per 2 elements) against 16 bytes of shared
-// memory per 8: bound by FMA issue and, for few (sequence, head) pairs, by the chain of tokens.
+// memory per 8: bound by FMA issue and, for few (sequence, head) pairs, by the chain of tokens (a
+// warp alone on its scheduler takes 0.2 us a token).  So when there are few chains, sequences are
+// cut into segments that run side by side: a first launch (SEG) makes what each segment adds to a
+// zero state, and a segment starts from S_in and those in front of it (in its own direction).
+// (7 packed sequences of up to 1000 tokens, 4 heads: 209 us without.)
 #pragma once
+
+#include <limits.h>
 
 #include "mixer_common.cuh"
 
@@ -42,6 +48,9 @@ struct SsmArgs {
     float* ckpt;                  // DC writes, DB reads: S behind each block [slot][H][DV][DQ]
     float* gs;                    // DB: <G, S> behind each block [DV / 32][slot][H]
     float* vk;                    // DC: dy . x per token [H][rows], or null
+    float* seg_state;             // SEG writes, the others read: [number][H][DV][DQ]
+    float* seg_decay;             // [number][H]
+    int seg;                      // tokens of a segment, a multiple of SSM_BLOCK (INT_MAX: none)
     const int32_t* cu;
     int64_t rows;
     int N, T, H, G, softplus;
@@ -53,7 +62,7 @@ __host__ __device__ __forceinline__ int64_t ssm_slots(int64_t rows, int64_t N, i
     return rows / block + N + 1;
 }
 
-template <int DQ, int DV, int MODE, typename IO>
+template <int DQ, int DV, int MODE, bool SEG, typename IO>
 __global__ void __launch_bounds__(SSM_THREADS)
 ssm_scan_kernel(const SsmArgs p) {
     constexpr bool REV = MODE == SSM_DX || MODE == SSM_DB;   // reverse time
@@ -61,17 +70,32 @@ ssm_scan_kernel(const SsmArgs p) {
     constexpr int NF = DQ / 16;                              // float4 per thread and state row
     constexpr int LQ = SSM_TT * DQ / 4 / SSM_THREADS;        // float4 of q (k) a thread stages
     using tr = io_traits<IO>;
-    __shared__ float4 qs[SSM_TT][DQ / 4], ks[SSM_TT][DQ / 4];
-    __shared__ float vs[SSM_TT][SSM_BV], os[SSM_TT][SSM_BV];
-    __shared__ float as[SSM_TT], st[SSM_TT];
+    // two tiles: one is worked on while the next is written; gates of 8 tiles at a time
+    __shared__ float4 qb[2][SSM_TT][DQ / 4], kb[2][SSM_TT][DQ / 4];
+    __shared__ float vb[2][SSM_TT][SSM_BV], ob[2][SSM_TT][SSM_BV];
+    __shared__ float ab[2][SSM_THREADS], sb[2][SSM_THREADS];
     __shared__ float part[SSM_THREADS / 32];
 
     constexpr int NSL = DV / SSM_BV;
     const int slice = blockIdx.x % NSL;
-    const int64_t nh = blockIdx.x / NSL;
-    const int n = (int)(nh / p.H), h = (int)(nh - (int64_t)n * p.H);
+    const int64_t number = blockIdx.x / NSL / p.H;
+    const int h = (int)(blockIdx.x / NSL - number * p.H);
+    int n, part_of;
     int64_t first, count;
-    if (!seq_range(p.cu, n, p.N, p.T, first, count)) return;  // uniform over the CTA
+    // every sequence's offsets are checked here, whether or not a number leads to it
+    if (number < p.N && !seq_range(p.cu, (int)number, p.N, p.T, first, count) && p.seg == INT_MAX) return;
+    if (!token_block(p.cu, p.N, p.T, p.seg, number, n, part_of) ||
+        !seq_range(p.cu, n, p.N, p.T, first, count))
+        return;
+    const int64_t nh = (int64_t)n * p.H + h, seq_first = first;
+    const int64_t begin = (int64_t)part_of * p.seg;  // of the segment in its sequence
+    if (part_of > 0 && begin >= count) return;       // a number that no segment has
+    const int64_t parts = count > 0 ? (count + p.seg - 1) / p.seg : 1;
+    // the segment that a direction ends with adds to no other
+    if (SEG && part_of == (REV ? 0 : parts - 1)) return;
+    const bool ends = part_of == (REV ? 0 : parts - 1);
+    first += begin;                                  // all uniform over the CTA
+    count = count - begin < p.seg ? count - begin : p.seg;
     const int g = h / (p.H / p.G);
     // heads of the streams: FWD q = c, k = b, v = x; DC q = dy, k = x, v = b; DX q = b, k = c,
     // v = dy; DB q = x, k = dy, v = c.  b and c have G heads, x and dy H.
@@ -91,7 +115,7 @@ ssm_scan_kernel(const SsmArgs p) {
     for (int j = 0; j < NF; ++j) {
         const int col = (4 * j + quarter) * 4;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.S_in) {
+        if (!SEG && p.S_in) {
             if constexpr (TRANS) {
                 const float* e = p.S_in + sbase + vrow;  // stored [DQ][DV]
                 s = make_float4(e[(int64_t)col * DV], e[(int64_t)(col + 1) * DV],
@@ -104,9 +128,24 @@ ssm_scan_kernel(const SsmArgs p) {
         S[2 * j + 1] = make_float2(s.z, s.w);
     }
 
+    if constexpr (!SEG) {  // the segments in front, in this direction
+        for (int64_t e = REV ? parts - 1 : 0; REV ? e > part_of : e < part_of; e += REV ? -1 : 1) {
+            const int64_t at = (number - part_of + e) * p.H + h;
+            const float d = p.seg_decay[at];
+            const float* a = p.seg_state + (at * DV + vrow) * DQ;
+#pragma unroll
+            for (int j = 0; j < NF; ++j) {
+                const float4 s = *reinterpret_cast<const float4*>(a + (4 * j + quarter) * 4);
+                S[2 * j] = __ffma2_rn(make_float2(d, d), S[2 * j], make_float2(s.x, s.y));
+                S[2 * j + 1] = __ffma2_rn(make_float2(d, d), S[2 * j + 1], make_float2(s.z, s.w));
+            }
+        }
+    }
+    float whole = 1.f;  // SEG: the decay of all tokens so far
     const int64_t ntile = (count + SSM_TT - 1) / SSM_TT;
     float4 nq[LQ], nk[LQ];
     float nv[4], ndt = 0.f;
+    constexpr int GT = SSM_THREADS / SSM_TT;  // tiles of a group of gates
     auto tile_start = [&](int64_t i) { return (REV ? ntile - 1 - i : i) * SSM_TT; };
     auto fetch = [&](int64_t i) {  // tile i's elements of this thread, zeros past the end
         const int64_t t0 = tile_start(i);
@@ -115,7 +154,7 @@ ssm_scan_kernel(const SsmArgs p) {
             const int idx = tid + e * SSM_THREADS, t = idx / (DQ / 4), c4 = idx % (DQ / 4);
             nq[e] = nk[e] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (t0 + t < count) {
-                nq[e] = load4<IO>(q + (first + t0 + t) * qstride + c4 * 4);
+                if constexpr (!SEG) nq[e] = load4<IO>(q + (first + t0 + t) * qstride + c4 * 4);
                 nk[e] = load4<IO>(k + (first + t0 + t) * qstride + c4 * 4);
             }
         }
@@ -124,33 +163,50 @@ ssm_scan_kernel(const SsmArgs p) {
             const int t = (tid >> 5) + 4 * e;
             nv[e] = t0 + t < count ? tr::to_f32(v[(first + t0 + t) * vstride + (tid & 31)]) : 0.f;
         }
-        if (tid < SSM_TT) ndt = t0 + tid < count ? p.dt[(first + t0 + tid) * p.H + h] : 0.f;
     };
-    if (ntile > 0) fetch(0);
-    for (int64_t i = 0; i < ntile; ++i) {
-        const int64_t t0 = tile_start(i);
-        const int len = (int)(count - t0 < SSM_TT ? count - t0 : SSM_TT);
-        __syncthreads();  // the tile before is used up
+    auto put = [&](int64_t i) {    // the fetched tile into its buffer
+        const int b = (int)(i & 1);
 #pragma unroll
         for (int e = 0; e < LQ; ++e) {
             const int idx = tid + e * SSM_THREADS;
-            qs[idx / (DQ / 4)][idx % (DQ / 4)] = nq[e];
-            ks[idx / (DQ / 4)][idx % (DQ / 4)] = nk[e];
+            if constexpr (!SEG) qb[b][idx / (DQ / 4)][idx % (DQ / 4)] = nq[e];
+            kb[b][idx / (DQ / 4)][idx % (DQ / 4)] = nk[e];
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) vs[(tid >> 5) + 4 * e][tid & 31] = nv[e];
-        if (tid < SSM_TT) {
-            const float step = scan_step(ndt + bias, p.softplus);
-            st[tid] = step;
-            as[tid] = expf(step * A);
-        }
+        for (int e = 0; e < 4; ++e) vb[b][(tid >> 5) + 4 * e][tid & 31] = nv[e];
+    };
+    auto fetch_gates = [&](int64_t g) {  // this thread's token of group g
+        const int64_t i = g * GT + tid / SSM_TT, t = tile_start(i) + tid % SSM_TT;
+        ndt = i < ntile && t < count ? p.dt[(first + t) * p.H + h] : 0.f;
+    };
+    auto put_gates = [&](int64_t g) {
+        const float step = scan_step(ndt + bias, p.softplus);
+        sb[g & 1][tid] = step;
+        ab[g & 1][tid] = expf(step * A);
+    };
+    if (ntile > 0) {
+        fetch_gates(0);
+        fetch(0);
+        put_gates(0);
+        put(0);
+        if (ntile > 1) fetch(1);
+        fetch_gates(1);
         __syncthreads();
-        if (i + 1 < ntile) fetch(i + 1);
-        if constexpr (MODE == SSM_DB) {
+    }
+    for (int64_t i = 0; i < ntile; ++i) {
+        const int64_t t0 = tile_start(i);
+        const int len = (int)(count - t0 < SSM_TT ? count - t0 : SSM_TT);
+        const auto& qs = qb[i & 1];
+        const auto& ks = kb[i & 1];
+        const auto& vs = vb[i & 1];
+        auto& os = ob[i & 1];
+        const float* as = ab[(i / GT) & 1] + i % GT * SSM_TT;
+        const float* st = sb[(i / GT) & 1] + i % GT * SSM_TT;
+        if constexpr (MODE == SSM_DB && !SEG) {
             // entering a block from its end: <G, S>, G = S here (the carried gradient)
             const int64_t e = t0 + len;
             if (e == count || e % SSM_BLOCK == 0) {
-                const int64_t slot = first / SSM_BLOCK + n + (e - 1) / SSM_BLOCK;
+                const int64_t slot = seq_first / SSM_BLOCK + n + (begin + e - 1) / SSM_BLOCK;
                 const float* cp = p.ckpt + ((slot * p.H + h) * DV + vrow) * DQ;
                 float dot = 0.f;
 #pragma unroll
@@ -170,8 +226,8 @@ ssm_scan_kernel(const SsmArgs p) {
                 __syncthreads();
             }
         }
-        for (int u = 0; u < len; ++u) {
-            const int t = REV ? len - 1 - u : u;
+        // one token; its output in all 4 threads of the row
+        auto token = [&](int t) -> float {
             const float a = as[t], step = st[t];
             const float vraw = vs[t][row];
             const float vv = REV ? vraw : vraw * step;
@@ -179,7 +235,7 @@ ssm_scan_kernel(const SsmArgs p) {
             float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int j = 0; j < NF; ++j) {
-                const float4 k4 = ks[t][4 * j + quarter], q4 = qs[t][4 * j + quarter];
+                const float4 k4 = ks[t][4 * j + quarter], q4 = SEG ? k4 : qs[t][4 * j + quarter];
                 const float2 kl = make_float2(k4.x, k4.y), kh = make_float2(k4.z, k4.w);
                 if constexpr (REV) {  // the carried state is decayed already
                     S[2 * j] = __ffma2_rn(v2, kl, S[2 * j]);
@@ -188,25 +244,54 @@ ssm_scan_kernel(const SsmArgs p) {
                     S[2 * j] = __ffma2_rn(a2, S[2 * j], __fmul2_rn(v2, kl));
                     S[2 * j + 1] = __ffma2_rn(a2, S[2 * j + 1], __fmul2_rn(v2, kh));
                 }
-                acc0 = __ffma2_rn(S[2 * j], make_float2(q4.x, q4.y), acc0);
-                acc1 = __ffma2_rn(S[2 * j + 1], make_float2(q4.z, q4.w), acc1);
+                if constexpr (!SEG) {
+                    acc0 = __ffma2_rn(S[2 * j], make_float2(q4.x, q4.y), acc0);
+                    acc1 = __ffma2_rn(S[2 * j + 1], make_float2(q4.z, q4.w), acc1);
+                }
                 if constexpr (REV) {
                     S[2 * j] = __fmul2_rn(a2, S[2 * j]);
                     S[2 * j + 1] = __fmul2_rn(a2, S[2 * j + 1]);
                 }
             }
-            float o = (acc0.x + acc0.y) + (acc1.x + acc1.y);
+            return (acc0.x + acc0.y) + (acc1.x + acc1.y);
+        };
+        auto give = [&](int t, float o) {
+            if constexpr (MODE == SSM_DX) o *= st[t];
+            os[t][row] = fmaf(skip, vs[t][row], o);
+        };
+        int u = 0;
+        // four tokens at a time, so that their shared-memory reads and the sums over a row's
+        // threads overlap; each thread of a row stores one of the four
+        for (; u + 4 <= len; u += 4) {
+            float o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = token(REV ? len - 1 - u - k : u + k);
+            if constexpr (SEG) {
+                whole *= (as[u] * as[u + 1]) * (as[u + 2] * as[u + 3]);
+                continue;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] += __shfl_xor_sync(0xffffffffu, o[k], 1);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] += __shfl_xor_sync(0xffffffffu, o[k], 2);
+            const float mine = quarter == 0 ? o[0] : quarter == 1 ? o[1] : quarter == 2 ? o[2] : o[3];
+            give(REV ? len - 1 - u - quarter : u + quarter, mine);
+        }
+        for (; u < len; ++u) {
+            const int t = REV ? len - 1 - u : u;
+            float o = token(t);
+            if constexpr (SEG) {
+                whole *= as[u];
+                continue;
+            }
             o += __shfl_xor_sync(0xffffffffu, o, 1);
             o += __shfl_xor_sync(0xffffffffu, o, 2);
-            if (quarter == 0) {
-                if constexpr (MODE == SSM_DX) o *= step;
-                os[t][row] = fmaf(skip, vraw, o);
-            }
+            if (quarter == 0) give(t, o);
         }
-        if constexpr (MODE == SSM_DC) {
+        if constexpr (MODE == SSM_DC && !SEG) {
             const int64_t e = t0 + len;  // S behind a block
             if (e == count || e % SSM_BLOCK == 0) {
-                const int64_t slot = first / SSM_BLOCK + n + (e - 1) / SSM_BLOCK;
+                const int64_t slot = seq_first / SSM_BLOCK + n + (begin + e - 1) / SSM_BLOCK;
                 float* cp = p.ckpt + ((slot * p.H + h) * DV + vrow) * DQ;
                 if (OSDN_IN_BOUNDS(slot, ssm_slots(p.rows, p.N, SSM_BLOCK)))
 #pragma unroll
@@ -228,11 +313,17 @@ ssm_scan_kernel(const SsmArgs p) {
                     p.vk[h * p.rows + first + t0 + (tid >> 3)] = dot;
             }
         }
+        if (i + 1 < ntile) put(i + 1);
+        if (i % GT == GT - 1) {  // the next group's gates, and the loads of the one behind it
+            put_gates(i / GT + 1);
+            fetch_gates(i / GT + 2);
+        }
+        if (i + 2 < ntile) fetch(i + 2);
         __syncthreads();
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int t = (tid >> 5) + 4 * e;
-            if (t < len && OSDN_IN_BOUNDS(first + t0 + t, p.rows)) {
+            if (!SEG && t < len && OSDN_IN_BOUNDS(first + t0 + t, p.rows)) {
                 const int64_t at = ((first + t0 + t) * p.H + h) * DV + slice * SSM_BV + (tid & 31);
                 if constexpr (TRANS)
                     static_cast<float*>(p.out)[at] = os[t][tid & 31];
@@ -241,11 +332,14 @@ ssm_scan_kernel(const SsmArgs p) {
             }
         }
     }
-    if (!TRANS && p.S_out && OSDN_IN_BOUNDS(nh, (int64_t)p.N * p.H)) {
+    float* out = SEG ? p.seg_state + (number * p.H + h) * DV * DQ : !TRANS && ends ? p.S_out : nullptr;
+    if (!SEG && out) out += sbase;
+    if (out && OSDN_IN_BOUNDS(nh, (int64_t)p.N * p.H)) {
 #pragma unroll
         for (int j = 0; j < NF; ++j)
-            *reinterpret_cast<float4*>(p.S_out + sbase + (int64_t)vrow * DQ + (4 * j + quarter) * 4) =
+            *reinterpret_cast<float4*>(out + (int64_t)vrow * DQ + (4 * j + quarter) * 4) =
                 make_float4(S[2 * j].x, S[2 * j].y, S[2 * j + 1].x, S[2 * j + 1].y);
+        if (SEG && tid == 0 && slice == 0) p.seg_decay[number * p.H + h] = whole;
     }
 }
 
@@ -327,17 +421,12 @@ ssm_gate_kernel(const float* __restrict__ pos, const float* __restrict__ ri,
     const int lane = threadIdx.x & 31;
     const int64_t slot = unit / H;
     const int h = (int)(unit - slot * H);
-    int lo = 0, hi = N - 1;  // the sequence that the block belongs to
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        const int64_t f = cu ? (int64_t)__ldg(cu + mid) : (int64_t)mid * T;
-        if (f / BLOCK + mid <= slot) lo = mid; else hi = mid - 1;
-    }
+    int n, s_of;
     int64_t first = 0, count = 0;
     float sA = 0.f, sD = 0.f, sb = 0.f;
-    const bool ok = seq_range(cu, lo, N, T, first, count);
-    const int64_t t0 = (slot - (first / BLOCK + lo)) * BLOCK;
-    if (ok && t0 >= 0 && t0 < count) {
+    const bool ok = token_block(cu, N, T, BLOCK, slot, n, s_of) && seq_range(cu, n, N, T, first, count);
+    const int64_t t0 = (int64_t)s_of * BLOCK;
+    if (ok && t0 < count) {
         const float Ah = A[h], bias = dt_bias ? dt_bias[h] : 0.f;
         float edge = 0.f;
         for (int s = 0; s < nslice; ++s) edge += gs[(s * slots + slot) * H + h];

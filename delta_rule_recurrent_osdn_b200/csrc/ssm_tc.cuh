@@ -200,21 +200,7 @@ __device__ __forceinline__ void tcs_mma(uint32_t d, uint64_t a, uint64_t b, uint
 // Segments.  When there are too few (sequence, head) chains for the machine, sequences are cut into
 // segments of p.seg tokens that run side by side: a first launch (SEG) makes what each segment
 // adds to a zero state, and a segment of the forward pass builds its initial state from S0 and
-// the segments in front of it.  Segments are numbered like blocks of tokens (ssm_slots): sequence
-// n's from first / seg + n on, with unused numbers in between.
-__device__ __forceinline__ bool tcs_segment(const TcsArgs& p, int slot, int& n, int& s) {
-    int lo = 0, hi = p.N - 1;  // the last n whose numbers start at or before slot
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        const int64_t first = p.cu ? (int64_t)__ldg(p.cu + mid) : (int64_t)mid * p.T;
-        if (first / p.seg + mid <= slot) lo = mid; else hi = mid - 1;
-    }
-    const int64_t first = p.cu ? (int64_t)__ldg(p.cu + lo) : (int64_t)lo * p.T;
-    n = lo;
-    s = (int)(slot - (first / p.seg + lo));
-    return s >= 0;
-}
-
+// the segments in front of it.
 template <int DQ, int MODE>
 __global__ void __launch_bounds__(TcsSmem<DQ, MODE>::THREADS, 1)
 ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -237,7 +223,7 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     int64_t first, count;
     // every sequence's offsets are checked here, whether or not a number leads to it
     if (slot < p.N && !seq_range(p.cu, slot, p.N, p.T, first, count) && p.seg == INT_MAX) return;
-    if (!tcs_segment(p, slot, n, seg) || !seq_range(p.cu, n, p.N, p.T, first, count)) return;
+    if (!token_block(p.cu, p.N, p.T, p.seg, slot, n, seg) || !seq_range(p.cu, n, p.N, p.T, first, count)) return;
     const int64_t start = (int64_t)seg * p.seg;  // of the segment in its sequence
     if (seg > 0 && start >= count) return;       // a number that no segment has
     const bool last = count - start <= p.seg;

@@ -94,17 +94,13 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t slot = blockIdx.x / p.H;
     const int h = (int)(blockIdx.x - slot * p.H), g = h / (p.H / p.G);
-    // the chunk with this number: sequence n's start at first / TCS_L + n
-    int lo = 0, hi = p.N - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        const int64_t f = p.cu ? (int64_t)__ldg(p.cu + mid) : (int64_t)mid * p.T;
-        if (f / TCS_L + mid <= slot) lo = mid; else hi = mid - 1;
-    }
+    int n, chunk;
     int64_t first, count;
-    if (!seq_range(p.cu, lo, p.N, p.T, first, count)) return;
-    const int64_t start = (slot - (first / TCS_L + lo)) * TCS_L;
-    if (start < 0 || start >= count) return;  // all uniform over the CTA
+    if (!token_block(p.cu, p.N, p.T, TCS_L, slot, n, chunk) ||
+        !seq_range(p.cu, n, p.N, p.T, first, count))
+        return;
+    const int64_t start = (int64_t)chunk * TCS_L;
+    if (start >= count) return;  // a number that no chunk has; all uniform over the CTA
     const int64_t row0 = first + start;
     const int len = count - start < TCS_L ? (int)(count - start) : TCS_L;
 

@@ -381,16 +381,19 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 def _placed(fn):
     """Runs an entry point with its first tensor's device current and, when `stream` is given, that
     stream: outputs and workspace are then allocated for the stream that the call launches on."""
+    first = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(t, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        t = args[0] if args else kw[first]
         if not t.is_cuda:
             raise ValueError("tensors must be CUDA tensors")
         if stream is None and t.device.index == _current_device():
-            return fn(t, *args, **kw)
+            return fn(*args, **kw)
         if stream is not None and stream.device != t.device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
         with torch.cuda.device(t.device), torch.cuda.stream(stream):
-            return fn(t, *args, **kw)
+            return fn(*args, **kw)
     return call
 
 

@@ -178,6 +178,9 @@ SCANS = [  # io, lens, packed, H, G, Dk, Dv, D, bias, state, softplus
     ("f32", [65, 65], False, 2, 2, 128, 64, True, True, False, True),
     ("f32", [5, 1, 130, 0, 64, 17], True, 4, 2, 64, 128, True, True, True, True),
     ("f32", [200], False, 3, 1, 128, 128, False, False, True, False),
+    # long enough for the few heads that sequences are cut into segments
+    ("f32", [300, 300], False, 2, 1, 64, 128, True, True, True, True),
+    ("f32", [5, 400, 0, 129, 128, 1], True, 2, 2, 128, 64, True, True, True, True),
     ("bf16", [1], False, 1, 1, 128, 128, True, True, True, True),
     ("bf16", [127, 127], False, 2, 1, 128, 128, True, True, False, True),
     ("bf16", [128], False, 2, 2, 64, 64, False, True, True, True),
@@ -343,7 +346,7 @@ def test_scan_keeps_sequences_apart(osdn, io):
 
 
 @pytest.mark.parametrize("io,lens,packed", [("bf16", [1100], False), ("bf16", [700, 900, 1], True),
-                                            ("f32", [150], False)])
+                                            ("f32", [150], False), ("f32", [301, 7, 290], True)])
 def test_scan_slow_decay(osdn, io, lens, packed):
     """States that hardly decay: what a sequence starts from, and every segment and chunk, reaches
     all of what follows."""
@@ -546,6 +549,16 @@ def test_binding_refuses(osdn):
         osdn.osdn_norm_bwd(x, x, x)
     with pytest.raises(ValueError, match="cuda:0|cpu|CUDA"):
         osdn.osdn_norm_fwd(x, x=x.cpu())
+
+
+def test_calls_by_keyword(osdn):
+    t = layer_inputs("bf16", [20], 2, 1, 64, 64, 5)
+    want = osdn.osdn_ssm_fwd(t["u"], t["dt"], t["A"], t["b"], t["c"])
+    got = osdn.osdn_ssm_fwd(c=t["c"], b=t["b"], A=t["A"], dt=t["dt"], x=t["u"],
+                            stream=torch.cuda.current_stream())
+    same(got, want)
+    with pytest.raises(TypeError, match="dt"):
+        osdn.osdn_ssm_fwd(t["u"])
 
 
 def layer(osdn, t, io, cu=None):
