@@ -439,6 +439,7 @@ template <int DK, int DV> osdn_status_t launch_ssm_bwd_tc(const SsmBwdCall& k) {
     g.pos = f32(w.pos); g.ri = f32(w.ri); g.rn = f32(w.rn); g.gs = f32(w.gs); g.wd = f32(w.wd); g.vk = k.dD ? f32(w.vk) : nullptr;
     g.cu = k.cu; g.rows = k.rows; g.N = (int)k.N; g.T = k.T; g.H = k.H; g.G = k.G;
     g.slots = ssm_slots(k.rows, k.N, TCS_L);
+    g.round = sm_count();
     if (g.slots * k.H > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
     using L = TcgSmem<DK, DV>;
     CUtensorMap mx, my, mb, mc;

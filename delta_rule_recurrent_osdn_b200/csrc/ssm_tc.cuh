@@ -80,7 +80,8 @@ template <int DQ, int MODE> struct TcsSmem {
     static constexpr uint32_t BAR = GATE + TCS_GATES * GATE_BYTES;
     static constexpr uint32_t TMEM_SLOT = BAR + (27 + 2 * TCS_GATES) * 8 + 8;
     static constexpr size_t BYTES = TMEM_SLOT + 16 + 1024;  // + alignment slack
-    static constexpr int THREADS = OUT ? 768 : 384;
+    static constexpr int THREADS = OUT ? 768 : 512;
+    static constexpr int VW = OUT ? 1 : 2;            // warpgroups that make V'
     // tensor memory: G / P (two buffers), B^T V' (its terms side by side), C S^T, P X
     static constexpr uint32_t COL_G = 0, COL_U = OUT ? 256 : 0, COL_Y1 = 384, COL_Y2 = 448;
     static constexpr uint32_t COLS = OUT ? 512 : 256;
@@ -282,13 +283,13 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             mbar_init(&v_empty[i], 1);
             mbar_init(&g_full[i], 1);
             mbar_init(&p_full[i], 8);
-            mbar_init(&vp_full[i], 4);
+            mbar_init(&vp_full[i], 4 * L::VW);
             mbar_init(&vp_free[i], 1);
         }
         for (int i = 0; i < TCS_GATES; ++i) {
             mbar_init(&gate_full[i], 1);
             // FWD: the output rows are the last readers; else V' and the state read them
-            mbar_init(&gate_free[i], OUT ? 4 : 8);
+            mbar_init(&gate_free[i], OUT ? 4 : 4 + 4 * L::VW);
         }
         mbar_init(u_full, 1);
         mbar_init(u_free, 4);
@@ -528,10 +529,12 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
         }
         if (!OUT && lane == 0) tc::bulk_wait_all();
-    } else if (warp < 12) {
+    } else if (warp < 8 + 4 * L::VW) {
         if constexpr (OUT) tc::reg_dec<72>();
         // ------------------------------------------------------------ V'
-        const int r = tid - 256, b = r >> 4;  // token of the chunk
+        const int r = tid & 127, b = r >> 4;  // token of the chunk
+        constexpr int NJ = 8 / L::VW;         // 8-channel groups of a thread
+        const int j0 = OUT ? 0 : (warp - 8) / 4 * NJ;
         for (int i = 0; i < nch; ++i) {
             if (!wait(&gate_full[i % TCS_GATES], i / TCS_GATES) || !wait(&v_full[i & 1], i >> 1)) break;
             const TcsGate* gt = gate(i);
@@ -547,7 +550,7 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             if (!live) {  // the next sequence's row: 0 x NaN must not reach a sum
                 const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-                for (int j = 0; j < 8; ++j) {
+                for (int j = j0; j < j0 + NJ; ++j) {
                     const uint32_t off = tc::sw128_off(r, j);
                     *reinterpret_cast<uint4*>(v + off) = z;
 #pragma unroll
@@ -555,12 +558,12 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         *reinterpret_cast<uint4*>(stage(i) + L::K + q * 16384 + off) = z;
                 }
             }
-            uint4 x[8];
+            uint4 x[NJ];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = *reinterpret_cast<const uint4*>(v + tc::sw128_off(r, j));
+            for (int j = 0; j < NJ; ++j) x[j] = *reinterpret_cast<const uint4*>(v + tc::sw128_off(r, j0 + j));
             if (i > 0 && !wait(vp_free, i - 1)) break;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < NJ; ++j) {
                 const uint32_t xw[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
                 uint32_t t0[4], t1[4], t2[4];
 #pragma unroll
@@ -571,7 +574,7 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     else split2_rn(t.x, t.y, t0[k], t1[k]);
                     if (!live) t0[k] = t1[k] = t2[k] = 0;
                 }
-                uint4* o = reinterpret_cast<uint4*>(vp + tc::sw128_off(r, j));
+                uint4* o = reinterpret_cast<uint4*>(vp + tc::sw128_off(r, j0 + j));
                 o[0] = make_uint4(t0[0], t0[1], t0[2], t0[3]);
                 o[1024] = make_uint4(t1[0], t1[1], t1[2], t1[3]);
                 if constexpr (L::NT == 3) o[2048] = make_uint4(t2[0], t2[1], t2[2], t2[3]);

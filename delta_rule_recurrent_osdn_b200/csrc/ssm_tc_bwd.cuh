@@ -47,7 +47,7 @@ struct TcgArgs {
     float* wd;                     // W_tt [H][rows]
     const int32_t* cu;
     int64_t rows, slots;
-    int N, T, H, G, softplus;
+    int N, T, H, G, softplus, round;  // round: CTAs that run at a time
 };
 
 template <int DK, int DV> struct TcgSmem {
@@ -168,6 +168,30 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             }
             load_term(0, imr);
             load_term(1, imr + L::TERM);
+            // what the CTA that follows here about a round later will load, into L2 meanwhile: its
+            // first loads then do not wait for HBM (156 -> 128 us at the 340M shape)
+            const int64_t ahead = (int64_t)blockIdx.x + p.round, aslot = ahead / p.H;
+            int an, achunk;
+            if (aslot < p.slots && token_block(p.cu, p.N, p.T, TCS_L, aslot, an, achunk)) {
+                const int ah = (int)(ahead - aslot * p.H), ag = ah / (p.H / p.G);
+                const int64_t af = p.cu ? (int64_t)__ldg(p.cu + an) : (int64_t)an * p.T;
+                const int64_t ar = af + (int64_t)achunk * TCS_L;
+                if (af >= 0 && ar < p.rows) {
+#pragma unroll
+                    for (int e = 0; e < DK / 64; ++e) {
+                        tc::tma_prefetch_3d(&tm_b, e * 64, ag, (int)ar);
+                        tc::tma_prefetch_3d(&tm_c, e * 64, ag, (int)ar);
+                    }
+#pragma unroll
+                    for (int e = 0; e < DV / 64; ++e) {
+                        tc::tma_prefetch_3d(&tm_x, e * 64, ah, (int)ar);
+                        tc::tma_prefetch_3d(&tm_dy, e * 64, ah, (int)ar);
+                    }
+                    const int64_t aat = (aslot * p.H + ah) * (int64_t)(TCS_TERMS * L::TERM);
+                    tc::bulk_prefetch(p.img_r + aat, TCS_TERMS * L::TERM);
+                    tc::bulk_prefetch(p.img + aat, TCS_TERMS * L::TERM);
+                }
+            }
             int n0 = 1, n1 = 1;  // terms asked for
             constexpr uint32_t ID_S = tc::idesc(1, 0, 0, 128, 128);   // scores
             constexpr uint32_t ID_KK = tc::idesc(1, 0, 0, 128, DK);   // rows x key channels, K-major
@@ -295,34 +319,51 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             return *reinterpret_cast<const uint4*>(smem + tile + (ch >> 6) * 16384 +
                                                    tc::sw128_off(r, (ch & 63) >> 3));
         };
+        // 32 channels (64 bytes) of each of the warp's rows, packed in w: four lanes exchange their
+        // quarters, so that a store covers 64 bytes of 8 rows instead of 16 of 32
+        auto store_rows = [&](__nv_bfloat16* base, int64_t stride, uint32_t (&w)[16]) {
+            const bool odd1 = lane & 1, odd2 = lane & 2;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // quarters 0 <-> 1 and 2 <-> 3 with the neighbour
+#pragma unroll
+                for (int q = 0; q < 4; q += 2) {
+                    const uint32_t t = __shfl_xor_sync(0xffffffffu, odd1 ? w[4 * q + e] : w[4 * q + 4 + e], 1);
+                    if (odd1) w[4 * q + e] = t; else w[4 * q + 4 + e] = t;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // 0 <-> 2 and 1 <-> 3 with the pair next to it
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t t = __shfl_xor_sync(0xffffffffu, odd2 ? w[4 * q + e] : w[4 * q + 8 + e], 2);
+                    if (odd2) w[4 * q + e] = t; else w[4 * q + 8 + e] = t;
+                }
+            }
+            const int r4 = 32 * wq + (lane & ~3);  // w[4 k ..]: this lane's quarter of row r4 + k
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (r4 + k < len && OSDN_IN_BOUNDS(row0 + r4 + k, p.rows))
+                    *reinterpret_cast<uint4*>(base + (row0 + r4 + k) * stride + 8 * (lane & 3)) =
+                        make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        };
+        // this warpgroup's quarter of rows of W channels (all heads: stride H * W)
+        auto put_bf16 = [&](__nv_bfloat16* base, auto width, uint32_t (&w)[16]) {
+            constexpr int W = decltype(width)::value;
+            __nv_bfloat16* o = base + wg * (W / 4);
+            if constexpr (W == 128) {
+                store_rows(o, (int64_t)p.H * W, w);
+            } else if (live && OSDN_IN_BOUNDS(row, p.rows)) {
+                uint4* e = reinterpret_cast<uint4*>(o + row * p.H * W);
+                e[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                e[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+            __syncwarp();
+        };
         auto arrive = [&](uint64_t* bar) {
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        // ---- 2^cum_L <R, S> from the two leading terms (both also on their way to shared memory)
-        float dot = 0.f;
-        {
-            const int64_t at = (slot * p.H + h) * (int64_t)(TCS_TERMS * L::TERM);
-            const uint4* a = reinterpret_cast<const uint4*>(p.img_r + at);
-            const uint4* b = reinterpret_cast<const uint4*>(p.img + at);
-            constexpr int NB = L::TERM / 16;
-#pragma unroll 2
-            for (int e = tid; e < NB; e += 512) {
-                const uint4 a0 = __ldg(a + e), a1 = __ldg(a + NB + e), b0 = __ldg(b + e), b1 = __ldg(b + NB + e);
-                const uint32_t x0[4] = {a0.x, a0.y, a0.z, a0.w}, x1[4] = {a1.x, a1.y, a1.z, a1.w};
-                const uint32_t y0[4] = {b0.x, b0.y, b0.z, b0.w}, y1[4] = {b1.x, b1.y, b1.z, b1.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    dot = fmaf(__uint_as_float(x0[k] << 16) + __uint_as_float(x1[k] << 16),
-                               __uint_as_float(y0[k] << 16) + __uint_as_float(y1[k] << 16), dot);
-                    dot = fmaf(__uint_as_float(x0[k] & 0xffff0000u) + __uint_as_float(x1[k] & 0xffff0000u),
-                               __uint_as_float(y0[k] & 0xffff0000u) + __uint_as_float(y1[k] & 0xffff0000u),
-                               dot);
-                }
-            }
-            dot = warp_sum_f(dot);
-        }
         bool ok = true;
         if (len < TCS_L && (ok = wait(tiles, 0))) {  // rows of the next sequence: 0 x NaN must not
             if (!live && wg == 0) {                  // reach a sum
@@ -339,8 +380,6 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         ok = ok && wait(gates, 0) && wait(sc1, 0);
         if (ok) {
             tc::fence_after_sync();
-            if (lane == 0 && OSDN_IN_BOUNDS(slot, p.slots))
-                p.gs[(warp * p.slots + slot) * p.H + h] = dot * ex2f(f->bh[8] + f->bl[8]);
             // ---- scores [j][i], i >= j: 2^(cum_i - cum_j) = 2^l_i 2^(base_b - cum_j)
             float ri = 0.f;
             const float sj = f->st[r];
@@ -457,13 +496,39 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             tc::tmem_st_wait();
             if (live && OSDN_IN_BOUNDS(row, p.rows)) p.rn[(wg * p.H + h) * p.rows + row] = rn;
             arrive(ew1);
+        }
+        // ---- 2^cum_L <R, S> from the two leading terms, in L2 by now
+        if (ok) {
+            float dot = 0.f;
+            const int64_t at = (slot * p.H + h) * (int64_t)(TCS_TERMS * L::TERM);
+            const uint4* a = reinterpret_cast<const uint4*>(p.img_r + at);
+            const uint4* b = reinterpret_cast<const uint4*>(p.img + at);
+            constexpr int NB = L::TERM / 16;
+#pragma unroll 2
+            for (int e = tid; e < NB; e += 512) {
+                const uint4 a0 = __ldg(a + e), a1 = __ldg(a + NB + e), b0 = __ldg(b + e), b1 = __ldg(b + NB + e);
+                const uint32_t x0[4] = {a0.x, a0.y, a0.z, a0.w}, x1[4] = {a1.x, a1.y, a1.z, a1.w};
+                const uint32_t y0[4] = {b0.x, b0.y, b0.z, b0.w}, y1[4] = {b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    dot = fmaf(__uint_as_float(x0[k] << 16) + __uint_as_float(x1[k] << 16),
+                               __uint_as_float(y0[k] << 16) + __uint_as_float(y1[k] << 16), dot);
+                    dot = fmaf(__uint_as_float(x0[k] & 0xffff0000u) + __uint_as_float(x1[k] & 0xffff0000u),
+                               __uint_as_float(y0[k] & 0xffff0000u) + __uint_as_float(y1[k] & 0xffff0000u),
+                               dot);
+                }
+            }
+            dot = warp_sum_f(dot);
+            if (lane == 0 && OSDN_IN_BOUNDS(slot, p.slots))
+                p.gs[(warp * p.slots + slot) * p.H + h] = dot * ex2f(f->bh[8] + f->bl[8]);
             ok = wait(acc1, 0);
         }
         if (ok) {
             tc::fence_after_sync();
             // ---- dx and db
             const float skip = p.D ? p.D[h] : 0.f;
-#pragma unroll 1
+            uint32_t w[16];
+#pragma unroll
             for (int q = 0; q < DV / 64; ++q) {
                 const int c = wg * (DV / 4) + 16 * q;
                 float v[16];
@@ -471,49 +536,39 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 const uint4 u0 = tile16(L::DY, c), u1 = tile16(L::DY, c + 8);
                 const uint32_t yw[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
                 tc::tmem_ld_wait();
-                uint32_t w[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    w[e] = pack2_rn(fmaf(st, v[2 * e], skip * __uint_as_float(yw[e] << 16)),
-                                    fmaf(st, v[2 * e + 1], skip * __uint_as_float(yw[e] & 0xffff0000u)));
-                if (live && OSDN_IN_BOUNDS(row, p.rows)) {
-                    uint4* o = reinterpret_cast<uint4*>(p.dx + (row * p.H + h) * DV + c);
-                    o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    o[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                }
-                __syncwarp();
+                    w[8 * q + e] = pack2_rn(fmaf(st, v[2 * e], skip * __uint_as_float(yw[e] << 16)),
+                                            fmaf(st, v[2 * e + 1], skip * __uint_as_float(yw[e] & 0xffff0000u)));
             }
+            put_bf16(p.dx + (int64_t)h * DV, std::integral_constant<int, DV>{}, w);
         }
-        // a head's row of db or dc, 16 channels
-        auto put = [&](__nv_bfloat16* o16, float* o32, int c, const float* v) {
-            if (!live || !OSDN_IN_BOUNDS(row, p.rows)) return;
-            const int64_t at = (row * p.H + h) * DK + c;
-            if (o16) {
-                uint32_t w[8];
+        // this warpgroup's quarter of a head's rows of db or dc, each value times k
+        auto give = [&](__nv_bfloat16* o16, float* o32, uint32_t acc, float k) {
+            uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = pack2_rn(v[2 * e], v[2 * e + 1]);
-                uint4* o = reinterpret_cast<uint4*>(o16 + at);
-                o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                o[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    *reinterpret_cast<float4*>(o32 + at + 4 * e) =
-                        make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-            }
-        };
-        if (ok) {
-#pragma unroll 1
             for (int q = 0; q < DK / 64; ++q) {
                 const int c = wg * (DK / 4) + 16 * q;
                 float v[16];
-                tc::tmem_ld16(tl + A1 + c, v);
+                tc::tmem_ld16(tl + acc + c, v);
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] *= st;
-                put(p.db, p.dbh, c, v);
+                for (int e = 0; e < 16; ++e) v[e] *= k;
+                if (o16) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[8 * q + e] = pack2_rn(v[2 * e], v[2 * e + 1]);
+                } else if (live && OSDN_IN_BOUNDS(row, p.rows)) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<float4*>(o32 + (row * p.H + h) * DK + c + 4 * e) =
+                            make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                }
                 __syncwarp();
             }
+            if (o16) put_bf16(o16 + (int64_t)h * DK, std::integral_constant<int, DK>{}, w);
+        };
+        if (ok) {
+            give(p.db, p.dbh, A1, st);
             arrive(out1);
             ok = wait(sc2, 0);
         }
@@ -606,15 +661,7 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         }
         if (ok) {
             tc::fence_after_sync();
-#pragma unroll 1
-            for (int q = 0; q < DK / 64; ++q) {
-                const int c = wg * (DK / 4) + 16 * q;
-                float v[16];
-                tc::tmem_ld16(tl + A0 + c, v);
-                tc::tmem_ld_wait();
-                put(p.dc, p.dch, c, v);
-                __syncwarp();
-            }
+            give(p.dc, p.dch, A0, 1.f);
         }
     }
     tc::fence_before_sync();
