@@ -268,14 +268,14 @@ ssm_scan_kernel(const SsmArgs p) {
             for (int k = 0; k < 4; ++k) o[k] = token(REV ? len - 1 - u - k : u + k);
             if constexpr (SEG) {
                 whole *= (as[u] * as[u + 1]) * (as[u + 2] * as[u + 3]);
-                continue;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] += __shfl_xor_sync(0xffffffffu, o[k], 1);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] += __shfl_xor_sync(0xffffffffu, o[k], 2);
+                const float mine = quarter == 0 ? o[0] : quarter == 1 ? o[1] : quarter == 2 ? o[2] : o[3];
+                give(REV ? len - 1 - u - quarter : u + quarter, mine);
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[k] += __shfl_xor_sync(0xffffffffu, o[k], 1);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[k] += __shfl_xor_sync(0xffffffffu, o[k], 2);
-            const float mine = quarter == 0 ? o[0] : quarter == 1 ? o[1] : quarter == 2 ? o[2] : o[3];
-            give(REV ? len - 1 - u - quarter : u + quarter, mine);
         }
         for (; u < len; ++u) {
             const int t = REV ? len - 1 - u : u;

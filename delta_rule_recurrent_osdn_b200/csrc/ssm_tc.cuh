@@ -26,8 +26,10 @@
 // Rows past a sequence's end inside its last tile belong to the next sequence: the rows of B, X
 // and V' are zeroed in shared memory before a product sums over them.
 //
-// Warp roles: 0 TMA loads (two tiles each of C, B and X), 1 MMA issue, 2-3 the gates (softplus, sums of log decays),
-// 4-7 the state, 8-11 V', 12-15 the output rows, 16-23 P.
+// Warp roles: 0 TMA loads (two tiles each of C, B and X), 1 MMA issue, 2-3 the gates (softplus,
+// sums of log decays), 4-7 the state, 8-15 V', 16-19 the output rows, 20-27 P.  (V' by one
+// warpgroup is on the chain from one state to the next: 99 against 96 us at B=4, T=4096, H=16,
+// Dk=Dv=128, 261 against 246 at T=65,536 with Dv=64.)
 // Hand-offs are mbarriers with bounded waits; a role that gives up leaves its loop, the others
 // run into their own bounds, and everything in flight is waited for before the CTA leaves.
 #pragma once
@@ -72,16 +74,16 @@ template <int DQ, int MODE> struct TcsSmem {
     static constexpr bool OUT = MODE == TCS_FWD;
     static constexpr uint32_t KB = DQ / 64 * 16384, QB = OUT ? KB : 0;
     static constexpr uint32_t Q = 0, K = QB, V = QB + KB, STAGE = V + 16384;
-    static constexpr int NT = OUT ? 2 : TCS_TERMS;    // bf16 terms of V'
+    static constexpr int NT = MODE == TCS_SAVE ? TCS_TERMS : 2;  // bf16 terms of V'
     static constexpr uint32_t VP = 2 * STAGE;
     static constexpr uint32_t S = VP + NT * 16384;    // the state as an operand (or image)
-    static constexpr uint32_t GATE = S + (OUT ? 16384 : TCS_TERMS * 16384);
+    static constexpr uint32_t GATE = S + (OUT ? 16384 : MODE == TCS_SAVE ? TCS_TERMS * 16384 : 0);
     static constexpr uint32_t GATE_BYTES = 1664;
     static constexpr uint32_t BAR = GATE + TCS_GATES * GATE_BYTES;
     static constexpr uint32_t TMEM_SLOT = BAR + (27 + 2 * TCS_GATES) * 8 + 8;
     static constexpr size_t BYTES = TMEM_SLOT + 16 + 1024;  // + alignment slack
-    static constexpr int THREADS = OUT ? 768 : 512;
-    static constexpr int VW = OUT ? 1 : 2;            // warpgroups that make V'
+    static constexpr int THREADS = OUT ? 896 : 512;
+    static constexpr int VW = 2;            // warpgroups that make V'
     // tensor memory: G / P (two buffers), B^T V' (its terms side by side), C S^T, P X
     static constexpr uint32_t COL_G = 0, COL_U = OUT ? 256 : 0, COL_Y1 = 384, COL_Y2 = 448;
     static constexpr uint32_t COLS = OUT ? 512 : 256;
@@ -306,7 +308,7 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     const uint32_t tmem = *tmem_slot;
     const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
 
-    // FWD: the launch's 6 x 80 registers are shared out 64 + 112 + 72 + 88 + 72 + 72
+    // FWD: the launch's 7 x 72 registers are shared out 64 + 104 + 2 x 56 + 80 + 2 x 72
     if (warp < 4) {
         if constexpr (OUT) tc::reg_dec<64>();
     if (warp == 0) {
@@ -414,7 +416,7 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
     }
     } else if (warp < 8) {
-        if constexpr (OUT) tc::reg_inc<112>();
+        if constexpr (OUT) tc::reg_inc<104>();
         // ------------------------------------------------------------ state
         const int r = tid - 128;  // key channel
         const bool on = DQ == 128 || r < DQ;
@@ -530,11 +532,11 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         if (!OUT && lane == 0) tc::bulk_wait_all();
     } else if (warp < 8 + 4 * L::VW) {
-        if constexpr (OUT) tc::reg_dec<72>();
+        if constexpr (OUT) tc::reg_dec<56>();
         // ------------------------------------------------------------ V'
         const int r = tid & 127, b = r >> 4;  // token of the chunk
         constexpr int NJ = 8 / L::VW;         // 8-channel groups of a thread
-        const int j0 = OUT ? 0 : (warp - 8) / 4 * NJ;
+        const int j0 = (warp - 8) / 4 * NJ;
         for (int i = 0; i < nch; ++i) {
             if (!wait(&gate_full[i % TCS_GATES], i / TCS_GATES) || !wait(&v_full[i & 1], i >> 1)) break;
             const TcsGate* gt = gate(i);
@@ -587,10 +589,10 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
         }
     } else if constexpr (OUT) {
-    if (warp < 16) {
-        tc::reg_inc<88>();
+    if (warp < 20) {
+        tc::reg_inc<80>();
         // ------------------------------------------------------------ output rows
-        const int r = tid - 384;  // token of the chunk
+        const int r = tid & 127;  // token of the chunk
         const float skip = p.D ? p.D[h] : 0.f;
         auto output = [&](int i) -> bool {
             const TcsGate* gt = gate(i);
@@ -642,11 +644,10 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         for (int i = 0; i < nch; ++i)
             if (!wait(&gate_full[i % TCS_GATES], i / TCS_GATES) || !output(i)) break;
     } else {
-        tc::reg_dec<72>();
         // ------------------------------------------------------------ P
         // two warpgroups share P's columns by sub-blocks; P's 16 columns of sub-block b lie over the
         // first half of their own scores, packed
-        const int wg = (warp - 16) >> 2, wq = warp & 3;
+        const int wg = (warp - 20) >> 2, wq = warp & 3;
         const int r = 32 * wq + lane, rb = r >> 4;
         for (int i = 0; i < nch; ++i) {
             if (!wait(&gate_full[i % TCS_GATES], i / TCS_GATES)) break;

@@ -169,7 +169,7 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             load_term(0, imr);
             load_term(1, imr + L::TERM);
             // what the CTA that follows here about a round later will load, into L2 meanwhile: its
-            // first loads then do not wait for HBM (156 -> 128 us at the 340M shape)
+            // first loads then do not wait for HBM (156 -> 135 us at the 340M shape)
             const int64_t ahead = (int64_t)blockIdx.x + p.round, aslot = ahead / p.H;
             int an, achunk;
             if (aslot < p.slots && token_block(p.cu, p.N, p.T, TCS_L, aslot, an, achunk)) {
