@@ -1,13 +1,15 @@
 """Benchmark of the OSDN forward pass (phase 1 scan + phase 2 chunked delta rule) on B200.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
-                    [--workload 1p3b|340m|long|varlen|decode]
+                    [--workload 1p3b|340m|long|varlen|decode|bwd|layer|layer_bwd|layer_step]
 
 One step is one ``osdn_fwd`` call -- the whole hot path: both phases, four kernels -- over one
 batch of seeded synthetic inputs resident in HBM.  The default workload is the 1.3B-layer shape
 (B=4, T=4096, H=16, d_k=d_v=128, bf16 I/O, APF on, eta=0.05); ``340m`` (B=8, T=2048, H=8, no
 APF), ``long`` (B=1, T=65536, H=16, S_0 and d_0 passed in) and ``varlen`` (32 packed sequences
 of U[128, 8192] tokens, H=16) are the other forward shapes; ``decode`` times ``osdn_step``.
+``layer``, ``layer_bwd`` and ``layer_step`` time the operators around the mixer one after another
+(short convolution, selective scan, gated head norm) with the 1.3B-layer shape's heads.
 Each timed step is bracketed by CUDA events on the launching stream, and a 256 MiB write
 between steps flushes the 126 MB L2 (outside the events).  Prints one JSON line on rank 0.
 
@@ -676,6 +678,169 @@ def bench_bwd(args):
     return 0
 
 
+LAYER = dict(B=4, T=4096, H=16, Dk=128, Dv=128, W=4, seed=11)  # the 1.3B-layer shape
+LAYER_STEP_N = 256  # sequences of a decode step, as in the decode workload
+LAYER_DESC = {
+    "layer": "short convolution, selective scan and gated head norm, forward",
+    "layer_bwd": "short convolution, selective scan and gated head norm, backward",
+    "layer_step": "short convolution, selective scan and gated head norm, one token per sequence",
+}
+# the kernels that one step of each launches
+LAYER_LAUNCHES = {"layer": 3, "layer_bwd": 8, "layer_step": 3}
+
+
+def layer_bytes(workload, tokens, N, H, Dk, Dv, W, es=2):
+    """HBM bytes that the three calls of a step cannot do without, each call reading its inputs and
+    writing its outputs once (weights of a few KB not counted).  One group: b and c have a head of
+    their own each."""
+    v, k = tokens * H * Dv * es, tokens * H * Dk * es  # x, y, gate; b, c
+    dt, S, conv = tokens * H * 4, N * H * Dv * Dk * 4, N * (W - 1) * H * Dv * es
+    if workload == "layer":  # conv: x, y, stateT; scan: x, b, c, dt, y, ST; norm: f, gate, out
+        return (2 * v + conv) + (2 * v + 2 * k + dt + S) + 3 * v
+    if workload == "layer_step":  # states are read and written
+        return (2 * v + 2 * conv) + (2 * v + 2 * k + dt + 2 * S) + 3 * v
+    # norm: f, gate, d out -> df, dgate; scan: x, b, c, dt, dy -> dx, db, dc, ddt; conv: x, dy -> dx
+    return 5 * v + (3 * v + 4 * k + 2 * dt) + 3 * v
+
+
+def layer_calls(workload, d, osdn):
+    """One step of a layer workload over the tensors d: the operators through their public calls,
+    each fed with what the one before gave."""
+    if workload == "layer_step":
+        u = osdn.osdn_conv_step(d["u"], d["w"], d["conv_state"], y=d["cu"])
+        o = osdn.osdn_ssm_step(u, d["dt"], d["A"], d["b"], d["c"], d["S"], D=d["D"], y=d["o"])
+    else:
+        u, _ = osdn.osdn_conv_fwd(d["u"], d["w"], y=d["cu"], stateT=d["conv_state"])
+        o = None
+        if workload == "layer":
+            o, _ = osdn.osdn_ssm_fwd(u, d["dt"], d["A"], d["b"], d["c"], D=d["D"], y=d["o"],
+                                     ST=d["S"], workspace=d["ws"])
+    return osdn.osdn_norm_fwd(o, gate=d["z"], w_post=d["wn"], x_out=d["out"])[0]
+
+
+def layer_grads(d, osdn):
+    """The backward step: from d out to the gradients of everything, given the forward's tensors."""
+    gn = osdn.osdn_norm_bwd(d["o"], d["dout"], gate=d["z"], w_post=d["wn"], workspace=d["ws_n"])
+    gs = osdn.osdn_ssm_bwd(d["cu"], d["dt"], d["A"], d["b"], d["c"], gn["df"], D=d["D"],
+                           workspace=d["ws_s"])
+    gc = osdn.osdn_conv_bwd(d["u"], d["w"], gs["dx"], workspace=d["ws_c"])
+    return gc["dx"]
+
+
+def layer_tensors(workload, dev, rank, osdn):
+    import torch
+    L = LAYER
+    lead = (LAYER_STEP_N,) if workload == "layer_step" else (L["B"], L["T"])
+    N, H, Dk, Dv, W = lead[0], L["H"], L["Dk"], L["Dv"], L["W"]
+    g = torch.Generator().manual_seed(L["seed"] + 1000 * rank)
+    mk = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    half = lambda *s: mk(*s).to(dev, torch.bfloat16)  # noqa: E731
+    d = dict(u=half(*lead, H, Dv), z=half(*lead, H, Dv), b=half(*lead, H, Dk), c=half(*lead, H, Dk),
+             dt=(mk(*lead, H) - 3.0).to(dev), A=-torch.linspace(1.0, 16.0, H).to(dev),
+             D=torch.ones(H, device=dev), w=(0.3 * mk(H * Dv, W)).to(dev),
+             wn=torch.ones(Dv, device=dev))
+    d["b"] *= Dk ** -0.5
+    d["conv_state"] = torch.zeros(N, W - 1, H * Dv, dtype=torch.bfloat16, device=dev)
+    d["S"] = torch.zeros(N, H, Dv, Dk, device=dev)
+    d["cu"], d["o"], d["out"] = (torch.empty_like(d["u"]) for _ in range(3))
+    if workload != "layer_step":
+        B, T = lead
+        scratch = lambda n: torch.empty(max(n, 1), dtype=torch.uint8, device=dev)  # noqa: E731
+        d["ws"] = scratch(osdn.osdn_ssm_fwd_workspace_bytes(B, T, H, Dk, Dv))
+        if workload == "layer_bwd":
+            io = osdn.OSDN_BF16
+            layer_calls("layer", d, osdn)
+            d["dout"] = half(*lead, H, Dv)
+            d["ws_s"] = scratch(osdn.LIB.osdn_ssm_bwd_workspace_bytes(0, B, T, H, Dk, Dv, io))
+            d["ws_c"] = scratch(osdn.LIB.osdn_conv_bwd_workspace_bytes(B, T, H * Dv, W))
+            d["ws_n"] = scratch(osdn.LIB.osdn_norm_bwd_workspace_bytes(B * T * H, Dv))
+    return d
+
+
+def bench_layer(args):
+    """The layer operators around the token mixer, one after another as a layer uses them."""
+    import torch
+    from delta_rule_recurrent_osdn_b200 import osdn
+
+    rank, world, local = dist_setup(args.gpus)
+    dev = torch.device("cuda", local)
+    torch.cuda.set_device(dev)
+    d = layer_tensors(args.workload, dev, rank, osdn)
+    grads = args.workload == "layer_bwd"
+    stream = torch.cuda.current_stream(dev)
+    flush = torch.empty(FLUSH_BYTES, dtype=torch.uint8, device=dev)
+
+    def step():
+        return layer_grads(d, osdn) if grads else layer_calls(args.workload, d, osdn)
+
+    def timed(fn, steps):
+        events = [[torch.cuda.Event(enable_timing=True) for _ in range(2)] for _ in range(steps)]
+        barrier(world, dev)
+        torch.cuda.synchronize(dev)
+        for i in range(steps):
+            flush.fill_(i & 0xFF)  # outside the events
+            events[i][0].record(stream)
+            fn()
+            events[i][1].record(stream)
+        torch.cuda.synchronize(dev)
+        barrier(world, dev)
+        return max_over_ranks(sum(a.elapsed_time(b) for a, b in events), world, dev)
+
+    for _ in range(args.warmup):
+        flush.fill_(1)
+        step()
+    with ClockSampler(local) as clk:
+        total_ms = timed(step, args.steps)
+    if osdn.osdn_get_device_status() != osdn.OSDN_OK:
+        raise RuntimeError("device status not OK after the timed region")
+
+    # ---- end to end: the step's tokens from pinned host memory, its result back, copies timed
+    names = ["u", "z", "b", "c", "dt"] + (["dout", "cu", "o"] if grads else [])
+    pinned = {k: d[k].cpu().pin_memory() for k in names}
+    back = torch.empty(d["u"].shape, dtype=d["u"].dtype).pin_memory()
+    h2d = sum(t.numel() * t.element_size() for t in pinned.values())
+    d2h = back.numel() * back.element_size()
+
+    def e2e_step():
+        for k, t in pinned.items():
+            d[k].copy_(t, non_blocking=True)
+        back.copy_(step(), non_blocking=True)
+
+    for _ in range(3):
+        e2e_step()
+    e2e_ms = timed(e2e_step, args.steps)
+    if rank == 0:
+        hbm, _, kind = read_peaks()
+        L = LAYER
+        N = LAYER_STEP_N if args.workload == "layer_step" else L["B"]
+        tokens = N if args.workload == "layer_step" else N * L["T"]
+        byts = layer_bytes(args.workload, tokens, N, L["H"], L["Dk"], L["Dv"], L["W"])
+        ms = total_ms / args.steps
+        achieved = byts / (ms / 1e3) / 1e9
+        print(json.dumps({
+            "metric": f"tokens/s ({LAYER_DESC[args.workload]}) at 1.3B-layer heads; % of HBM roofline",
+            "value": world * tokens / (ms / 1e3), "unit": "tokens/s", "n_gpus": world,
+            "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms,
+            "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16",
+            "data": "synthetic",
+            "config": {"workload": LAYER_DESC[args.workload], "N": N, "T": tokens // N, "H": L["H"],
+                       "d_k": L["Dk"], "d_v": L["Dv"], "conv_width": L["W"], "io": "bf16",
+                       "l2": "flushed between timed steps (256 MiB write)"},
+            "roofline": {"bound": "hbm", "scope": "one step, every call's inputs and outputs once",
+                         "achieved": achieved, "peak": hbm, "peak_kind": f"{kind} hbm_gbs",
+                         "unit": "GB/s", "frac": achieved / hbm, "traffic": None,
+                         "algorithmic_bytes_per_launch": byts},
+            "cpu_baseline": None,
+            "e2e": {"value": world * tokens * args.steps / (e2e_ms / 1e3), "unit": "tokens/s",
+                    "h2d_bytes_per_step": h2d, "d2h_bytes_per_step": d2h},
+            "gpu_launches": LAYER_LAUNCHES[args.workload] * args.steps, "clocks": clk.summary(),
+            "gpu": torch.cuda.get_device_name(dev)}))
+    if world > 1:
+        import torch.distributed as dist
+        dist.destroy_process_group()
+    return 0
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -684,14 +849,22 @@ def main(argv=None):
     ap.add_argument("--impl", choices=["ours", "reference"], default="ours")
     ap.add_argument("--cpu-seconds", type=float, default=12.0)
     ap.add_argument("--no-cpu-baseline", action="store_true")
-    ap.add_argument("--workload", choices=list(FORWARD) + ["decode", "bwd"], default="1p3b",
-                    help="a forward-pass shape (default: the 1.3B layer), decode (osdn_step) or "
-                         "bwd (osdn_bwd at the 1.3B-layer shape)")
+    ap.add_argument("--workload", choices=list(FORWARD) + ["decode", "bwd"] + list(LAYER_DESC),
+                    default="1p3b",
+                    help="a forward-pass shape (default: the 1.3B layer), decode (osdn_step), "
+                         "bwd (osdn_bwd at the 1.3B-layer shape) or the operators around the "
+                         "mixer: layer, layer_bwd, layer_step")
     args = ap.parse_args(argv)
     if args.warmup < 3:
         ap.error("--warmup must be at least 3")
+    if args.impl == "reference" and args.workload in LAYER_DESC:
+        print(json.dumps({"impl": "reference", "unavailable":
+                          "the oracle states the token mixer, not the operators around it"}))
+        return 0
     if args.impl == "reference":
         return bench_reference(args)
+    if args.workload in LAYER_DESC:
+        return bench_layer(args)
     if args.workload == "decode":
         return bench_decode(args)
     if args.workload == "bwd":
