@@ -260,35 +260,40 @@ bool make_chunk_map(CUtensorMap* m, const void* base, int D, int heads, int64_t 
 //   a chunk's time per chunk: two segments win from about 8 chunks on).
 //   Packed sequences, whose lengths the host does not know: twice the tokens that an even split
 //   of the whole would give a CTA, so only sequences far above the average are cut.
-SsmSegments ssm_segments(bool packed, int64_t rows, int64_t N, int64_t T, int H, int Dk, int Dv) {
-    const int64_t nvt = Dv / TCS_BV, chunks = ceil_div(packed ? rows : T, TCS_L), sms = 148;
+//   The backward pass's chains go both ways (dirs 2), a CTA each, and their first launch costs
+//   more (three terms of V'): three segments of 8 chunks at least (B=1, T=7112, H=16, Dv=64: 252
+//   us uncut, 216 in four; two segments at T=2048: 85 uncut, 96 cut), and packed sequences stay
+//   whole (six of up to 4096 tokens, H=16: 229, cut 263).
+SsmSegments ssm_segments(bool packed, int64_t rows, int64_t N, int64_t T, int H, int Dk, int Dv,
+                         int dirs) {
+    const int64_t nvt = dirs * Dv / TCS_BV, chunks = ceil_div(packed ? rows : T, TCS_L), sms = 148;
     SsmSegments s = {INT_MAX, N, 0, 0, 0};
     int64_t len = chunks;
-    if (packed) {
+    if (packed && dirs == 1) {
         len = 2 * ceil_div(chunks * H * nvt, sms);
         len = len < 4 ? 4 : len;
-    } else if (N * H * nvt > 0) {
-        const int64_t most = chunks / 4, fit = sms / (N * H * nvt);
+    } else if (!packed && N * H * nvt > 0) {
+        const int64_t most = chunks / (4 * dirs), fit = sms / (N * H * nvt);
         const int64_t segs = fit < most ? fit : most;
-        if (segs >= 2) len = ceil_div(chunks, segs);
+        if (segs > dirs) len = ceil_div(chunks, segs);
     }
     if (len < chunks && len * TCS_L < INT_MAX) {
         s.seg = (int)(len * TCS_L);
         s.slots = rows / s.seg + N;
         s.state = 0;
-        s.decay = up256((size_t)s.slots * H * Dv * Dk * 4);
-        s.bytes = s.decay + up256((size_t)s.slots * H * 4);
+        s.decay = up256((size_t)dirs * s.slots * H * Dv * Dk * 4);
+        s.bytes = s.decay + up256((size_t)dirs * s.slots * H * 4);
     }
     return s;
 }
 
-// q, k: [rows][G][DQ], v, v2: [rows][H][nvt * 64] (v2: dy, used by SAVE alone).  slots: the
+// q, k: [rows][G][DQ], v, v2: [rows][H][nvt * 64] (v2: dy, for both directions).  slots: the
 // segments' numbers, or the sequences'.
 template <int DQ, int MODE>
 osdn_status_t launch_tc_chain(const void* q, const void* k, const void* v, const void* v2,
                               const TcsArgs& a, int64_t slots, cudaStream_t stream) {
     using L = TcsSmem<DQ, MODE>;
-    const int64_t ctas = slots * a.H * a.nvt * (MODE == TCS_SAVE ? 2 : 1);
+    const int64_t ctas = slots * a.H * a.nvt * (L::BOTH ? 2 : 1);
     if (ctas == 0) return OSDN_OK;
     if (ctas > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
     CUtensorMap mq, mk, mv, mv2;
@@ -317,6 +322,10 @@ osdn_status_t check_ssm(int32_t H, int32_t G, int32_t Dk, int32_t Dv) {
     return H > 65535 ? OSDN_ERR_UNSUPPORTED : OSDN_OK;
 }
 
+SsmSegments ssm_bwd_segments(int64_t rows, int64_t N, int64_t T, int H, int Dk, int Dv) {
+    return ssm_segments(rows != N * T, rows, N, T, H, Dk, Dv, 2);
+}
+
 // Workspace of osdn_ssm_bwd, each part rounded up to 256 bytes.  fp32 tokens: the heads' dc and
 // db, the state behind each block of SSM_BLOCK tokens.  bf16 tokens: the states in front of and
 // the gradients behind each chunk as images of bf16 terms, the heads' dc and db when heads share
@@ -337,7 +346,8 @@ SsmBwdWorkspace ssm_bwd_workspace(int64_t rows, int64_t N, int64_t T, int32_t H,
     const size_t th = (size_t)rows * H, slots = (size_t)ssm_slots(rows, N, tc ? TCS_L : SSM_BLOCK);
     const size_t heads = !tc || G < H ? th * Dk * 4 : 0, shares = tc ? 4 : 1;
     const size_t image = slots * H * Dk * Dv * (tc ? TCS_TERMS * 2 : 4);
-    w.seg = take(tc ? 0 : ssm_f32_segments(rows, N, T, H, Dk, Dv).bytes);
+    w.seg = take((tc ? ssm_bwd_segments(rows, N, T, H, Dk, Dv)
+                     : ssm_f32_segments(rows, N, T, H, Dk, Dv)).bytes);
     w.dch = take(heads);
     w.dbh = take(heads);
     w.ckpt = take(image);
@@ -421,10 +431,16 @@ template <int DK, int DV> osdn_status_t launch_ssm_bwd_tc(const SsmBwdCall& k) {
     TcsArgs a = {};
     a.dt = k.dt; a.A = k.A; a.dt_bias = k.dt_bias; a.softplus = k.softplus; a.cu = k.cu;
     a.rows = k.rows; a.N = (int)k.N; a.T = k.T; a.H = k.H; a.G = k.G; a.nvt = DV / TCS_BV;
-    a.seg = INT_MAX;
+    const SsmSegments sg = ssm_bwd_segments(k.rows, k.N, k.T, k.H, DK, DV);
+    a.seg = sg.seg;
+    a.seg_state = f32(w.seg + sg.state); a.seg_decay = f32(w.seg + sg.decay);
     a.S_in = k.S0; a.img = k.ws + w.ckpt; a.img_r = k.ws + w.ckpt_r;
     a.dST = k.dST; a.dS0 = k.dS0;
-    osdn_status_t st = launch_tc_chain<DK, TCS_SAVE>(k.c, k.b, k.x, k.dy, a, k.N, k.stream);
+    osdn_status_t st = OSDN_OK;
+    if (a.seg != INT_MAX)
+        st = launch_tc_chain<DK, TCS_SEG_SAVE>(k.c, k.b, k.x, k.dy, a, sg.slots, k.stream);
+    if (st == OSDN_OK)
+        st = launch_tc_chain<DK, TCS_SAVE>(k.c, k.b, k.x, k.dy, a, sg.slots, k.stream);
     if (st != OSDN_OK) return st;
     TcgArgs g = {};
     g.dt = k.dt; g.A = k.A; g.dt_bias = k.dt_bias; g.D = k.D; g.softplus = k.softplus;
@@ -593,7 +609,7 @@ osdn_status_t osdn_ssm_fwd(const void* x, const float* dt, const float* A, const
         t.S_in = S0; t.y = static_cast<__nv_bfloat16*>(y); t.S_out = ST; t.cu = cu_seqlens;
         t.rows = rows; t.N = (int)N; t.T = T; t.H = H; t.G = G; t.softplus = softplus;
         t.nvt = Dv / TCS_BV;
-        const SsmSegments sg = ssm_segments(cu_seqlens != nullptr, rows, N, T, H, Dk, Dv);
+        const SsmSegments sg = ssm_segments(cu_seqlens != nullptr, rows, N, T, H, Dk, Dv, 1);
         t.seg = sg.seg;
         t.seg_state = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sg.state);
         t.seg_decay = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sg.decay);
@@ -610,7 +626,7 @@ size_t osdn_ssm_fwd_workspace_bytes(int32_t num_seqs, int32_t B, int32_t T, int3
         (Dv != 64 && Dv != 128) || (io != OSDN_BF16 && io != OSDN_F32) || (int64_t)B * T == 0)
         return 0;
     const int64_t rows = (int64_t)B * T, N = num_seqs > 0 ? num_seqs : B;
-    return io == OSDN_BF16 ? ssm_segments(num_seqs > 0, rows, N, T, H, Dk, Dv).bytes
+    return io == OSDN_BF16 ? ssm_segments(num_seqs > 0, rows, N, T, H, Dk, Dv, 1).bytes
                            : ssm_f32_segments(rows, N, T, H, Dk, Dv).bytes;
 }
 

@@ -10,8 +10,10 @@
 //
 // Some 20 operations per element and two to four sums over the row: bound by HBM if those stay
 // cheap, so a row is held in the registers of TPR threads, sums go by shuffles (and through shared
-// memory when a row takes several warps), and the forward pass has the next row's loads in flight
-// while it works on one.
+// memory when a row takes several warps), and the next row's loads are in flight while one is
+// worked on.  Forward: 57 us at 16384 bf16 rows of 2048 with residual, gate and both norms (336 MB:
+// 51 us at copy speed).  Backward: 47 us at 131,072 rows of 128 with a gate (168 MB: 26 us), bound
+// by issue: some 40 operations a value, and sums of weight gradients that cross rows.
 #pragma once
 
 #include "mixer_common.cuh"

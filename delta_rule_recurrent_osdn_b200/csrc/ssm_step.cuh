@@ -4,7 +4,8 @@
 // 2 x 4 Dk Dv bytes per (sequence, head) and everything else a few hundred.
 //
 // One CTA of Dv / 8 warps per (sequence, head).  A warp owns 8 state rows, a lane Dk / 32
-// neighbouring columns of each; all 8 row loads are issued before the first use.
+// neighbouring columns of each; all 8 row loads are issued before the first use.  256 sequences x
+// 16 heads of 128 x 128: 83 us, 539 MB at 99% of copy speed.
 #pragma once
 
 #include "mixer_common.cuh"

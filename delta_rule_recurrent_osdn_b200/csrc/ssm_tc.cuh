@@ -30,6 +30,9 @@
 // sums of log decays), 4-7 the state, 8-15 V', 16-19 the output rows, 20-27 P.  (V' by one
 // warpgroup is on the chain from one state to the next: 99 against 96 us at B=4, T=4096, H=16,
 // Dk=Dv=128, 261 against 246 at T=65,536 with Dv=64.)
+// Bound by the chain: about 3 us a chunk at 4096 tokens (four products wait for one another
+// through shared and tensor memory, and the P and output warps issue some 2000 instructions a
+// scheduler), 96 us against 42 for its 274 MB at copy speed.
 // Hand-offs are mbarriers with bounded waits; a role that gives up leaves its loop, the others
 // run into their own bounds, and everything in flight is waited for before the CTA leaves.
 #pragma once
@@ -48,8 +51,8 @@ constexpr int TCS_GATES = 8; // chunks whose gates are kept: they are made well 
 // What a launch of the chain does: the forward pass; for the backward pass the states S in front
 // of every chunk and, backwards in time over c and dy, the gradients R that reach the states
 // behind them, both stored as images of TCS_TERMS bf16 terms (half the CTAs each); what each
-// segment of a sequence adds to a zero state.
-enum { TCS_FWD = 0, TCS_SAVE = 1, TCS_SEG = 2 };
+// segment of a sequence adds to a zero state, for FWD or (SEG_SAVE, both directions) for SAVE.
+enum { TCS_FWD = 0, TCS_SAVE = 1, TCS_SEG = 2, TCS_SEG_SAVE = 3 };
 constexpr int TCS_TERMS = 3;
 
 struct TcsArgs {
@@ -64,8 +67,8 @@ struct TcsArgs {
     float* dS0;                    // SAVE: dS0, or null
     const int32_t* cu;
     int64_t rows;
-    float* seg_state;              // SEG writes, FWD reads: [slot][H][nvt][64][DQ]
-    float* seg_decay;              // ... and the segment's whole log2 decay [slot][H]
+    float* seg_state;              // SEG writes, FWD reads: [direction][slot][H][nvt][64][DQ]
+    float* seg_decay;              // ... and the segment's whole log2 decay [direction][slot][H]
     int seg;                       // tokens of a segment (a multiple of TCS_L; INT_MAX: none)
     int N, T, H, G, softplus, nvt;
 };
@@ -74,7 +77,9 @@ template <int DQ, int MODE> struct TcsSmem {
     static constexpr bool OUT = MODE == TCS_FWD;
     static constexpr uint32_t KB = DQ / 64 * 16384, QB = OUT ? KB : 0;
     static constexpr uint32_t Q = 0, K = QB, V = QB + KB, STAGE = V + 16384;
-    static constexpr int NT = MODE == TCS_SAVE ? TCS_TERMS : 2;  // bf16 terms of V'
+    static constexpr bool SEG = MODE == TCS_SEG || MODE == TCS_SEG_SAVE;
+    static constexpr bool BOTH = MODE == TCS_SAVE || MODE == TCS_SEG_SAVE;  // directions
+    static constexpr int NT = BOTH ? TCS_TERMS : 2;  // bf16 terms of V'
     static constexpr uint32_t VP = 2 * STAGE;
     static constexpr uint32_t S = VP + NT * 16384;    // the state as an operand (or image)
     static constexpr uint32_t GATE = S + (OUT ? 16384 : MODE == TCS_SAVE ? TCS_TERMS * 16384 : 0);
@@ -201,9 +206,9 @@ __device__ __forceinline__ void tcs_mma(uint32_t d, uint64_t a, uint64_t b, uint
 }
 
 // Segments.  When there are too few (sequence, head) chains for the machine, sequences are cut into
-// segments of p.seg tokens that run side by side: a first launch (SEG) makes what each segment
-// adds to a zero state, and a segment of the forward pass builds its initial state from S0 and
-// the segments in front of it.
+// segments of p.seg tokens that run side by side: a first launch (SEG, SEG_SAVE) makes what each
+// segment adds to a zero state, and a segment of FWD or SAVE builds its initial state from S0 and
+// the segments in front of it (backwards: from dST and those behind it).
 template <int DQ, int MODE>
 __global__ void __launch_bounds__(TcsSmem<DQ, MODE>::THREADS, 1)
 ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -211,8 +216,8 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     const TcsArgs p) {
     using L = TcsSmem<DQ, MODE>;
     constexpr bool OUT = L::OUT;
-    // SAVE: the second half of the grid goes backwards over q and v2 (c and dy)
-    const bool rev = MODE == TCS_SAVE && blockIdx.x >= gridDim.x / 2;
+    // the second half of the grid goes backwards over q and v2 (c and dy)
+    const bool rev = L::BOTH && blockIdx.x >= gridDim.x / 2;
     const uint32_t block = rev ? blockIdx.x - gridDim.x / 2 : blockIdx.x;
     const CUtensorMap* map_k = rev ? &tm_q : &tm_k;
     const CUtensorMap* map_v = rev ? &tm_v2 : &tm_v;
@@ -230,7 +235,10 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     const int64_t start = (int64_t)seg * p.seg;  // of the segment in its sequence
     if (seg > 0 && start >= count) return;       // a number that no segment has
     const bool last = count - start <= p.seg;
-    if (MODE == TCS_SEG && last) return;
+    if (L::SEG && (rev ? seg == 0 : last)) return;  // adds to no other segment
+    const int base = slot - seg;                 // the sequence's first segment
+    const int segs = last ? seg + 1 : (int)((count + p.seg - 1) / p.seg);
+    const int64_t half = rev ? p.rows / p.seg + p.N : 0;  // backwards: the second set of numbers
     first += start;                              // all uniform over the CTA
     count = last ? count - start : p.seg;
     const int nch = (int)((count + TCS_L - 1) / TCS_L);
@@ -422,14 +430,15 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         const bool on = DQ == 128 || r < DQ;
         float S[TCS_BV];
         const int64_t sbase = (nh * DV + vt * TCS_BV) * DQ + r;  // stored [value][key]
-        const float* s_in = rev ? p.dST : MODE == TCS_SEG ? nullptr : p.S_in;
+        const float* s_in = L::SEG ? nullptr : rev ? p.dST : p.S_in;
 #pragma unroll
         for (int j = 0; j < TCS_BV; ++j)
             S[j] = on && s_in ? s_in[sbase + (int64_t)j * DQ] : 0.f;
-        if constexpr (OUT) {
-            for (int e = slot - seg; on && e < slot; ++e) {  // the segments in front
-                const float d = ex2f(p.seg_decay[(int64_t)e * p.H + h]);
-                const float* a = p.seg_state + (((int64_t)e * p.H + h) * p.nvt + vt) * (TCS_BV * DQ) + r;
+        if constexpr (!L::SEG) {  // the segments in front, the nearest last
+            for (int e = rev ? base + segs - 1 : base; on && e != slot; e += rev ? -1 : 1) {
+                const int64_t at = (half + e) * p.H + h;
+                const float d = ex2f(p.seg_decay[at]);
+                const float* a = p.seg_state + (at * p.nvt + vt) * (TCS_BV * DQ) + r;
 #pragma unroll
                 for (int j = 0; j < TCS_BV; ++j) S[j] = fmaf(d, S[j], a[j * DQ]);
             }
@@ -458,7 +467,7 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 tc::fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_full);
-            } else if constexpr (MODE == TCS_SEG) {
+            } else if constexpr (L::SEG) {
                 total += gate(i)->bh[8];
             } else {
                 // images: rows of 128 bytes as the products read them, the terms one after another
@@ -515,8 +524,8 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(u_free);
         }
-        if constexpr (MODE == TCS_SEG) {
-            const int64_t at = (int64_t)slot * p.H + h;
+        if constexpr (L::SEG) {
+            const int64_t at = (half + slot) * p.H + h;
             if (on && OSDN_IN_BOUNDS(slot, p.rows / p.seg + p.N)) {
 #pragma unroll
                 for (int j = 0; j < TCS_BV; ++j)
@@ -525,7 +534,7 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
         } else {
             float* s_out = rev ? p.dS0 : p.S_out;
-            if (on && s_out && last && OSDN_IN_BOUNDS(nh, (int64_t)p.N * p.H)) {
+            if (on && s_out && (rev ? seg == 0 : last) && OSDN_IN_BOUNDS(nh, (int64_t)p.N * p.H)) {
 #pragma unroll
                 for (int j = 0; j < TCS_BV; ++j) s_out[sbase + (int64_t)j * DQ] = S[j];
             }

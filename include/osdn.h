@@ -294,7 +294,7 @@ OSDN_API osdn_status_t osdn_step(const void* q, const void* k, const void* v, co
  *   x, y    [B,T,C] io dtype (C = all channels of a token: q, k, v of [B,T,H,D] have C = H * D).
  *   weight  [C,W] float32.   bias [C] float32, or NULL.   silu 0 or 1.
  *   state0  [N,W-1,C] io dtype, or NULL.   stateT [N,W-1,C] io dtype, written, or NULL.
- * W in 2..4, C >= 1 (16-byte accesses when C is a multiple of 8 (bf16) or 4 (f32)).
+ * W in 2..4, C >= 1 (fastest when C is a multiple of 4).
  * y and stateT must not overlap anything else.
  */
 OSDN_API osdn_status_t osdn_conv_fwd(const void* x, const float* weight, const float* bias,
@@ -335,7 +335,7 @@ OSDN_API osdn_status_t osdn_conv_bwd(const void* x, const float* weight, const f
  *   D       [H] float32, or NULL for 0.   dt_bias [H] float32, or NULL for 0.
  *   S0, ST  [N,H,Dv,Dk] float32 (as for osdn_chunk_fwd); S0 NULL for zeros, ST NULL to skip.
  *   workspace  osdn_ssm_fwd_workspace_bytes(...) bytes, 256-byte aligned (NULL if that is 0).
- * Dk, Dv in {64, 128}; H a multiple of G.  y and ST must not overlap anything else.
+ * Dk, Dv in {64, 128}; H <= 65535 and a multiple of G.  y and ST must not overlap anything else.
  */
 OSDN_API size_t osdn_ssm_fwd_workspace_bytes(int32_t num_seqs, int32_t B, int32_t T, int32_t H,
                                              int32_t Dk, int32_t Dv, osdn_dtype_t io);

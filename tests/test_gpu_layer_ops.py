@@ -193,6 +193,10 @@ SCANS = [  # io, lens, packed, H, G, Dk, Dv, D, bias, state, softplus
     ("bf16", [1100], False, 2, 1, 64, 128, True, True, True, True),
     ("bf16", [1400, 3, 0, 512, 200], True, 2, 2, 128, 64, True, True, True, True),
     ("bf16", [1, 1025], True, 3, 1, 128, 128, False, True, False, True),
+    # ... in the backward pass too
+    ("bf16", [3200], False, 1, 1, 128, 64, True, True, True, True),
+    ("bf16", [3109], True, 2, 1, 64, 64, True, True, True, True),
+    ("bf16", [3081, 3081], False, 1, 1, 64, 128, False, True, False, True),
 ]
 SCAN_IDS = [f"{s[0]}-{'.'.join(map(str, s[1]))}-H{s[3]}G{s[4]}k{s[5]}v{s[6]}" for s in SCANS]
 
@@ -346,6 +350,7 @@ def test_scan_keeps_sequences_apart(osdn, io):
 
 
 @pytest.mark.parametrize("io,lens,packed", [("bf16", [1100], False), ("bf16", [700, 900, 1], True),
+                                            ("bf16", [3200], False),
                                             ("f32", [150], False), ("f32", [301, 7, 290], True)])
 def test_scan_slow_decay(osdn, io, lens, packed):
     """States that hardly decay: what a sequence starts from, and every segment and chunk, reaches
