@@ -1,4 +1,5 @@
-"""B200-native forward pass of the Online Scaled DeltaNet (OSDN) token mixer.
+"""B200-native Online Scaled DeltaNet (OSDN) token mixer and the operators of a layer around it
+(short causal convolution, selective scan, block norm).
 
 The compute lives in ``libosdn.so`` (hand-written sm_100a CUDA kernels behind a C ABI,
 declared in ``include/osdn.h``).  Import ``delta_rule_recurrent_osdn_b200.osdn`` for the thin
