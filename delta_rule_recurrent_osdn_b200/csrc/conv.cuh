@@ -18,6 +18,7 @@
 namespace osdn {
 
 constexpr int CONV_THREADS = 128;
+constexpr int CONV_MAX_C = 1 << 30;  // a channel's number, rounded up to whole blocks, is an int
 // Channels of a thread.  With 8 (16 bytes of bf16) the filters, the last inputs and the loads in
 // flight leave too few warps: 4 x 4096 tokens of 2048 channels 57 us against 34, the gradient at
 // 8 x 2048 of 1024 115 against 47 (L2 cold).

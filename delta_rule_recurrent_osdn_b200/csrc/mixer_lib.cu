@@ -496,7 +496,7 @@ osdn_status_t osdn_conv_fwd(const void* x, const float* weight, const float* bia
     osdn_status_t st = check_tokens(cu_seqlens, num_seqs, B, T, io, &rows, &N);
     if (st != OSDN_OK) return st;
     if (C < 1 || (silu != 0 && silu != 1)) return OSDN_ERR_INVALID_ARG;
-    if (W < 2 || W > 4) return OSDN_ERR_UNSUPPORTED;
+    if (W < 2 || W > 4 || C > CONV_MAX_C) return OSDN_ERR_UNSUPPORTED;
     if (!weight || (rows > 0 && (!x || !y))) return OSDN_ERR_INVALID_ARG;
     const size_t es = io_size(io), xb = (size_t)rows * C * es, sb = (size_t)N * (W - 1) * C * es;
     const Buf in[] = {{x, xb}, {weight, (size_t)C * W * 4}, {bias, (size_t)C * 4}, {state0, sb},
@@ -517,7 +517,7 @@ osdn_status_t osdn_conv_step(const void* x, const float* weight, const float* bi
                              osdn_dtype_t io, void* stream) {
     if (io != OSDN_BF16 && io != OSDN_F32) return OSDN_ERR_INVALID_ARG;
     if (N < 0 || C < 1 || (silu != 0 && silu != 1)) return OSDN_ERR_INVALID_ARG;
-    if (W < 2 || W > 4) return OSDN_ERR_UNSUPPORTED;
+    if (W < 2 || W > 4 || C > CONV_MAX_C) return OSDN_ERR_UNSUPPORTED;
     if (N == 0) return OSDN_OK;
     if (!x || !weight || !state || !y) return OSDN_ERR_INVALID_ARG;
     const size_t xb = (size_t)N * C * io_size(io);
@@ -532,7 +532,7 @@ osdn_status_t osdn_conv_step(const void* x, const float* weight, const float* bi
 }
 
 size_t osdn_conv_bwd_workspace_bytes(int32_t B, int32_t T, int32_t C, int32_t W) {
-    if (B < 0 || T < 0 || C < 1 || W < 2 || W > 4) return 0;
+    if (B < 0 || T < 0 || C < 1 || C > CONV_MAX_C || W < 2 || W > 4) return 0;
     return up256((size_t)conv_bwd_plan((int64_t)B * T, C).row_blocks * (W + 1) * C * 4);
 }
 
@@ -547,7 +547,7 @@ osdn_status_t osdn_conv_bwd(const void* x, const float* weight, const float* bia
     if (st != OSDN_OK) return st;
     if (C < 1 || (silu != 0 && silu != 1) || (dy_io != OSDN_F32 && dy_io != io))
         return OSDN_ERR_INVALID_ARG;
-    if (W < 2 || W > 4) return OSDN_ERR_UNSUPPORTED;
+    if (W < 2 || W > 4 || C > CONV_MAX_C) return OSDN_ERR_UNSUPPORTED;
     if (!weight || !dweight || (rows > 0 && (!x || !dy || !dx))) return OSDN_ERR_INVALID_ARG;
     const size_t need = osdn_conv_bwd_workspace_bytes(B, T, C, W);
     st = check_workspace(workspace, workspace_bytes, need);

@@ -294,7 +294,7 @@ OSDN_API osdn_status_t osdn_step(const void* q, const void* k, const void* v, co
  *   x, y    [B,T,C] io dtype (C = all channels of a token: q, k, v of [B,T,H,D] have C = H * D).
  *   weight  [C,W] float32.   bias [C] float32, or NULL.   silu 0 or 1.
  *   state0  [N,W-1,C] io dtype, or NULL.   stateT [N,W-1,C] io dtype, written, or NULL.
- * W in 2..4, C >= 1 (fastest when C is a multiple of 4).
+ * W in 2..4, 1 <= C <= 2^30 (fastest when C is a multiple of 4).
  * y and stateT must not overlap anything else.
  */
 OSDN_API osdn_status_t osdn_conv_fwd(const void* x, const float* weight, const float* bias,

@@ -699,3 +699,117 @@ def test_two_streams_at_once(osdn):
     for g, w in zip(got, want):
         same(g, w)
     finish(osdn)
+
+
+# ============================================================================ what calls may be
+@pytest.mark.parametrize("io,lens", [("bf16", [150, 150]), ("bf16", [3200]), ("f32", [90, 90])])
+@pytest.mark.parametrize("given", ["S0", "dST"])
+def test_scan_bwd_with_one_of_the_states(osdn, io, lens, given):
+    H, G, Dk, Dv = 2, 1, 64, 64
+    a, rng = scan_inputs(io, lens, H, G, Dk, Dv, True, True, given == "S0", True, seed=9)
+    dy = rounded(rng.standard_normal(a["x"].shape), io)
+    dST = rounded(rng.standard_normal((len(lens), H, Dv, Dk)), "f32") if given == "dST" else None
+    want = scan_ref(a, True, lens, dy=dy, dST=dST)
+    mag = scan_ref(a, True, lens, dy=dy, dST=dST, absolute=True)
+    t = scan_dev(a, io, lens, False)
+    g = scan_bwd(osdn, t, dev(dy, io).reshape(t["x"].shape), dev(dST))
+    finish(osdn)
+    coarse, fine = scan_factors(io, lens, Dk)
+    for name in ("dx", "db", "dc"):
+        close(g[name].reshape(want[name].shape), want[name],
+              U[io] * np.abs(want[name]) + coarse * mag[name], name)
+    close(g["ddt"].reshape(-1, H), want["ddt"],
+          (np.abs(a["A"]) * mag["cancel"] + mag["ddt"]) * fine, "ddt")
+    assert (g["dS0"] is None) == (given == "dST")
+    if given == "S0":
+        close(g["dS0"], want["dS0"], fine * mag["dS0"], "dS0")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_scan_of_growing_states(osdn, io):
+    """A > 0, and steps below 0 (no softplus): states grow by up to e^4 over a sequence."""
+    lens, H, G, Dk, Dv = [200, 200], 2, 2, 64, 64
+    a, rng = scan_inputs(io, lens, H, G, Dk, Dv, True, False, True, False, seed=10)
+    a["dt"] = rounded(rng.uniform(-0.1, 0.1, a["dt"].shape), "f32")
+    a["dt"][:, 0] = rounded(np.abs(a["dt"][:, 0]), "f32")
+    a["A"][:] = rounded([0.4, 0.6], "f32")
+    dy = rounded(rng.standard_normal(a["x"].shape), io)
+    want = scan_ref(a, False, lens, dy=dy)
+    mag = scan_ref(a, False, lens, dy=dy, absolute=True)
+    t = scan_dev(a, io, lens, False)
+    y, ST = scan_fwd(osdn, t, False)
+    g = scan_bwd(osdn, t, dev(dy, io).reshape(t["x"].shape), None, False)
+    finish(osdn)
+    coarse, fine = scan_factors(io, lens, Dk)
+    close(y.reshape(want["y"].shape), want["y"], U[io] * np.abs(want["y"]) + coarse * mag["y"], "y")
+    close(ST, want["ST"], fine * mag["ST"], "ST")
+    for name in ("dx", "db", "dc"):
+        close(g[name].reshape(want[name].shape), want[name],
+              U[io] * np.abs(want[name]) + coarse * mag[name], name)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_thousands_of_tiny_sequences(osdn, io):
+    """More sequences than the convolution has blocks for them, none of more than two tokens."""
+    rng = np.random.default_rng(11)
+    lens = [int(v) for v in rng.integers(0, 3, 5000)]
+    n, C, W = sum(lens), 64, 4
+    a, _ = conv_inputs(io, lens, C, W, True, True)
+    args = (a["x"], a["weight"], a["bias"], a["state0"], True, lens)
+    want, mag = R.conv(*args), R.conv(*args, absolute=True)
+    y, st = osdn.osdn_conv_fwd(dev(a["x"], io).reshape(1, n, C), dev(a["weight"]), dev(a["bias"]),
+                               dev(a["state0"], io), "silu", offsets(lens))
+    close(y.reshape(-1, C), want["y"], U[io] * np.abs(want["y"]) + 80 * E * mag["y"], "y")
+    np.testing.assert_array_equal(host(st), want["stateT"])
+    s, _ = scan_inputs(io, lens, 1, 1, 64, 64, True, True, True, True)
+    dy = rounded(rng.standard_normal(s["x"].shape), io)
+    want, mag = scan_ref(s, True, lens, dy=dy), scan_ref(s, True, lens, dy=dy, absolute=True)
+    t = scan_dev(s, io, lens, True)
+    y, ST = scan_fwd(osdn, t)
+    g = scan_bwd(osdn, t, dev(dy, io).reshape(t["x"].shape))
+    finish(osdn)
+    coarse, fine = scan_factors(io, lens, 64)
+    close(y.reshape(want["y"].shape), want["y"], U[io] * np.abs(want["y"]) + coarse * mag["y"], "y")
+    close(ST, want["ST"], fine * mag["ST"], "ST")
+    for name in ("dx", "db", "dc"):
+        close(g[name].reshape(want[name].shape), want[name],
+              U[io] * np.abs(want[name]) + coarse * mag[name], name)
+
+
+def test_offsets_past_32_bits(osdn):
+    """Tensors of more than 2^31 values: the last head, channels and rows are those of a call on
+    them alone (the scan's to bf16 rounding: its chains are cut elsewhere)."""
+    T, H, Dv, Dk = 66000, 256, 128, 64
+    g = torch.Generator(device="cuda").manual_seed(12)
+    draw = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    x = draw(1, T, H, Dv)
+    assert x.numel() > 2 ** 31
+    w = torch.randn(H * Dv, 4, generator=g, device="cuda")
+    last = lambda t: t[:, :, -1:].clone()  # noqa: E731
+    y, st = osdn.osdn_conv_fwd(x, w)
+    y1, st1 = osdn.osdn_conv_fwd(last(x), w[-Dv:].clone())
+    assert torch.equal(last(y), y1) and torch.equal(st[..., -Dv:], st1)
+    del y
+    dy = draw(1, T, H, Dv)
+    c = osdn.osdn_conv_bwd(x, w, dy)
+    c1 = osdn.osdn_conv_bwd(last(x), w[-Dv:].clone(), last(dy))
+    assert torch.equal(last(c["dx"]), c1["dx"])
+    err = (c["dweight"][-Dv:] - c1["dweight"]).norm() / c1["dweight"].norm()
+    assert err <= T * E
+    del c
+    u, _ = osdn.osdn_norm_fwd(x, gate=dy, w_post=torch.ones(Dv, device="cuda"))
+    u1, _ = osdn.osdn_norm_fwd(last(x), gate=last(dy), w_post=torch.ones(Dv, device="cuda"))
+    assert torch.equal(last(u), u1)
+    del u
+    b, cc = 0.2 * draw(1, T, 1, Dk), 0.2 * draw(1, T, 1, Dk)
+    dt, A = torch.randn(1, T, H, generator=g, device="cuda") - 3, torch.full((H,), -4.0, device="cuda")
+    o, ST = osdn.osdn_ssm_fwd(x, dt, A, b, cc)
+    o1, ST1 = osdn.osdn_ssm_fwd(last(x), last(dt), A[-1:].clone(), b, cc)
+    near = lambda p, q, tol: (p.float() - q.float()).norm() <= tol * q.float().norm()  # noqa: E731
+    assert near(last(o), o1, 2 ** -7) and near(ST[:, -1:], ST1, 2.0 ** -15)
+    del o
+    s = osdn.osdn_ssm_bwd(x, dt, A, b, cc, dy)
+    s1 = osdn.osdn_ssm_bwd(last(x), last(dt), A[-1:].clone(), b, cc, last(dy))
+    finish(osdn)
+    assert near(last(s["dx"]), s1["dx"], 2 ** -7) and near(last(s["ddt"]), s1["ddt"], 2.0 ** -13)
+    assert near(s["dA"][-1:], s1["dA"], 2.0 ** -13)

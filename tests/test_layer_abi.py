@@ -47,7 +47,7 @@ CONV = dict(x=fake(1), weight=fake(2), bias=fake(3), state0=fake(4), silu=1, y=f
 
 @pytest.mark.parametrize("kw,status", [
     (dict(C=0), INV), (dict(T=-1), INV), (dict(B=-1), INV), (dict(silu=2), INV), (dict(io=5), INV),
-    (dict(W=1), UNS), (dict(W=5), UNS),
+    (dict(W=1), UNS), (dict(W=5), UNS), (dict(C=(1 << 30) + 1), UNS),
     (dict(x=None), INV), (dict(y=None), INV), (dict(weight=None), INV),
     (dict(cu=fake(9), num_seqs=2), INV),                       # packed needs B == 1
     (dict(cu=fake(9), num_seqs=0, B=1), INV),                  # tokens of no sequence
