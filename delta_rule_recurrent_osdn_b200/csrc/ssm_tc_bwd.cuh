@@ -27,8 +27,8 @@
 // Warps 0-15: element-wise work, thread = row, the four warpgroups taking every fourth 16-column
 // sub-block of scores and a quarter of the outputs' columns; warp 16: loads and MMAs; 17: gates.
 // The images' terms pass through two slots of shared memory, each loaded again once used up.
-// 340M layer (B=8, T=2048, H=8, 128 x 128): 135 us for 405 MB read and 81 written, seven rounds
-// of CTAs at 19 us each.  A CTA's products, its element-wise work and its stores follow one
+// 340M layer (B=8, T=2048, H=8, 128 x 128): 121 us for 405 MB read and 81 written, seven rounds
+// of CTAs at 17 us each.  A CTA's products, its element-wise work and its stores follow one
 // another, and shared memory (four tiles, two terms) leaves room for one CTA on an SM.
 #pragma once
 
@@ -171,30 +171,18 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             }
             load_term(0, imr);
             load_term(1, imr + L::TERM);
-            // what the CTA that follows here about a round later will load, into L2 meanwhile: its
-            // first loads then do not wait for HBM (156 -> 135 us at the 340M shape)
+            // What the CTA that follows here about a round later will load, into L2 meanwhile: its
+            // first loads then do not wait for HBM.  Asked for once this CTA's own loads (all but
+            // one term) are under way, which would stand in line behind it: 121 us at the 340M
+            // shape, 135 when asked for at the start, 156 without.
             const int64_t ahead = (int64_t)blockIdx.x + p.round, aslot = ahead / p.H;
+            const int ah = (int)(ahead - aslot * p.H), ag = ah / (p.H / p.G);
             int an, achunk;
-            if (aslot < p.slots && token_block(p.cu, p.N, p.T, TCS_L, aslot, an, achunk)) {
-                const int ah = (int)(ahead - aslot * p.H), ag = ah / (p.H / p.G);
-                const int64_t af = p.cu ? (int64_t)__ldg(p.cu + an) : (int64_t)an * p.T;
-                const int64_t ar = af + (int64_t)achunk * TCS_L;
-                if (af >= 0 && ar < p.rows) {
-#pragma unroll
-                    for (int e = 0; e < DK / 64; ++e) {
-                        tc::tma_prefetch_3d(&tm_b, e * 64, ag, (int)ar);
-                        tc::tma_prefetch_3d(&tm_c, e * 64, ag, (int)ar);
-                    }
-#pragma unroll
-                    for (int e = 0; e < DV / 64; ++e) {
-                        tc::tma_prefetch_3d(&tm_x, e * 64, ah, (int)ar);
-                        tc::tma_prefetch_3d(&tm_dy, e * 64, ah, (int)ar);
-                    }
-                    const int64_t aat = (aslot * p.H + ah) * (int64_t)(TCS_TERMS * L::TERM);
-                    tc::bulk_prefetch(p.img_r + aat, TCS_TERMS * L::TERM);
-                    tc::bulk_prefetch(p.img + aat, TCS_TERMS * L::TERM);
-                }
-            }
+            int64_t ar = -1;
+            if (aslot < p.slots && token_block(p.cu, p.N, p.T, TCS_L, aslot, an, achunk))
+                ar = (p.cu ? (int64_t)__ldg(p.cu + an) : (int64_t)an * p.T) + (int64_t)achunk * TCS_L;
+            if (ar >= p.rows) ar = -1;
+            const int64_t aat = (aslot * p.H + ah) * (int64_t)(TCS_TERMS * L::TERM);
             int n0 = 1, n1 = 1;  // terms asked for
             constexpr uint32_t ID_S = tc::idesc(1, 0, 0, 128, 128);   // scores
             constexpr uint32_t ID_KK = tc::idesc(1, 0, 0, 128, DK);   // rows x key channels, K-major
@@ -260,6 +248,19 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             if (ok) {
                 load_term(0, im + L::TERM);
                 n0 = 3;
+                if (ar >= 0) {
+#pragma unroll
+                    for (int e = 0; e < DK / 64; ++e) {
+                        tc::tma_prefetch_3d(&tm_b, e * 64, ag, (int)ar);
+                        tc::tma_prefetch_3d(&tm_c, e * 64, ag, (int)ar);
+                    }
+#pragma unroll
+                    for (int e = 0; e < DV / 64; ++e) {
+                        tc::tma_prefetch_3d(&tm_x, e * 64, ah, (int)ar);
+                        tc::tma_prefetch_3d(&tm_dy, e * 64, ah, (int)ar);
+                    }
+                    tc::bulk_prefetch(p.img_r + aat, TCS_TERMS * L::TERM);
+                }
                 ok = tcs_wait(ew1, 0);
             }
             if (ok) {
@@ -280,6 +281,7 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             if (ok) {
                 load_term(1, im + 2 * L::TERM);
                 n1 = 3;
+                if (ar >= 0) tc::bulk_prefetch(p.img + aat, TCS_TERMS * L::TERM);
                 ok = tcs_wait(img0, 2);
             }
             if (ok) {
