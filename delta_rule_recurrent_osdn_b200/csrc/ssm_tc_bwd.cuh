@@ -21,8 +21,9 @@
 //
 // Nine products a chunk: three of scores (x.dy in both orientations: P X-like products read the
 // weighted scores as rows), three with the states, three with the weighted scores.  Tensor
-// memory holds two score tiles and two accumulators; the state products go
-// in first, are scaled by their rows' decays in place, and the weighted scores accumulate on top.
+// memory holds two score tiles and two accumulators, and dc takes the place of the first scores
+// once they are used up; the state products go in first, are scaled by their rows' decays in
+// place, and the weighted scores accumulate on top.
 //
 // Warps 0-15: element-wise work, thread = row, the four warpgroups taking every fourth 16-column
 // sub-block of scores and a quarter of the outputs' columns; warp 16: loads and MMAs; 17: gates.
@@ -112,14 +113,13 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     uint64_t* img0 = bars + 1;     // slots 0 and 1: a term landed
     uint64_t* img1 = bars + 14;
     uint64_t* use0 = bars + 15;    // ... used up (MMA commit)
-    uint64_t* use1 = bars + 16;
+    uint64_t* use1 = bars + 8;
     uint64_t* gates = bars + 2;
     uint64_t* zeroed = bars + 3;   // dead rows of a short chunk
     uint64_t* sc1 = bars + 4;      // scores [j][i]
     uint64_t* in1 = bars + 5;      // R products
     uint64_t* ew1 = bars + 6;      // weighted scores and scaled R products written
     uint64_t* acc1 = bars + 7;     // dx, db complete
-    uint64_t* out1 = bars + 8;     // ... read
     uint64_t* sc2 = bars + 9;      // scores [i][j]
     uint64_t* in2 = bars + 10;     // S product
     uint64_t* ew2 = bars + 11;
@@ -136,9 +136,9 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         tc::tmem_relinquish();
     }
     if (tid == 0) {
-        for (int i = 0; i < 17; ++i) {
+        for (int i = 0; i < 16; ++i) {
             uint64_t* b = bars + i;
-            mbar_init(b, b == zeroed || b == ew1 || b == out1 || b == ew2 ? 16 : 1);
+            mbar_init(b, b == zeroed || b == ew1 || b == ew2 ? 16 : 1);
         }
         tc::fence_mbar_init();
     }
@@ -259,7 +259,6 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                         tc::tma_prefetch_3d(&tm_x, e * 64, ah, (int)ar);
                         tc::tma_prefetch_3d(&tm_dy, e * 64, ah, (int)ar);
                     }
-                    tc::bulk_prefetch(p.img_r + aat, TCS_TERMS * L::TERM);
                 }
                 ok = tcs_wait(ew1, 0);
             }
@@ -270,32 +269,35 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 tc::mma_commit(acc1);
                 scores(T1, ady, ax, NV{});  // dy_i . x_j
                 tc::mma_commit(sc2);
-                ok = tcs_wait(img1, 1) && tcs_wait(out1, 0);
+                ok = tcs_wait(img1, 1) && tcs_wait(acc1, 0);  // T0 used up
             }
             if (ok) {
                 tc::fence_after_sync();
-                state_k(A0, ady, 1, false);  // S^T dy_i
+                state_k(T0, ady, 1, false);  // S^T dy_i
                 tc::mma_commit(use1);
                 ok = tcs_wait(use1, 1);
             }
             if (ok) {
                 load_term(1, im + 2 * L::TERM);
                 n1 = 3;
-                if (ar >= 0) tc::bulk_prefetch(p.img + aat, TCS_TERMS * L::TERM);
+                if (ar >= 0) {
+                    tc::bulk_prefetch(p.img_r + aat, TCS_TERMS * L::TERM);
+                    tc::bulk_prefetch(p.img + aat, TCS_TERMS * L::TERM);
+                }
                 ok = tcs_wait(img0, 2);
             }
             if (ok) {
-                state_k(A0, ady, 0, true);
+                state_k(T0, ady, 0, true);
                 ok = tcs_wait(img1, 2);
             }
             if (ok) {
-                state_k(A0, ady, 1, true);
+                state_k(T0, ady, 1, true);
                 tc::mma_commit(in2);
                 ok = tcs_wait(ew2, 0);
             }
             if (ok) {
                 tc::fence_after_sync();
-                weighted(A0, T1, ab, ID_MK);
+                weighted(T0, T1, ab, ID_MK);
                 tc::mma_commit(acc2);
             }
             tc::mma_commit(drain);
@@ -574,7 +576,6 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         };
         if (ok) {
             give(p.db, p.dbh, A1, st);
-            arrive(out1);
             ok = wait(sc2, 0);
         }
         float pos = 0.f;
@@ -645,7 +646,7 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             for (int q = 0; q < DK / 64; ++q) {
                 const int c = wg * (DK / 4) + 16 * q;
                 float v[16];
-                tc::tmem_ld16(tl + A0 + c, v);
+                tc::tmem_ld16(tl + T0 + c, v);
                 const uint4 u0 = tile16(L::C, c), u1 = tile16(L::C, c + 8);
                 const uint32_t cw[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
                 tc::tmem_ld_wait();
@@ -657,7 +658,7 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     v[2 * e] = t.x;
                     v[2 * e + 1] = t.y;
                 }
-                tc::tmem_st16(tl + A0 + c, v);
+                tc::tmem_st16(tl + T0 + c, v);
             }
             tc::tmem_st_wait();
             if (live && OSDN_IN_BOUNDS(row, p.rows)) p.pos[(wg * p.H + h) * p.rows + row] = pos;
@@ -666,7 +667,7 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         }
         if (ok) {
             tc::fence_after_sync();
-            give(p.dc, p.dch, A0, 1.f);
+            give(p.dc, p.dch, T0, 1.f);
         }
     }
     tc::fence_before_sync();
