@@ -28,8 +28,8 @@
 // Warps 0-15: element-wise work, thread = row, the four warpgroups taking every fourth 16-column
 // sub-block of scores and a quarter of the outputs' columns; warp 16: loads and MMAs; 17: gates.
 // The images' terms pass through two slots of shared memory, each loaded again once used up.
-// 340M layer (B=8, T=2048, H=8, 128 x 128): 121 us for 405 MB read and 81 written, seven rounds
-// of CTAs at 17 us each.  A CTA's products, its element-wise work and its stores follow one
+// 340M layer (B=8, T=2048, H=8, 128 x 128): 114 us for 405 MB read and 81 written, seven rounds
+// of CTAs at 16 us each.  A CTA's products, its element-wise work and its stores follow one
 // another, and shared memory (four tiles, two terms) leaves room for one CTA on an SM.
 #pragma once
 
@@ -385,10 +385,13 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             arrive(zeroed);
         }
         ok = ok && wait(gates, 0) && wait(sc1, 0);
+        // Sums of a token are stored once a phase's results are handed over: a store can wait for
+        // those of the outputs in front of it.
+        const bool mine = (rb & 3) == wg;  // this thread has its row's diagonal element
+        float diag = 0.f, ri = 0.f, rn = 0.f;
         if (ok) {
             tc::fence_after_sync();
             // ---- scores [j][i], i >= j: 2^(cum_i - cum_j) = 2^l_i 2^(base_b - cum_j)
-            float ri = 0.f;
             const float sj = f->st[r];
             float* rowsum = reinterpret_cast<float*>(smem + L::ROWSUM) + wq * TCS_L;
 #pragma unroll 1
@@ -426,7 +429,6 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     }
                     tc::tmem_ld_wait();
                     const int own = b == rb ? r & 15 : -1;  // the diagonal's column
-                    float diag = 0.f;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float2 t = make_float2(wt[2 * e], wt[2 * e + 1]);
@@ -442,7 +444,6 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                         s1[2 * e] = sj * x.x;
                         s1[2 * e + 1] = sj * x.y;
                     }
-                    if (own >= 0 && live && OSDN_IN_BOUNDS(row, p.rows)) p.wd[h * p.rows + row] = diag;
                     __syncwarp();
                     // 16 columns summed over the warp's 32 rows: each step halves the columns a
                     // lane keeps and doubles the rows that they stand for
@@ -462,7 +463,6 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 tc::tmem_st8(tl + T0 + 16 * b, w1);
                 tc::tmem_st8(tl + T1 + 16 * b, w2);
             }
-            if (live && OSDN_IN_BOUNDS(row, p.rows)) p.ri[(wg * p.H + h) * p.rows + row] = ri;
         }
         ok = ok && wait(in1, 0);
         const float st = f->st[r];
@@ -471,7 +471,6 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             // ---- R products scaled by 2^(cum_L - cum_j) in place
             const float e1 = ex2f((f->bh[8] - f->bh[rb]) + (f->bl[8] - f->bl[rb]) - f->l[r]);
             const float2 e2 = make_float2(e1, e1);
-            float rn = 0.f;
 #pragma unroll 1
             for (int q = 0; q < DV / 64; ++q) {
                 const int c = wg * (DV / 4) + 16 * q;
@@ -501,8 +500,13 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 tc::tmem_st16(tl + A1 + c, v);
             }
             tc::tmem_st_wait();
-            if (live && OSDN_IN_BOUNDS(row, p.rows)) p.rn[(wg * p.H + h) * p.rows + row] = rn;
             arrive(ew1);
+            if (live && OSDN_IN_BOUNDS(row, p.rows)) {
+                const int64_t at = h * p.rows + row, share = (wg * (int64_t)p.H) * p.rows;
+                p.ri[share + at] = ri;
+                p.rn[share + at] = rn;
+                if (mine) p.wd[at] = diag;
+            }
         }
         // ---- 2^cum_L <R, S> from the two leading terms, in L2 by now
         if (ok) {
@@ -619,13 +623,9 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                         }
                     }
                     tc::tmem_ld_wait();
-                    if (b == rb && p.vk && live) {
-                        float v = 0.f;
+                    const int own = b == rb ? r & 15 : -1;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v = e == (r & 15) ? s2[e] : v;
-                        p.vk[h * p.rows + row] = v;
-                    }
-                    __syncwarp();
+                    for (int e = 0; e < 16; ++e) diag = e == own ? s2[e] : diag;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float2 v = __fmul2_rn(make_float2(wt[2 * e], wt[2 * e + 1]),
@@ -661,8 +661,11 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 tc::tmem_st16(tl + T0 + c, v);
             }
             tc::tmem_st_wait();
-            if (live && OSDN_IN_BOUNDS(row, p.rows)) p.pos[(wg * p.H + h) * p.rows + row] = pos;
             arrive(ew2);
+            if (live && OSDN_IN_BOUNDS(row, p.rows)) {
+                p.pos[(wg * p.H + h) * p.rows + row] = pos;
+                if (mine && p.vk) p.vk[h * p.rows + row] = diag;  // dy . x
+            }
             ok = wait(acc2, 0);
         }
         if (ok) {
