@@ -28,7 +28,7 @@
 // Warps 0-15: element-wise work, thread = row, the four warpgroups taking every fourth 16-column
 // sub-block of scores and a quarter of the outputs' columns; warp 16: loads and MMAs; 17: gates.
 // The images' terms pass through two slots of shared memory, each loaded again once used up.
-// 340M layer (B=8, T=2048, H=8, 128 x 128): 114 us for 405 MB read and 81 written, seven rounds
+// 340M layer (B=8, T=2048, H=8, 128 x 128): 112 us for 364 MB read and 82 written, seven rounds
 // of CTAs at 16 us each.  A CTA's products, its element-wise work and its stores follow one
 // another, and shared memory (four tiles, two terms) leaves room for one CTA on an SM.
 #pragma once
