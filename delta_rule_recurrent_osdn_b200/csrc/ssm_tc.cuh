@@ -447,7 +447,10 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         uint8_t* so = smem + L::S;
         for (int i = 0; i < nch; ++i) {
             if (!wait(&gate_full[i % TCS_GATES], i / TCS_GATES)) break;
-            const float decay = ex2f(gate(i)->bh[8] + gate(i)->bl[8]);
+            // all that is needed of the slot, before it is given back
+            const float log_decay = gate(i)->bh[8] + gate(i)->bl[8];
+            const float decay = ex2f(log_decay);
+            if constexpr (L::SEG) total += log_decay;
             if (!OUT) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&gate_free[i % TCS_GATES]);
@@ -467,9 +470,7 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 tc::fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_full);
-            } else if constexpr (L::SEG) {
-                total += gate(i)->bh[8];
-            } else {
+            } else if constexpr (!L::SEG) {
                 // images: rows of 128 bytes as the products read them, the terms one after another
                 const int64_t cs = first / TCS_L + n + chunk_of(i);
                 if (on) {
