@@ -267,12 +267,15 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 weighted(A0, T0, ady, ID_MV);
                 weighted(A1, T1, ac, ID_MK);
                 tc::mma_commit(acc1);
-                scores(T1, ady, ax, NV{});  // dy_i . x_j
-                tc::mma_commit(sc2);
-                ok = tcs_wait(img1, 1) && tcs_wait(acc1, 0);  // T0 used up
-            }
+                ok = tcs_wait(acc1, 0);  // T0 and T1 used up: nothing orders products with
+            }                            // different accumulators but a wait
             if (ok) {
                 tc::fence_after_sync();
+                scores(T1, ady, ax, NV{});  // dy_i . x_j
+                tc::mma_commit(sc2);
+                ok = tcs_wait(img1, 1);
+            }
+            if (ok) {
                 state_k(T0, ady, 1, false);  // S^T dy_i
                 tc::mma_commit(use1);
                 ok = tcs_wait(use1, 1);

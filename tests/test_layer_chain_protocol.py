@@ -75,3 +75,45 @@ def test_state_reads_its_gates_before_it_gives_them_back():
 
 def test_a_read_behind_the_release_is_caught():
     assert count_caught(lambda seed: ring(["read", "free", "read"], 3 * RING, seed), range(300)) > 0
+
+
+# ------------------------------------------------- tensor memory between products (chunk gradients)
+# Products with different accumulators may complete in any order: a score tile that one product
+# reads is overwritten by another only behind a wait for a commit that covers the first.
+def tile_hazards(text):
+    """Score tiles overwritten by a product while one issued before may still read them."""
+    pattern = re.compile(r"(?P<weighted>weighted\((\w+), (?P<src>\w+),)"
+                         r"|(?P<over>(?:scores|state_k)\((?P<dst>\w+),|tcg_mma<[^;]*?\(tmem \+ (?P<dst2>\w+),)"
+                         r"|mma_commit\((?P<commit>\w+)\)|tcs_wait\((?P<wait>\w+),")
+    pending, covered, bad, steps = set(), {}, [], []
+    for m in pattern.finditer(text):
+        if m.group("weighted"):
+            steps.append(m.group("src"))
+            pending.add(m.group("src"))
+        elif m.group("over"):
+            dst = m.group("dst") or m.group("dst2")
+            steps.append(dst)
+            if dst in pending:
+                bad.append(dst)
+        elif m.group("commit"):
+            covered[m.group("commit")] = set(pending)
+        else:
+            pending -= covered.pop(m.group("wait"), set())
+    return bad, steps
+
+
+def issue_order():
+    text = source("ssm_tc_bwd.cuh")
+    at = text.index("bool ok = tcs_wait(tiles, 0)")
+    return text[at:text.index("tc::mma_commit(drain)", at)]
+
+
+def test_score_tiles_are_overwritten_once_used_up():
+    bad, steps = tile_hazards(issue_order())
+    assert {"T0", "T1", "A0", "A1"} <= set(steps)  # the source was understood
+    assert not bad
+
+
+def test_an_early_overwrite_is_caught():
+    assert tile_hazards("weighted(A1, T1, ac); tc::mma_commit(acc1); scores(T1, ady);")[0] == ["T1"]
+    assert not tile_hazards("weighted(A1, T1, ac); tc::mma_commit(acc1); tcs_wait(acc1, 0); scores(T1, ady);")[0]
