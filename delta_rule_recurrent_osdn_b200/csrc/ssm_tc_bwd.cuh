@@ -374,9 +374,10 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        bool ok = true;
-        if (len < TCS_L && (ok = wait(tiles, 0))) {  // rows of the next sequence: 0 x NaN must not
-            if (!live && wg == 0) {                  // reach a sum
+        // every warp that reads the tiles waits for the copies itself
+        bool ok = wait(tiles, 0);
+        if (ok && len < TCS_L) {     // rows of the next sequence: 0 x NaN must not reach a sum
+            if (!live && wg == 0) {
                 const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
                 for (int t = 0; t < (int)(L::IMG / 16384); ++t)

@@ -117,3 +117,13 @@ def test_score_tiles_are_overwritten_once_used_up():
 def test_an_early_overwrite_is_caught():
     assert tile_hazards("weighted(A1, T1, ac); tc::mma_commit(acc1); scores(T1, ady);")[0] == ["T1"]
     assert not tile_hazards("weighted(A1, T1, ac); tc::mma_commit(acc1); tcs_wait(acc1, 0); scores(T1, ady);")[0]
+
+
+# ------------------------------------------------------------ copies seen by the warps that read them
+def test_the_warps_that_read_token_tiles_wait_for_the_copies():
+    """A copy's bytes are visible to threads that saw its barrier complete: the element-wise warps of
+    the chunk gradients, which read rows of the tiles, wait for it whatever the chunk's length."""
+    text = source("ssm_tc_bwd.cuh")
+    role = text[text.index("bool ok", text.index("auto arrive = [&]")):]
+    first = role[:role.index("tile16(")]
+    assert re.match(r"bool ok = wait\(tiles, 0\);", first)
