@@ -279,8 +279,13 @@ norm_bwd_kernel(const IO* __restrict__ f, const IO* __restrict__ x, const IO* __
         }
         if constexpr (NEXT) {
             float n[V], g[V];
-            if (w_post) norm_mul(n, v, w, scale);
-            else norm_axpy(n, scale - 1.f, v, v);
+            if (w_post) {
+                norm_mul(n, v, w, scale);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) n[e] = v[e];
+                norm_scale(n, scale);
+            }
             if (gate && !gate_first) {
                 rg.to(g);
 #pragma unroll
