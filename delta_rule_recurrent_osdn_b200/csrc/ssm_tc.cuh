@@ -12,8 +12,9 @@
 // V'_j = 2^(cum_L - cum_j) step_j x_j.
 //
 // Decays.  cum is kept per sub-block of 16 tokens: an offset l_j inside the sub-block and the
-// sub-blocks' bases as two fp32 terms (summed in 64 bits), so differences of far sums lose
-// nothing.  Between sub-blocks 2^(cum_i - cum_j) = 2^(cum_i - end_b) 2^(end_b - cum_j), end_b the
+// sub-blocks' bases, each summed in 64 bits and kept as two fp32 terms, so differences of far sums
+// lose nothing, nor do those of tokens behind one that forgets the state (whose own log decay can
+// be thousands: with l_j as one term the weights behind it were 8e-5 off at -1000).  Between sub-blocks 2^(cum_i - cum_j) = 2^(cum_i - end_b) 2^(end_b - cum_j), end_b the
 // sum at the end of j's sub-block: both factors are at most 1 when A <= 0, the second is one
 // value per token and the first one per row and sub-block, so only the 16 x 16 blocks on the
 // diagonal take an exponential per element.
@@ -83,7 +84,7 @@ template <int DQ, int MODE> struct TcsSmem {
     static constexpr uint32_t VP = 2 * STAGE;
     static constexpr uint32_t S = VP + NT * 16384;    // the state as an operand (or image)
     static constexpr uint32_t GATE = S + (OUT ? 16384 : MODE == TCS_SAVE ? TCS_TERMS * 16384 : 0);
-    static constexpr uint32_t GATE_BYTES = 1664;
+    static constexpr uint32_t GATE_BYTES = 2192;
     static constexpr uint32_t BAR = GATE + TCS_GATES * GATE_BYTES;
     static constexpr uint32_t TMEM_SLOT = BAR + (27 + 2 * TCS_GATES) * 8 + 8;
     static constexpr size_t BYTES = TMEM_SLOT + 16 + 1024;  // + alignment slack
@@ -98,10 +99,12 @@ static_assert(TcsSmem<128, TCS_FWD>::BYTES <= 232448 && TcsSmem<128, TCS_SAVE>::
 
 // One chunk's gates in shared memory.
 struct TcsGate {
-    float l[TCS_L];    // sum of log2 decays from the token's sub-block's start, itself included
+    float l[TCS_L];    // sum of log2 decays from the token's sub-block's start, itself included,
+    float l2[TCS_L];   // ... and what l leaves of it
     float g[TCS_L];    // 2^(end - l) step;  backwards in time: 2^l
     float st[TCS_L];   // step
     float bh[9], bl[9];  // sums in front of each sub-block and behind the last, two terms each
+    float th[8], tl[8];  // each sub-block's own sum, two terms
 };
 static_assert(sizeof(TcsGate) <= TcsSmem<128, TCS_FWD>::GATE_BYTES, "gate arrays");
 
@@ -165,15 +168,17 @@ __device__ __forceinline__ void tcs_gates(bool rev, TcsGate* g, const float* __r
     // 4 tokens a lane, 4 lanes a sub-block
     const float4 d4 = *reinterpret_cast<const float4*>(g->l + 4 * lane);
     const float4 s4 = *reinterpret_cast<const float4*>(g->st + 4 * lane);
-    float4 l4 = make_float4(d4.x, d4.x + d4.y, (d4.x + d4.y) + d4.z, ((d4.x + d4.y) + d4.z) + d4.w);
-    float own = l4.w, pre = 0.f;
+    double l[4] = {d4.x, (double)d4.x + d4.y, 0.0, 0.0};
+    l[2] = l[1] + d4.z;
+    l[3] = l[2] + d4.w;
+    double own = l[3], pre = 0.0;
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) {
-        const float o = __shfl_up_sync(0xffffffffu, own, off, 4);
+        const double o = __shfl_up_sync(0xffffffffu, own, off, 4);
         if ((lane & 3) >= off) { own += o; pre += o; }
     }
-    const float tot = __shfl_sync(0xffffffffu, own, 3, 4);  // the sub-block's sum
-    double base = (double)tot;
+    const double tot = __shfl_sync(0xffffffffu, own, 3, 4);  // the sub-block's sum
+    double base = tot;
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
         const double o = __shfl_up_sync(0xffffffffu, base, off);
@@ -181,17 +186,25 @@ __device__ __forceinline__ void tcs_gates(bool rev, TcsGate* g, const float* __r
     }
     if ((lane & 3) == 0) {
         const int b = lane >> 2;
-        const float hi = (float)base;
+        const float hi = (float)base, th = (float)tot;
         g->bh[b + 1] = hi;
         g->bl[b + 1] = (float)(base - (double)hi);
+        g->th[b] = th;
+        g->tl[b] = (float)(tot - (double)th);
         if (b == 0) g->bh[0] = g->bl[0] = 0.f;
     }
-    l4.x += pre; l4.y += pre; l4.z += pre; l4.w += pre;
-    *reinterpret_cast<float4*>(g->l + 4 * lane) = l4;
-    *reinterpret_cast<float4*>(g->g + 4 * lane) =
-        rev ? make_float4(ex2f(l4.x), ex2f(l4.y), ex2f(l4.z), ex2f(l4.w))
-            : make_float4(ex2f(tot - l4.x) * s4.x, ex2f(tot - l4.y) * s4.y, ex2f(tot - l4.z) * s4.z,
-                          ex2f(tot - l4.w) * s4.w);
+    float hi[4], lo[4], w[4];
+    const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        l[e] += pre;
+        hi[e] = (float)l[e];
+        lo[e] = (float)(l[e] - (double)hi[e]);
+        w[e] = rev ? ex2f(hi[e]) : ex2f((float)(tot - l[e])) * s[e];
+    }
+    *reinterpret_cast<float4*>(g->l + 4 * lane) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<float4*>(g->l2 + 4 * lane) = make_float4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<float4*>(g->g + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
 }
 
 // One operand pair's K steps: `n` MMAs, the descriptors' start addresses (16-byte units) moving
@@ -693,19 +706,23 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             {  // the sub-blocks on the diagonal: wg = 0: of the first 16 rows, wg = 1: of the others
                 const int b = 2 * wq + wg;
                 tc::tmem_ld16(col + 16 * b, x);
-                // cum_r - (the sum in front of the sub-block): l_r itself where it is the row's own
-                const float d = (bh - gt->bh[b]) + (bl - gt->bl[b]) + lr;
+                // cum_r - cum_j: l_r - l_j where the sub-block is the row's own, (its sum - l_j) + l_r
+                // where it is the one in front
+                const bool own = rb == b;
+                const float dh = own ? lr : gt->th[b], dl = own ? gt->l2[r] : gt->tl[b];
+                const float rest = own ? 0.f : lr;
                 const float4* lp = reinterpret_cast<const float4*>(gt->l + 16 * b);
+                const float4* mp = reinterpret_cast<const float4*>(gt->l2 + 16 * b);
                 const float4* sp = reinterpret_cast<const float4*>(gt->st + 16 * b);
                 const int c0 = 16 * b;
                 float wt[16];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float4 l4 = lp[e], s4 = sp[e];
-                    wt[4 * e] = ex2f(d - l4.x) * s4.x;
-                    wt[4 * e + 1] = ex2f(d - l4.y) * s4.y;
-                    wt[4 * e + 2] = ex2f(d - l4.z) * s4.z;
-                    wt[4 * e + 3] = ex2f(d - l4.w) * s4.w;
+                    const float4 l4 = lp[e], m4 = mp[e], s4 = sp[e];
+                    wt[4 * e] = ex2f((dh - l4.x) + (dl - m4.x) + rest) * s4.x;
+                    wt[4 * e + 1] = ex2f((dh - l4.y) + (dl - m4.y) + rest) * s4.y;
+                    wt[4 * e + 2] = ex2f((dh - l4.z) + (dl - m4.z) + rest) * s4.z;
+                    wt[4 * e + 3] = ex2f((dh - l4.w) + (dl - m4.w) + rest) * s4.w;
                 }
                 tc::tmem_ld_wait();
                 // what lies past the diagonal is left out, infinities and NaN too

@@ -59,7 +59,7 @@ template <int DK, int DV> struct TcgSmem {
     static constexpr uint32_t X = 0, DY = TV, B = 2 * TV, C = 2 * TV + TK, IMG = 2 * TV + 2 * TK;
     static constexpr uint32_t IMG_ONE = DK * 128, TERM = DV / 64 * IMG_ONE;
     static constexpr uint32_t GATE = IMG + 2 * TERM;
-    static constexpr uint32_t ROWSUM = GATE + 2304;  // [4 row quarters][128] shares of sum_j W_ij step_j
+    static constexpr uint32_t ROWSUM = GATE + 2704;  // [4 row quarters][128] shares of sum_j W_ij step_j
     static constexpr uint32_t BAR = ROWSUM + 4 * TCS_L * 4;
     static constexpr uint32_t TMEM_SLOT = BAR + 20 * 8;
     static constexpr size_t BYTES = TMEM_SLOT + 16 + 1024;
@@ -72,9 +72,9 @@ struct TcgGate {
     float r[TCS_L];
     TcsGate f;
 };
-static_assert(sizeof(TcgGate) <= 2304, "gate arrays");
+static_assert(sizeof(TcgGate) <= 2704, "gate arrays");
 static_assert(offsetof(TcgGate, f) % 16 == 0 && offsetof(TcsGate, g) % 16 == 0 &&
-                  offsetof(TcsGate, st) % 16 == 0 && TcsSmem<128, TCS_FWD>::GATE_BYTES % 16 == 0,
+                  offsetof(TcsGate, st) % 16 == 0 && offsetof(TcsGate, l2) % 16 == 0 && TcsSmem<128, TCS_FWD>::GATE_BYTES % 16 == 0,
               "the arrays are read 16 bytes at a time");
 
 // K steps of a product: n MMAs, start addresses moving by da / db (16-byte units) per step and by
@@ -393,6 +393,8 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         // those of the outputs in front of it.
         const bool mine = (rb & 3) == wg;  // this thread has its row's diagonal element
         float diag = 0.f, ri = 0.f, rn = 0.f;
+        // l_r, two terms; from behind token r to the end of its sub-block
+        const float lr = f->l[r], lr2 = f->l2[r], to_end = (f->th[rb] - lr) + (f->tl[rb] - lr2);
         if (ok) {
             tc::fence_after_sync();
             // ---- scores [j][i], i >= j: 2^(cum_i - cum_j) = 2^l_i 2^(base_b - cum_j)
@@ -409,20 +411,23 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     float s1[16], s2[16], wt[16];
                     tc::tmem_ld16(tl + T0 + 16 * b, s1);
                     tc::tmem_ld16(tl + T1 + 16 * b, s2);
-                    const float d = (f->bh[b] - f->bh[rb]) + (f->bl[b] - f->bl[rb]) - f->l[r];
-                    if (b <= 2 * wq + 1) {
+                    if (b <= 2 * wq + 1) {  // the row's own sub-block, or the one behind
+                        const float dh = b == rb ? lr : 0.f, dl = b == rb ? lr2 : 0.f;
+                        const float rest = b == rb ? 0.f : to_end;
                         const float4* lp = reinterpret_cast<const float4*>(f->l + 16 * b);
+                        const float4* mp = reinterpret_cast<const float4*>(f->l2 + 16 * b);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float4 l4 = lp[e];
+                            const float4 l4 = lp[e], m4 = mp[e];
                             const int c = 16 * b + 4 * e;
-                            wt[4 * e] = c < r ? 0.f : ex2f(d + l4.x);
-                            wt[4 * e + 1] = c + 1 < r ? 0.f : ex2f(d + l4.y);
-                            wt[4 * e + 2] = c + 2 < r ? 0.f : ex2f(d + l4.z);
-                            wt[4 * e + 3] = c + 3 < r ? 0.f : ex2f(d + l4.w);
+                            wt[4 * e] = c < r ? 0.f : ex2f((l4.x - dh) + (m4.x - dl) + rest);
+                            wt[4 * e + 1] = c + 1 < r ? 0.f : ex2f((l4.y - dh) + (m4.y - dl) + rest);
+                            wt[4 * e + 2] = c + 2 < r ? 0.f : ex2f((l4.z - dh) + (m4.z - dl) + rest);
+                            wt[4 * e + 3] = c + 3 < r ? 0.f : ex2f((l4.w - dh) + (m4.w - dl) + rest);
                         }
                     } else {
-                        const float fr = ex2f(d);
+                        const float fr =
+                            ex2f((f->bh[b] - f->bh[rb + 1]) + (f->bl[b] - f->bl[rb + 1]) + to_end);
                         const float4* gp = reinterpret_cast<const float4*>(gt->r + 16 * b);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -473,7 +478,7 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         if (ok) {
             tc::fence_after_sync();
             // ---- R products scaled by 2^(cum_L - cum_j) in place
-            const float e1 = ex2f((f->bh[8] - f->bh[rb]) + (f->bl[8] - f->bl[rb]) - f->l[r]);
+            const float e1 = ex2f((f->bh[8] - f->bh[rb + 1]) + (f->bl[8] - f->bl[rb + 1]) + to_end);
             const float2 e2 = make_float2(e1, e1);
 #pragma unroll 1
             for (int q = 0; q < DV / 64; ++q) {
@@ -604,20 +609,22 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     float s2[16], wt[16];
                     tc::tmem_ld16(tl + T1 + 16 * b, s2);
                     if (b >= 2 * wq) {
-                        const float d = (f->bh[rb] - f->bh[b]) + (f->bl[rb] - f->bl[b]) + f->l[r];
+                        const float dh = b == rb ? lr : f->th[b], dl = b == rb ? lr2 : f->tl[b];
+                        const float rest = b == rb ? 0.f : lr;
                         const float4* lp = reinterpret_cast<const float4*>(f->l + 16 * b);
+                        const float4* mp = reinterpret_cast<const float4*>(f->l2 + 16 * b);
                         const float4* sp = reinterpret_cast<const float4*>(f->st + 16 * b);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float4 l4 = lp[e], s4 = sp[e];
+                            const float4 l4 = lp[e], m4 = mp[e], s4 = sp[e];
                             const int c = 16 * b + 4 * e;
-                            wt[4 * e] = c > r ? 0.f : ex2f(d - l4.x) * s4.x;
-                            wt[4 * e + 1] = c + 1 > r ? 0.f : ex2f(d - l4.y) * s4.y;
-                            wt[4 * e + 2] = c + 2 > r ? 0.f : ex2f(d - l4.z) * s4.z;
-                            wt[4 * e + 3] = c + 3 > r ? 0.f : ex2f(d - l4.w) * s4.w;
+                            wt[4 * e] = c > r ? 0.f : ex2f((dh - l4.x) + (dl - m4.x) + rest) * s4.x;
+                            wt[4 * e + 1] = c + 1 > r ? 0.f : ex2f((dh - l4.y) + (dl - m4.y) + rest) * s4.y;
+                            wt[4 * e + 2] = c + 2 > r ? 0.f : ex2f((dh - l4.z) + (dl - m4.z) + rest) * s4.z;
+                            wt[4 * e + 3] = c + 3 > r ? 0.f : ex2f((dh - l4.w) + (dl - m4.w) + rest) * s4.w;
                         }
                     } else {
-                        const float fr = ex2f((f->bh[rb] - f->bh[b + 1]) + (f->bl[rb] - f->bl[b + 1]) + f->l[r]);
+                        const float fr = ex2f((f->bh[rb] - f->bh[b + 1]) + (f->bl[rb] - f->bl[b + 1]) + lr);
                         const float4* gp = reinterpret_cast<const float4*>(f->g + 16 * b);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -644,7 +651,7 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         if (ok) {
             tc::fence_after_sync();
             // ---- the S product scaled by 2^cum_i in place
-            const float e1 = ex2f(f->bh[rb] + f->l[r] + f->bl[rb]);
+            const float e1 = ex2f(f->bh[rb] + lr + f->bl[rb]);
             const float2 e2 = make_float2(e1, e1);
 #pragma unroll 1
             for (int q = 0; q < DK / 64; ++q) {

@@ -9,7 +9,9 @@ import pytest
 import torch
 
 from tests import layer_ref as R
-from tests.test_gpu_layer_ops import E, U, close, dev, finish, norm_inputs, osdn, rounded  # noqa: F401
+from tests.step_gradient_bounds import bounds, relative_error
+from tests.test_gpu_layer_ops import (E, U, close, dev, finish, norm_inputs, osdn, rounded,  # noqa: F401
+                                      scan_bwd, scan_dev, scan_fwd, scan_inputs, scan_ref)
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +51,61 @@ def test_norm_gradients_at_small_scales(osdn, io, res, gate, scale):  # noqa: F8
     if gate:
         close(g["dgate"], want["dgate"], U[io] * np.abs(want["dgate"]) + k * np.abs(s32) * 2 * mag *
               np.abs(a["f"]) * np.maximum(1.0, np.abs(a["gate"])), "dgate")
+
+
+# ====================================================================================== scan
+def near(got, want, tol, name):
+    """Per head (the axis in front of the last two, the last of 1- and 2-d results): the L2 norm of the
+    difference is within tol (an absolute norm, or a number relative to that of `want`)."""
+    got = np.asarray(got if isinstance(got, np.ndarray) else got.detach().double().cpu().numpy())
+    want = np.asarray(want).reshape(got.shape)
+    axes = tuple(i for i in range(got.ndim) if i != (got.ndim - 1 if got.ndim < 3 else got.ndim - 3))
+    norm = lambda t: np.sqrt((t * t).sum(axes)) if axes else np.abs(t)  # noqa: E731
+    lim = tol * norm(want) if np.ndim(tol) == 0 else tol
+    assert np.all(np.isfinite(got)), name
+    assert np.all(norm(got - want) <= lim + 1e-30), (name, norm(got - want), lim)
+
+
+def step_gradients(g, want, a, io, softplus, lens, dy, dST):
+    """ddt, dA and ddt_bias within the norms of tests/step_gradient_bounds.py."""
+    lim = bounds(a, io, softplus, lens, dy, dST)
+    H = a["A"].size
+    near(g["ddt"].reshape(-1, H), want["ddt"].reshape(-1, H), lim["ddt"], "ddt")
+    near(g["dA"], want["dA"], lim["dA"], "dA")
+    if g["ddt_bias"] is not None:
+        near(g["ddt_bias"], want["ddt_bias"], lim["ddt_bias"], "ddt_bias")
+
+
+RESETS = [  # io, lens, packed, H, G, Dk, Dv
+    ("bf16", [300], False, 2, 1, 64, 64),
+    ("bf16", [5, 300, 64], True, 2, 2, 128, 64),
+    ("bf16", [1100], False, 2, 1, 64, 128),     # cut into segments
+    ("bf16", [3200], False, 2, 1, 64, 64),      # ... in the backward pass too
+    ("f32", [300], False, 2, 1, 64, 64),
+]
+
+
+@pytest.mark.parametrize("io,lens,packed,H,G,Dk,Dv", RESETS)
+@pytest.mark.parametrize("every", [True, False])
+@pytest.mark.parametrize("dt", [40.0, 1e3, 1e4])
+def test_scan_behind_tokens_that_forget(osdn, io, lens, packed, H, G, Dk, Dv, every, dt):  # noqa: F811
+    """Tokens with steps of 40 to 10,000 (log2 decays down to -230,000 for one head, -1 to -290 for the
+    other): what follows them decays among itself as if they were not there.  One such token in every
+    16, or one 10 tokens before the end.  bf16 states come from values as two bf16 terms (2^-17 at
+    most) and two exponentials (2^-22 each); dS0 from three terms and as many exponentials as chunks."""
+    a, rng = scan_inputs(io, lens, H, G, Dk, Dv, True, True, True, True, seed=31)
+    a["A"][:] = rounded([-16.0, -0.02], "f32")
+    if every:
+        a["dt"][1::16] = dt
+    else:
+        a["dt"][-10] = dt
+    dy = rounded(rng.standard_normal(a["x"].shape), io)
+    dST = rounded(0.3 * rng.standard_normal(a["S0"].shape), "f32")
+    want = scan_ref(a, True, lens, dy=dy, dST=dST)
+    t = scan_dev(a, io, lens, packed)
+    y, ST = scan_fwd(osdn, t)
+    g = scan_bwd(osdn, t, dev(dy, io).reshape(t["x"].shape), dev(dST))
+    finish(osdn)
+    near(ST, want["ST"], 2.0 ** -17 + 2.0 ** -20 if io == "bf16" else 2 * relative_error(io, max(lens)), "ST")
+    near(g["dS0"], want["dS0"], 2.0 ** -19 if io == "bf16" else 2 * relative_error(io, max(lens)), "dS0")
+    step_gradients(g, want, a, io, True, lens, dy, dST)

@@ -82,13 +82,15 @@ def test_a_read_behind_the_release_is_caught():
 # reads is overwritten by another only behind a wait for a commit that covers the first.
 def tile_hazards(text):
     """Score tiles overwritten by a product while one issued before may still read them."""
-    pattern = re.compile(r"(?P<weighted>weighted\((\w+), (?P<src>\w+),)"
+    pattern = re.compile(r"(?P<weighted>weighted\((?P<acc>\w+), (?P<src>\w+),)"
                          r"|(?P<over>(?:scores|state_k)\((?P<dst>\w+),|tcg_mma<[^;]*?\(tmem \+ (?P<dst2>\w+),)"
                          r"|mma_commit\((?P<commit>\w+)\)|tcs_wait\((?P<wait>\w+),")
     pending, covered, bad, steps = set(), {}, [], []
     for m in pattern.finditer(text):
         if m.group("weighted"):
-            steps.append(m.group("src"))
+            steps += [m.group("acc"), m.group("src")]
+            if m.group("acc") in pending:
+                bad.append(m.group("acc"))
             pending.add(m.group("src"))
         elif m.group("over"):
             dst = m.group("dst") or m.group("dst2")
