@@ -517,26 +517,30 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 if (mine) p.wd[at] = diag;
             }
         }
-        // ---- 2^cum_L <R, S> from the two leading terms, in L2 by now
+        // ---- 2^cum_L <R, S> from all three terms (where states hardly decay it is most of the step
+        // gradient: with two terms dA was 3.5e-6 off there), in L2 by now
         if (ok) {
             float dot = 0.f;
             const int64_t at = (slot * p.H + h) * (int64_t)(TCS_TERMS * L::TERM);
             const uint4* a = reinterpret_cast<const uint4*>(p.img_r + at);
             const uint4* b = reinterpret_cast<const uint4*>(p.img + at);
             constexpr int NB = L::TERM / 16;
+            // the lower and the upper halves of word k, their terms added from the smallest on
+            auto lo = [](const uint4 (&t)[3], int k) {
+                const uint32_t w[3] = {(&t[0].x)[k], (&t[1].x)[k], (&t[2].x)[k]};
+                return __uint_as_float(w[0] << 16) + (__uint_as_float(w[1] << 16) + __uint_as_float(w[2] << 16));
+            };
+            auto hi = [](const uint4 (&t)[3], int k) {
+                const uint32_t w[3] = {(&t[0].x)[k], (&t[1].x)[k], (&t[2].x)[k]};
+                return __uint_as_float(w[0] & 0xffff0000u) +
+                       (__uint_as_float(w[1] & 0xffff0000u) + __uint_as_float(w[2] & 0xffff0000u));
+            };
 #pragma unroll 2
             for (int e = tid; e < NB; e += 512) {
-                const uint4 a0 = __ldg(a + e), a1 = __ldg(a + NB + e), b0 = __ldg(b + e), b1 = __ldg(b + NB + e);
-                const uint32_t x0[4] = {a0.x, a0.y, a0.z, a0.w}, x1[4] = {a1.x, a1.y, a1.z, a1.w};
-                const uint32_t y0[4] = {b0.x, b0.y, b0.z, b0.w}, y1[4] = {b1.x, b1.y, b1.z, b1.w};
+                const uint4 x[3] = {__ldg(a + e), __ldg(a + NB + e), __ldg(a + 2 * NB + e)};
+                const uint4 y[3] = {__ldg(b + e), __ldg(b + NB + e), __ldg(b + 2 * NB + e)};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    dot = fmaf(__uint_as_float(x0[k] << 16) + __uint_as_float(x1[k] << 16),
-                               __uint_as_float(y0[k] << 16) + __uint_as_float(y1[k] << 16), dot);
-                    dot = fmaf(__uint_as_float(x0[k] & 0xffff0000u) + __uint_as_float(x1[k] & 0xffff0000u),
-                               __uint_as_float(y0[k] & 0xffff0000u) + __uint_as_float(y1[k] & 0xffff0000u),
-                               dot);
-                }
+                for (int k = 0; k < 4; ++k) dot = fmaf(hi(x, k), hi(y, k), fmaf(lo(x, k), lo(y, k), dot));
             }
             dot = warp_sum_f(dot);
             if (lane == 0 && OSDN_IN_BOUNDS(slot, p.slots))

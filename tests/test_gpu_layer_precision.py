@@ -10,8 +10,9 @@ import torch
 
 from tests import layer_ref as R
 from tests.step_gradient_bounds import bounds, relative_error
-from tests.test_gpu_layer_ops import (E, U, close, dev, finish, norm_inputs, osdn, rounded,  # noqa: F401
-                                      scan_bwd, scan_dev, scan_fwd, scan_inputs, scan_ref)
+from tests.test_gpu_layer_ops import (E, SCANS, U, close, dev, finish, norm_inputs, osdn,  # noqa: F401
+                                      rounded, scan_bwd, scan_dev, scan_fwd, scan_inputs,
+                                      scan_ref)
 
 pytestmark = pytest.mark.gpu
 
@@ -108,4 +109,44 @@ def test_scan_behind_tokens_that_forget(osdn, io, lens, packed, H, G, Dk, Dv, ev
     finish(osdn)
     near(ST, want["ST"], 2.0 ** -17 + 2.0 ** -20 if io == "bf16" else 2 * relative_error(io, max(lens)), "ST")
     near(g["dS0"], want["dS0"], 2.0 ** -19 if io == "bf16" else 2 * relative_error(io, max(lens)), "dS0")
+    step_gradients(g, want, a, io, True, lens, dy, dST)
+
+
+@pytest.mark.parametrize("case", SCANS, ids=lambda s: f"{s[0]}-{'.'.join(map(str, s[1]))}-H{s[3]}G{s[4]}k{s[5]}v{s[6]}")
+@pytest.mark.parametrize("kind", ["plain", "slow", "extreme"])
+def test_scan_gradients_by_norm(osdn, case, kind):  # noqa: F811
+    """The step gradients within the norms of tests/step_gradient_bounds.py, which zeros and
+    gradients without the <G, S> terms fail (tests/test_step_gradient_bounds.py).  slow: states that hardly decay.  extreme: masked tokens
+    (dt = -inf), tokens that forget, a head that never decays."""
+    io, lens, packed, H, G, Dk, Dv, D, bias, state, softplus = case
+    a, rng = scan_inputs(io, lens, H, G, Dk, Dv, D, bias, state, softplus, seed=41)
+    n, N = sum(lens), len(lens)
+    if kind == "slow":
+        a["A"][:] = rounded(-np.geomspace(0.002, 0.05, H), "f32")
+    if kind == "extreme":
+        if softplus:
+            a["dt"][3:8] = -np.inf
+        a["dt"][n // 2] = 40.0
+        a["A"][-1] = 0.0
+    dy = rounded(rng.standard_normal((n, H, Dv)), io)
+    dST = rounded(0.3 * rng.standard_normal((N, H, Dv, Dk)), "f32") if state else None
+    with np.errstate(invalid="ignore"):
+        want = scan_ref(a, softplus, lens, dy=dy, dST=dST)
+    t = scan_dev(a, io, lens, packed)
+    g = scan_bwd(osdn, t, dev(dy, io).reshape(t["x"].shape), dev(dST), softplus)
+    finish(osdn)
+    step_gradients(g, want, a, io, softplus, lens, dy, dST)
+
+
+@pytest.mark.parametrize("io,lens", [("bf16", [150, 150]), ("bf16", [3200]), ("f32", [90, 90])])
+@pytest.mark.parametrize("given", ["S0", "dST"])
+def test_step_gradients_with_one_of_the_states(osdn, io, lens, given):  # noqa: F811
+    a, rng = scan_inputs(io, lens, 2, 1, 64, 64, True, True, given == "S0", True, seed=43)
+    a["A"][:] = rounded([-0.01, -4.0], "f32")
+    dy = rounded(rng.standard_normal(a["x"].shape), io)
+    dST = rounded(rng.standard_normal((len(lens), 2, 64, 64)), "f32") if given == "dST" else None
+    want = scan_ref(a, True, lens, dy=dy, dST=dST)
+    t = scan_dev(a, io, lens, False)
+    g = scan_bwd(osdn, t, dev(dy, io).reshape(t["x"].shape), dev(dST))
+    finish(osdn)
     step_gradients(g, want, a, io, True, lens, dy, dST)
