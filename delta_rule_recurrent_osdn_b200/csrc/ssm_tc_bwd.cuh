@@ -15,9 +15,9 @@
 // thread and over columns across them, so what cancels between the sums does so to fp32 (two
 // evaluations of W, each good to 2^-22, left dA wrong by up to 1e-5); what crosses the chunk's
 // ends is summed without cancelling.
-// Rounding: the weighted scores go into a product as bf16 (errors that reach dx, db, dc only,
-// bf16 themselves); S and R as three bf16 terms where pos and rn are made from them (with two, dA
-// was up to 1e-5 off), as one in R b_j.
+// Rounding: the weighted scores go into a product as two bf16 terms (with one, dx, db and dc were
+// 2.3e-3 off in L2 norm, where rounding the results alone gives 1.66e-3); S and R as three bf16
+// terms where pos and rn are made from them (with two, dA was up to 1e-5 off), as two in R b_j.
 //
 // Nine products a chunk: three of scores (x.dy in both orientations: P X-like products read the
 // weighted scores as rows), three with the states, three with the weighted scores.  Tensor
@@ -203,12 +203,17 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 tcg_mma<DV / 16>(tmem + d, kd(a), kd(ai + s * L::TERM), ID_KK, 2, 2, 1024 - 8,
                                  (L::IMG_ONE >> 4) - 8, acc);
             };
-            // weighted scores times a token tile, added
+            // weighted scores, two terms, times a token tile, added
             auto weighted = [&](uint32_t d, uint32_t s, uint32_t b, uint32_t id) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    tc::mma_bf16_ts(tmem + d, tmem + s + 16 * e, tc::sw128_desc(b + e * 2048, 16384, 1024),
-                                    id, 1);
+                for (int e = 0; e < 16; ++e)
+                    tc::mma_bf16_ts(tmem + d, tmem + s + 16 * (e & 7) + (e & 8),
+                                    tc::sw128_desc(b + (e & 7) * 2048, 16384, 1024), id, 1);
+            };
+            // R b_j, R's term in slot s: key channels summed, [key][value] read MN-major
+            auto state_v = [&](int s, bool acc) {
+                tcg_mma<DK / 16>(tmem + A0, kd(ab), tc::sw128_desc(ai + s * L::TERM, L::IMG_ONE, 1024),
+                                 ID_MV, 2, 128, 1024 - 8, 0, acc);
             };
             bool ok = tcs_wait(tiles, 0) && (len == TCS_L || tcs_wait(zeroed, 0));
             if (ok) {
@@ -218,14 +223,13 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 ok = tcs_wait(img0, 0);
             }
             if (ok) {
-                // R b_j: key channels summed, [key][value] read MN-major
-                tcg_mma<DK / 16>(tmem + A0, kd(ab), tc::sw128_desc(ai, L::IMG_ONE, 1024), ID_MV, 2, 128,
-                                 1024 - 8, 0, false);
+                state_v(0, false);          // R b_j
                 state_k(A1, ax, 0, false);  // R^T x_j
                 tc::mma_commit(use0);
                 ok = tcs_wait(img1, 0);
             }
             if (ok) {
+                state_v(1, true);
                 state_k(A1, ax, 1, true);
                 tc::mma_commit(use1);
                 ok = tcs_wait(use0, 0);
@@ -402,10 +406,10 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             float* rowsum = reinterpret_cast<float*>(smem + L::ROWSUM) + wq * TCS_L;
 #pragma unroll 1
             for (int b = wg; b < 8; b += 4) {
-                uint32_t w1[8], w2[8];
+                uint32_t w1[16], w2[16];  // the leading terms, then the second
                 if (b < 2 * wq) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w1[e] = w2[e] = 0;
+                    for (int e = 0; e < 16; ++e) w1[e] = w2[e] = 0;
                     if (lane < 16) rowsum[16 * b + lane] = 0.f;
                 } else {
                     float s1[16], s2[16], wt[16];
@@ -443,8 +447,8 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                         const float2 t = make_float2(wt[2 * e], wt[2 * e + 1]);
                         const float2 u = __fmul2_rn(t, make_float2(s1[2 * e], s1[2 * e + 1]));
                         const float2 v = __fmul2_rn(t, make_float2(s2[2 * e], s2[2 * e + 1]));
-                        w1[e] = pack2_rn(u.x, u.y);
-                        w2[e] = pack2_rn(v.x, v.y);
+                        split2_rn(u.x, u.y, w1[e], w1[8 + e]);
+                        split2_rn(v.x, v.y, w2[e], w2[8 + e]);
                         float2 x = __fmul2_rn(u, make_float2(s2[2 * e], s2[2 * e + 1]));  // W
                         if (own == 2 * e) { diag = x.x; x.x = 0.f; }
                         if (own == 2 * e + 1) { diag = x.y; x.y = 0.f; }
@@ -470,7 +474,9 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     if (!(lane & 1)) rowsum[16 * b + (lane >> 1)] = sum;
                 }
                 tc::tmem_st8(tl + T0 + 16 * b, w1);
+                tc::tmem_st8(tl + T0 + 16 * b + 8, w1 + 8);
                 tc::tmem_st8(tl + T1 + 16 * b, w2);
+                tc::tmem_st8(tl + T1 + 16 * b + 8, w2 + 8);
             }
         }
         ok = ok && wait(in1, 0);
@@ -605,10 +611,10 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             // ---- scores [i][j], j <= i
 #pragma unroll 1
             for (int b = wg; b < 8; b += 4) {
-                uint32_t w2[8];
+                uint32_t w2[16];
                 if (b > 2 * wq + 1) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w2[e] = 0;
+                    for (int e = 0; e < 16; ++e) w2[e] = 0;
                 } else {
                     float s2[16], wt[16];
                     tc::tmem_ld16(tl + T1 + 16 * b, s2);
@@ -645,10 +651,11 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     for (int e = 0; e < 8; ++e) {
                         const float2 v = __fmul2_rn(make_float2(wt[2 * e], wt[2 * e + 1]),
                                                     make_float2(s2[2 * e], s2[2 * e + 1]));
-                        w2[e] = pack2_rn(v.x, v.y);
+                        split2_rn(v.x, v.y, w2[e], w2[8 + e]);
                     }
                 }
                 tc::tmem_st8(tl + T1 + 16 * b, w2);
+                tc::tmem_st8(tl + T1 + 16 * b + 8, w2 + 8);
             }
             ok = wait(in2, 0);
         }

@@ -67,6 +67,11 @@ def near(got, want, tol, name):
     assert np.all(norm(got - want) <= lim + 1e-30), (name, norm(got - want), lim)
 
 
+def relative_l2(got, want):
+    want = np.asarray(want).reshape(got.shape)
+    return np.linalg.norm(got.detach().double().cpu().numpy() - want) / max(np.linalg.norm(want), 1e-300)
+
+
 def step_gradients(g, want, a, io, softplus, lens, dy, dST):
     """ddt, dA and ddt_bias within the norms of tests/step_gradient_bounds.py."""
     lim = bounds(a, io, softplus, lens, dy, dST)
@@ -109,14 +114,24 @@ def test_scan_behind_tokens_that_forget(osdn, io, lens, packed, H, G, Dk, Dv, ev
     finish(osdn)
     near(ST, want["ST"], 2.0 ** -17 + 2.0 ** -20 if io == "bf16" else 2 * relative_error(io, max(lens)), "ST")
     near(g["dS0"], want["dS0"], 2.0 ** -19 if io == "bf16" else 2 * relative_error(io, max(lens)), "dS0")
+    for name in ("dx", "db", "dc"):  # the result's own rounding, and two bf16 terms' 2^-16
+        l2 = relative_l2(g[name], want[name])
+        assert l2 <= (2.0 ** -8 + 2.0 ** -14 if io == "bf16" else 2 * relative_error(io, max(lens))), (name, l2)
     step_gradients(g, want, a, io, True, lens, dy, dST)
+
+
+# Rounding a value x in [2^e, 2^(e+1)) to bf16 is off by up to 2^-8 2^e, evenly: in L2 norm 2^-8 / sqrt(3)
+# times the root of sum 2^2e / sum x^2: 1.53e-3 for values spread evenly in log x, 1.66e-3 for normal ones.
+# What else a kernel adds stays below what a second rounding of that size would (2.35e-3 together).
+ROUNDED = 1.9e-3
 
 
 @pytest.mark.parametrize("case", SCANS, ids=lambda s: f"{s[0]}-{'.'.join(map(str, s[1]))}-H{s[3]}G{s[4]}k{s[5]}v{s[6]}")
 @pytest.mark.parametrize("kind", ["plain", "slow", "extreme"])
 def test_scan_gradients_by_norm(osdn, case, kind):  # noqa: F811
-    """The step gradients within the norms of tests/step_gradient_bounds.py, which zeros and
-    gradients without the <G, S> terms fail (tests/test_step_gradient_bounds.py).  slow: states that hardly decay.  extreme: masked tokens
+    """Every gradient in L2 norm: dx, db, dc to their own rounding, the step gradients within the norms
+    of tests/step_gradient_bounds.py, which zeros and gradients without the <G, S> terms fail
+    (tests/test_step_gradient_bounds.py).  slow: states that hardly decay.  extreme: masked tokens
     (dt = -inf), tokens that forget, a head that never decays."""
     io, lens, packed, H, G, Dk, Dv, D, bias, state, softplus = case
     a, rng = scan_inputs(io, lens, H, G, Dk, Dv, D, bias, state, softplus, seed=41)
@@ -135,6 +150,9 @@ def test_scan_gradients_by_norm(osdn, case, kind):  # noqa: F811
     t = scan_dev(a, io, lens, packed)
     g = scan_bwd(osdn, t, dev(dy, io).reshape(t["x"].shape), dev(dST), softplus)
     finish(osdn)
+    for name in ("dx", "db", "dc"):
+        l2 = relative_l2(g[name], want[name])
+        assert l2 <= (ROUNDED if io == "bf16" else 2 * relative_error(io, max(lens))), (name, l2)
     step_gradients(g, want, a, io, softplus, lens, dy, dST)
 
 

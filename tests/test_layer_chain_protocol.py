@@ -83,7 +83,7 @@ def test_a_read_behind_the_release_is_caught():
 def tile_hazards(text):
     """Score tiles overwritten by a product while one issued before may still read them."""
     pattern = re.compile(r"(?P<weighted>weighted\((?P<acc>\w+), (?P<src>\w+),)"
-                         r"|(?P<over>(?:scores|state_k)\((?P<dst>\w+),|tcg_mma<[^;]*?\(tmem \+ (?P<dst2>\w+),)"
+                         r"|(?P<over>(?:scores|state_k)\((?P<dst>\w+),)"
                          r"|mma_commit\((?P<commit>\w+)\)|tcs_wait\((?P<wait>\w+),")
     pending, covered, bad, steps = set(), {}, [], []
     for m in pattern.finditer(text):
@@ -93,10 +93,9 @@ def tile_hazards(text):
                 bad.append(m.group("acc"))
             pending.add(m.group("src"))
         elif m.group("over"):
-            dst = m.group("dst") or m.group("dst2")
-            steps.append(dst)
-            if dst in pending:
-                bad.append(dst)
+            steps.append(m.group("dst"))
+            if m.group("dst") in pending:
+                bad.append(m.group("dst"))
         elif m.group("commit"):
             covered[m.group("commit")] = set(pending)
         else:
