@@ -19,10 +19,14 @@
 // value per token and the first one per row and sub-block, so only the 16 x 16 blocks on the
 // diagonal take an exponential per element.
 //
-// Precision.  b, c and x enter products as stored.  V' goes in as two bf16 terms (2.4e-6 rms off),
-// three where the state leads to gradients of steps (sums over many tokens that nearly cancel), so
-// states are fp32 results; P and the state in C S^T are rounded once to bf16: their errors reach
-// only y, which is rounded to bf16 itself.
+// Precision.  b, c and x enter products as stored, P as two bf16 terms (with one, y was 2.35e-3 off in
+// L2 norm without D, where rounding y alone gives 1.66e-3; 108 -> 114 us at B=4, T=4096, H=16,
+// Dk=Dv=128).  V' goes in as two bf16 terms (each value 2^-17 off at most: ST is 2.5e-6 off; a third
+// needs 16 KB of shared memory that the forward pass does not have), three where the state leads to
+// gradients of steps (sums over many tokens that nearly cancel), and states are fp32 sums.  The state
+// in C S^T is rounded once to bf16: what that adds to y is independent from element to element and at
+// most of the size of y's own rounding, 2.35e-3 together where the state makes up all of y.  (A second
+// term fits where V' was once it is used up, but lies on the chain from state to state: 133 us.)
 //
 // Rows past a sequence's end inside its last tile belong to the next sequence: the rows of B, X
 // and V' are zeroed in shared memory before a product sums over them.
@@ -416,9 +420,9 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     if (!(ok = tcs_wait(&p_full[s], ph))) break;
                     tc::fence_after_sync();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        tc::mma_bf16_ts(tmem + L::COL_Y2, tmem + L::COL_G + s * 128 + 16 * e,
-                                        tc::sw128_desc(v + e * 2048, 16384, 1024), ID_Y, e != 0);
+                    for (int e = 0; e < 16; ++e)  // P's leading terms, then the second
+                        tc::mma_bf16_ts(tmem + L::COL_Y2, tmem + L::COL_G + s * 128 + 16 * (e & 7) + (e & 8),
+                                        tc::sw128_desc(v + (e & 7) * 2048, 16384, 1024), ID_Y, e != 0);
                     tc::mma_commit(y_full);
                 }
                 tc::mma_commit(&v_empty[s]);
@@ -668,8 +672,8 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             if (!wait(&gate_full[i % TCS_GATES], i / TCS_GATES) || !output(i)) break;
     } else {
         // ------------------------------------------------------------ P
-        // two warpgroups share P's columns by sub-blocks; P's 16 columns of sub-block b lie over the
-        // first half of their own scores, packed
+        // two warpgroups share P's columns by sub-blocks; P's 16 columns of sub-block b lie over their
+        // own scores, packed: the leading terms over the first half, the second over the other
         const int wg = (warp - 20) >> 2, wq = warp & 3;
         const int r = 32 * wq + lane, rb = r >> 4;
         for (int i = 0; i < nch; ++i) {
@@ -680,7 +684,7 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             tc::fence_after_sync();
             const uint32_t col = tmem + tlane + L::COL_G + (i & 1) * 128;
             float x[16];
-            uint32_t w[8];
+            uint32_t w[16];  // two terms
 #pragma unroll 1
             for (int k = 0; k < wq; ++k) {  // sub-blocks in front of every row of the warp
                 const int b = 2 * k + wg;
@@ -698,10 +702,11 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                                                 make_float2(x[4 * e], x[4 * e + 1]));
                     const float2 u = __fmul2_rn(__fmul2_rn(f2, make_float2(g4[e].z, g4[e].w)),
                                                 make_float2(x[4 * e + 2], x[4 * e + 3]));
-                    w[2 * e] = pack2_rn(t.x, t.y);
-                    w[2 * e + 1] = pack2_rn(u.x, u.y);
+                    split2_rn(t.x, t.y, w[2 * e], w[8 + 2 * e]);
+                    split2_rn(u.x, u.y, w[2 * e + 1], w[8 + 2 * e + 1]);
                 }
                 tc::tmem_st8(col + 16 * b, w);
+                tc::tmem_st8(col + 16 * b + 8, w + 8);
             }
             {  // the sub-blocks on the diagonal: wg = 0: of the first 16 rows, wg = 1: of the others
                 const int b = 2 * wq + wg;
@@ -728,15 +733,19 @@ ssm_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 // what lies past the diagonal is left out, infinities and NaN too
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    w[e] = pack2_rn(c0 + 2 * e > r ? 0.f : x[2 * e] * wt[2 * e],
-                                    c0 + 2 * e + 1 > r ? 0.f : x[2 * e + 1] * wt[2 * e + 1]);
+                    split2_rn(c0 + 2 * e > r ? 0.f : x[2 * e] * wt[2 * e],
+                              c0 + 2 * e + 1 > r ? 0.f : x[2 * e + 1] * wt[2 * e + 1], w[e], w[8 + e]);
                 __syncwarp();
                 tc::tmem_st8(col + 16 * b, w);
+                tc::tmem_st8(col + 16 * b + 8, w + 8);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] = 0;
 #pragma unroll 1
-            for (int k = wq + 1; k < 4; ++k) tc::tmem_st8(col + 16 * (2 * k + wg), w);
+            for (int k = wq + 1; k < 4; ++k) {
+                tc::tmem_st8(col + 16 * (2 * k + wg), w);
+                tc::tmem_st8(col + 16 * (2 * k + wg) + 8, w);
+            }
             tc::tmem_st_wait();
             tc::fence_before_sync();
             __syncwarp();

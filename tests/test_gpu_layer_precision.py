@@ -168,3 +168,28 @@ def test_step_gradients_with_one_of_the_states(osdn, io, lens, given):  # noqa: 
     g = scan_bwd(osdn, t, dev(dy, io).reshape(t["x"].shape), dev(dST))
     finish(osdn)
     step_gradients(g, want, a, io, True, lens, dy, dST)
+
+
+# two more: chunks alone, with no state in front of them
+ALONE = [("bf16", [128, 128], False, 4, 2, 128, 128, False, True, False, True),
+         ("bf16", [100, 5, 61], True, 2, 1, 64, 128, False, True, False, True)]
+
+
+@pytest.mark.parametrize("case", [s for s in SCANS if s[0] == "bf16"] + ALONE,
+                         ids=lambda s: f"{'.'.join(map(str, s[1]))}-H{s[3]}G{s[4]}k{s[5]}v{s[6]}")
+@pytest.mark.parametrize("forget", [False, True])
+def test_scan_outputs_by_norm(osdn, case, forget):  # noqa: F811
+    """y in L2 norm, without D (which would make up most of y), and ST to the two bf16 terms of the
+    values it is a sum of.  Within a chunk y is as good as its own rounding.  What an earlier state adds
+    is a sum over key channels of elements rounded to bf16 each, independently: relative to that part of
+    y another 1.66e-3 (as ROUNDED above), and sqrt(1.66^2 + 1.66^2) = 2.35e-3 together where it is all
+    of y; 2.5e-3 leaves both 6%.  forget: one token dominates those behind it."""
+    io, lens, packed, H, G, Dk, Dv, _, bias, state, softplus = case
+    a, rng = scan_inputs(io, lens, H, G, Dk, Dv, False, bias, state, softplus, seed=44)
+    if forget:
+        a["dt"][sum(lens) // 3] = 1e3
+    want = scan_ref(a, softplus, lens)
+    y, ST = scan_fwd(osdn, scan_dev(a, io, lens, packed), softplus)
+    finish(osdn)
+    assert relative_l2(y, want["y"]) <= (2.5e-3 if state or max(lens) > 128 else ROUNDED)
+    near(ST, want["ST"], 2.0 ** -17 + 2.0 ** -20, "ST")
