@@ -419,6 +419,12 @@ def _out(t, name, dtype, shape, device):
     return t
 
 
+def _fits(where, *sizes):
+    """The C entry points take sizes as int32, and ctypes would pass the lower half of a larger one."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise OsdnError(OSDN_ERR_UNSUPPORTED, where)
+
+
 def _packed(cu_seqlens, B, device):
     """(address, num_seqs, N) of packed offsets, or (None, 0, B)."""
     if cu_seqlens is None:
@@ -474,6 +480,7 @@ def osdn_conv_fwd(x, weight, bias=None, state0=None, activation: Optional[str] =
     io, dev, dt = _io(x), x.device, x.dtype
     B, T = x.shape[0], x.shape[1]
     cu, num_seqs, N = _packed(cu_seqlens, B, dev)
+    _fits("osdn_conv_fwd", B, T, C, W, N)
     y = torch.empty_like(x) if y is None else _out(y, "y", dt, x.shape, dev)
     if stateT is not None or return_state:
         stateT = _out(stateT, "stateT", dt, (N, W - 1, C), dev)
@@ -492,6 +499,7 @@ def osdn_conv_step(x, weight, state, bias=None, activation: Optional[str] = "sil
     [N, W - 1, C] in x's dtype, moved on by one token in place.  Returns y of x's shape."""
     C, W = _conv_dims(x, weight, 1)
     io, dev, dt, N = _io(x), x.device, x.dtype, x.shape[0]
+    _fits("osdn_conv_step", N, C, W)
     if state is None:
         raise ValueError("state is required")
     y = torch.empty_like(x) if y is None else _out(y, "y", dt, x.shape, dev)
@@ -517,6 +525,7 @@ def osdn_conv_bwd(x, weight, dy, bias=None, state0=None, dstateT=None,
     if dy.dtype not in (dt, f32):
         raise TypeError(f"dy must be {dt} or torch.float32, got {dy.dtype}")
     cu, num_seqs, N = _packed(cu_seqlens, B, dev)
+    _fits("osdn_conv_bwd", B, T, C, W, N)
     g = {"dx": torch.empty_like(x), "dweight": torch.empty((C, W), dtype=f32, device=dev),
          "dbias": None if bias is None else torch.empty((C,), dtype=f32, device=dev),
          "dstate0": None if state0 is None else torch.empty((N, W - 1, C), dtype=f32, device=dev)}
@@ -546,6 +555,7 @@ def _ssm_args(x, dt, A, b, c, D, dt_bias, lead, dev):
 def osdn_ssm_fwd_workspace_bytes(B: int, T: int, H: int, Dk: int, Dv: int, dtype=torch.bfloat16,
                                  num_seqs: int = 0) -> int:
     io = OSDN_BF16 if dtype == torch.bfloat16 else OSDN_F32
+    _fits("osdn_ssm_fwd_workspace_bytes", num_seqs, B, T, H, Dk, Dv)
     return int(LIB.osdn_ssm_fwd_workspace_bytes(num_seqs, B, T, H, Dk, Dv, io))
 
 
@@ -561,6 +571,7 @@ def osdn_ssm_fwd(x, dt, A, b, c, D=None, dt_bias=None, softplus: bool = True, S0
     B, T = x.shape[0], x.shape[1]
     args, H, G, Dk, Dv = _ssm_args(x, dt, A, b, c, D, dt_bias, (B, T), dev)
     cu, num_seqs, N = _packed(cu_seqlens, B, dev)
+    _fits("osdn_ssm_fwd", B, T, H, G, Dk, Dv, N)
     y = torch.empty_like(x) if y is None else _out(y, "y", x.dtype, x.shape, dev)
     if ST is not None or return_ST:
         ST = _out(ST, "ST", torch.float32, (N, H, Dv, Dk), dev)
@@ -579,6 +590,7 @@ def osdn_ssm_step(x, dt, A, b, c, S, D=None, dt_bias=None, softplus: bool = True
     [N, G, Dk]; dt [N, H] float32; S [N, H, Dv, Dk] float32, updated in place.  Returns y."""
     io, dev, N = _io(x), x.device, x.shape[0]
     args, H, G, Dk, Dv = _ssm_args(x, dt, A, b, c, D, dt_bias, (N,), dev)
+    _fits("osdn_ssm_step", N, H, G, Dk, Dv)
     if S is None:
         raise ValueError("S is required")
     y = torch.empty_like(x) if y is None else _out(y, "y", x.dtype, x.shape, dev)
@@ -598,6 +610,7 @@ def osdn_ssm_bwd(x, dt, A, b, c, dy, D=None, dt_bias=None, softplus: bool = True
     B, T = x.shape[0], x.shape[1]
     args, H, G, Dk, Dv = _ssm_args(x, dt, A, b, c, D, dt_bias, (B, T), dev)
     cu, num_seqs, N = _packed(cu_seqlens, B, dev)
+    _fits("osdn_ssm_bwd", B, T, H, G, Dk, Dv, N)
 
     def like(t):
         return None if t is None else torch.empty_like(t)
@@ -641,6 +654,7 @@ def osdn_norm_fwd(f, x=None, gate=None, w_post=None, w_next=None, gate_act: str 
     w_next) skips x_out."""
     io, dev = _io(f), f.device
     args, R, D = _norm_args(f, x, gate, w_post, w_next, dev)
+    _fits("osdn_norm_fwd", D)
     if x_out is not None or return_x_out or w_next is None:
         x_out = torch.empty_like(f) if x_out is None else _out(x_out, "x_out", f.dtype, f.shape, dev)
     if w_next is not None:
@@ -661,6 +675,7 @@ def osdn_norm_bwd(f, dx_out=None, dh=None, x=None, gate=None, w_post=None, w_nex
     in float32; None where the input is."""
     io, dev = _io(f), f.device
     args, R, D = _norm_args(f, x, gate, w_post, w_next, dev)
+    _fits("osdn_norm_bwd", D)
     if (dh is None) != (w_next is None):
         raise ValueError("dh is given exactly when w_next is")
     if dh is None and dx_out is None:
