@@ -22,7 +22,7 @@ constexpr int CONV_MAX_C = 1 << 30;  // a channel's number, rounded up to whole 
 // Channels of a thread.  With 8 (16 bytes of bf16) the filters, the last inputs and the loads in
 // flight leave too few warps: 4 x 4096 tokens of 2048 channels 57 us against 34, the gradient at
 // 8 x 2048 of 1024 115 against 47 (L2 cold).
-template <typename IO> constexpr int CONV_MAX_V = 4;
+constexpr int CONV_MAX_V = 4;
 constexpr int CONV_BWD_MAX_V = 4;
 // resident blocks of the forward kernel on an SM, by the bytes of a thread's access
 constexpr int conv_per_sm(int bytes) { return bytes == 16 ? 5 : 7; }

@@ -94,7 +94,7 @@ osdn_status_t launch_conv_fwd(const void* x, const float* weight, const float* b
                               const void* state0, int silu, void* y, void* stateT,
                               const int32_t* cu, int N, int T, int C, int W, int64_t rows,
                               cudaStream_t stream) {
-    return conv_dispatch<CONV_MAX_V<IO>>(C, W, [&](auto v, auto w) -> osdn_status_t {
+    return conv_dispatch<CONV_MAX_V>(C, W, [&](auto v, auto w) -> osdn_status_t {
         constexpr int V = decltype(v)::value, WW = decltype(w)::value;
         const int64_t gx = ceil_div(C, (int64_t)V * CONV_THREADS);
         int64_t strip = conv_strip(rows, gx, conv_per_sm(V * sizeof(IO)), 64);
@@ -116,7 +116,7 @@ osdn_status_t launch_conv_fwd(const void* x, const float* weight, const float* b
 template <typename IO>
 osdn_status_t launch_conv_step(const void* x, const float* weight, const float* bias, void* state,
                                int silu, void* y, int N, int C, int W, cudaStream_t stream) {
-    return conv_dispatch<CONV_MAX_V<IO>>(C, W, [&](auto v, auto w) -> osdn_status_t {
+    return conv_dispatch<CONV_MAX_V>(C, W, [&](auto v, auto w) -> osdn_status_t {
         constexpr int V = decltype(v)::value, WW = decltype(w)::value;
         const int64_t gx = ceil_div(C, (int64_t)V * CONV_THREADS);
         conv_step_kernel<V, WW, IO><<<dim3((unsigned)gx, (unsigned)(N < 32768 ? N : 32768)),
@@ -214,13 +214,13 @@ osdn_status_t launch_ssm_scan_one(const SsmArgs& a, int64_t slots, int DQ, int D
     if (ctas > 0x7fffffff) return OSDN_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)ctas), block(SSM_THREADS);
     if (DQ == 128 && DV == 128)
-        ssm_scan_kernel<128, 128, MODE, SEG, float><<<grid, block, 0, stream>>>(a);
+        ssm_scan_kernel<128, 128, MODE, SEG><<<grid, block, 0, stream>>>(a);
     else if (DQ == 128)
-        ssm_scan_kernel<128, 64, MODE, SEG, float><<<grid, block, 0, stream>>>(a);
+        ssm_scan_kernel<128, 64, MODE, SEG><<<grid, block, 0, stream>>>(a);
     else if (DV == 128)
-        ssm_scan_kernel<64, 128, MODE, SEG, float><<<grid, block, 0, stream>>>(a);
+        ssm_scan_kernel<64, 128, MODE, SEG><<<grid, block, 0, stream>>>(a);
     else
-        ssm_scan_kernel<64, 64, MODE, SEG, float><<<grid, block, 0, stream>>>(a);
+        ssm_scan_kernel<64, 64, MODE, SEG><<<grid, block, 0, stream>>>(a);
     return launch_status();
 }
 
@@ -402,11 +402,13 @@ osdn_status_t launch_ssm_bwd_f32(const SsmBwdCall& k) {
     a.cu = k.cu; a.rows = k.rows; a.N = (int)k.N; a.T = k.T; a.H = k.H; a.G = k.G;
     a.ckpt = f32(w.ckpt);
     a.gs = f32(w.gs);
+    const float *x = static_cast<const float*>(k.x), *b = static_cast<const float*>(k.b),
+                *c = static_cast<const float*>(k.c), *dy = static_cast<const float*>(k.dy);
     SsmArgs dcp = a, dxp = a, dbp = a;
-    dcp.q = k.dy; dcp.k = k.x; dcp.v = k.b; dcp.S_in = k.S0; dcp.out = f32(w.dch);
+    dcp.q = dy; dcp.k = x; dcp.v = b; dcp.S_in = k.S0; dcp.out = f32(w.dch);
     dcp.vk = k.dD ? f32(w.vk) : nullptr;
-    dxp.q = k.b; dxp.k = k.c; dxp.v = k.dy; dxp.S_in = k.dST; dxp.out = k.dx; dxp.S_out = k.dS0;
-    dbp.q = k.x; dbp.k = k.dy; dbp.v = k.c; dbp.S_in = k.dST; dbp.out = f32(w.dbh);
+    dxp.q = b; dxp.k = c; dxp.v = dy; dxp.S_in = k.dST; dxp.out = static_cast<float*>(k.dx); dxp.S_out = k.dS0;
+    dbp.q = x; dbp.k = dy; dbp.v = c; dbp.S_in = k.dST; dbp.out = f32(w.dbh);
     const SsmSegments sg = ssm_f32_segments(k.rows, k.N, k.T, k.H, k.Dk, k.Dv);
     osdn_status_t st = launch_ssm_scan<SSM_DC>(dcp, sg, k.ws + w.seg, k.Dv, k.Dk, k.stream);
     if (st == OSDN_OK) st = launch_ssm_scan<SSM_DX>(dxp, sg, k.ws + w.seg, k.Dk, k.Dv, k.stream);
@@ -415,9 +417,8 @@ osdn_status_t launch_ssm_bwd_f32(const SsmBwdCall& k) {
     if (k.rows > 0) {
         const int64_t need = ceil_div(k.rows * k.G, 8), cap = 16LL * sm_count();
         const dim3 grid((unsigned)(need < cap ? need : cap));
-        auto kern = k.Dk == 128 ? ssm_group_kernel<128, float> : ssm_group_kernel<64, float>;
-        kern<<<grid, 256, 0, k.stream>>>(f32(w.dch), f32(w.dbh), static_cast<const float*>(k.b),
-                                         static_cast<const float*>(k.c), k.dt, k.dt_bias, k.softplus,
+        auto kern = k.Dk == 128 ? ssm_group_kernel<128> : ssm_group_kernel<64>;
+        kern<<<grid, 256, 0, k.stream>>>(f32(w.dch), f32(w.dbh), b, c, k.dt, k.dt_bias, k.softplus,
                                          static_cast<float*>(k.db), static_cast<float*>(k.dc),
                                          f32(w.pos), f32(w.ri), k.rows, k.H, k.G);
         st = launch_status();
@@ -600,10 +601,6 @@ osdn_status_t osdn_ssm_fwd(const void* x, const float* dt, const float* A, const
     st = check_buffers(in, 9, out, 3);
     if (st != OSDN_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    SsmArgs a = {};
-    a.q = c; a.k = b; a.v = x; a.dt = dt; a.A = A; a.D = D; a.dt_bias = dt_bias; a.S_in = S0;
-    a.out = y; a.S_out = ST; a.cu = cu_seqlens; a.rows = rows; a.N = (int)N; a.T = T; a.H = H;
-    a.G = G; a.softplus = softplus;
     // bf16 tokens run on the tensor cores; fp32 ones, and calls without tokens (states pass
     // through), token by token
     if (io == OSDN_BF16 && rows > 0) {
@@ -619,6 +616,11 @@ osdn_status_t osdn_ssm_fwd(const void* x, const float* dt, const float* A, const
         return Dk == 128 ? launch_tc_fwd<128>(c, b, x, t, sg.slots, s)
                          : launch_tc_fwd<64>(c, b, x, t, sg.slots, s);
     }
+    SsmArgs a = {};
+    a.q = static_cast<const float*>(c); a.k = static_cast<const float*>(b);
+    a.v = static_cast<const float*>(x); a.out = static_cast<float*>(y);
+    a.dt = dt; a.A = A; a.D = D; a.dt_bias = dt_bias; a.S_in = S0; a.S_out = ST; a.cu = cu_seqlens;
+    a.rows = rows; a.N = (int)N; a.T = T; a.H = H; a.G = G; a.softplus = softplus;
     return launch_ssm_scan<SSM_FWD>(a, ssm_f32_segments(rows, N, T, H, Dk, Dv),
                                     static_cast<uint8_t*>(workspace), Dk, Dv, s);
 }

@@ -41,10 +41,10 @@ constexpr int SSM_BLOCK = 64;     // tokens between two restarts of the step gra
 enum { SSM_FWD = 0, SSM_DC = 1, SSM_DX = 2, SSM_DB = 3 };
 
 struct SsmArgs {
-    const void *q, *k, *v;        // io streams [rows][heads][.]
+    const float *q, *k, *v;       // streams [rows][heads][.]
     const float *dt, *A, *D, *dt_bias;
     const float *S_in;            // FWD, DC: S0; DX, DB: dST; may be null
-    void* out;                    // FWD: y, DX: dx (io); DC, DB: fp32 per head [rows][H][DV]
+    float* out;                   // FWD: y, DX: dx; DC, DB: per head [rows][H][DV]
     float* S_out;                 // FWD: ST, DX: dS0; may be null
     float* ckpt;                  // DC writes, DB reads: S behind each block [slot][H][DV][DQ]
     float* gs;                    // DB: <G, S> behind each block [DV / 32][slot][H]
@@ -63,14 +63,13 @@ __host__ __device__ __forceinline__ int64_t ssm_slots(int64_t rows, int64_t N, i
     return rows / block + N + 1;
 }
 
-template <int DQ, int DV, int MODE, bool SEG, typename IO>
+template <int DQ, int DV, int MODE, bool SEG>
 __global__ void __launch_bounds__(SSM_THREADS)
 ssm_scan_kernel(const SsmArgs p) {
     constexpr bool REV = MODE == SSM_DX || MODE == SSM_DB;   // reverse time
     constexpr bool TRANS = MODE == SSM_DC || MODE == SSM_DB; // state rows are key channels
     constexpr int NF = DQ / 16;                              // float4 per thread and state row
     constexpr int LQ = SSM_TT * DQ / 4 / SSM_THREADS;        // float4 of q (k) a thread stages
-    using tr = io_traits<IO>;
     // two tiles: one is worked on while the next is written; gates of 8 tiles at a time
     __shared__ float4 qb[2][SSM_TT][DQ / 4], kb[2][SSM_TT][DQ / 4];
     __shared__ float vb[2][SSM_TT][SSM_BV], ob[2][SSM_TT][SSM_BV];
@@ -102,9 +101,9 @@ ssm_scan_kernel(const SsmArgs p) {
     // v = dy; DB q = x, k = dy, v = c.  b and c have G heads, x and dy H.
     const int qh = TRANS ? p.H : p.G, vh = TRANS ? p.G : p.H;
     const int64_t qstride = (int64_t)qh * DQ, vstride = (int64_t)vh * DV;
-    const IO* q = static_cast<const IO*>(p.q) + (TRANS ? h : g) * DQ;
-    const IO* k = static_cast<const IO*>(p.k) + (TRANS ? h : g) * DQ;
-    const IO* v = static_cast<const IO*>(p.v) + (TRANS ? g : h) * DV + slice * SSM_BV;
+    const float* q = p.q + (TRANS ? h : g) * DQ;
+    const float* k = p.k + (TRANS ? h : g) * DQ;
+    const float* v = p.v + (TRANS ? g : h) * DV + slice * SSM_BV;
     const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
     const float skip = !TRANS && p.D ? p.D[h] : 0.f;
 
@@ -155,14 +154,14 @@ ssm_scan_kernel(const SsmArgs p) {
             const int idx = tid + e * SSM_THREADS, t = idx / (DQ / 4), c4 = idx % (DQ / 4);
             nq[e] = nk[e] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (t0 + t < count) {
-                if constexpr (!SEG) nq[e] = load4<IO>(q + (first + t0 + t) * qstride + c4 * 4);
-                nk[e] = load4<IO>(k + (first + t0 + t) * qstride + c4 * 4);
+                if constexpr (!SEG) nq[e] = load4<float>(q + (first + t0 + t) * qstride + c4 * 4);
+                nk[e] = load4<float>(k + (first + t0 + t) * qstride + c4 * 4);
             }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int t = (tid >> 5) + 4 * e;
-            nv[e] = t0 + t < count ? tr::to_f32(v[(first + t0 + t) * vstride + (tid & 31)]) : 0.f;
+            nv[e] = t0 + t < count ? v[(first + t0 + t) * vstride + (tid & 31)] : 0.f;
         }
     };
     auto put = [&](int64_t i) {    // the fetched tile into its buffer
@@ -326,10 +325,7 @@ ssm_scan_kernel(const SsmArgs p) {
             const int t = (tid >> 5) + 4 * e;
             if (!SEG && t < len && OSDN_IN_BOUNDS(first + t0 + t, p.rows)) {
                 const int64_t at = ((first + t0 + t) * p.H + h) * DV + slice * SSM_BV + (tid & 31);
-                if constexpr (TRANS)
-                    static_cast<float*>(p.out)[at] = os[t][tid & 31];
-                else
-                    static_cast<IO*>(p.out)[at] = tr::from_f32(os[t][tid & 31]);
+                p.out[at] = os[t][tid & 31];
             }
         }
     }
@@ -347,12 +343,12 @@ ssm_scan_kernel(const SsmArgs p) {
 // The heads' shares of dc and db summed over each group, and per head pos = c . dc and the
 // unscaled neg / step = b . db / step.  dch, dbh: [rows][H][DK] fp32, dbh before its factor step.
 // A warp per (row, group).
-template <int DK, typename IO>
+template <int DK>
 __global__ void __launch_bounds__(256)
 ssm_group_kernel(const float* __restrict__ dch, const float* __restrict__ dbh,
-                 const IO* __restrict__ b, const IO* __restrict__ c, const float* __restrict__ dt,
-                 const float* __restrict__ dt_bias, int softplus, IO* __restrict__ db,
-                 IO* __restrict__ dc, float* __restrict__ pos, float* __restrict__ rneg,
+                 const float* __restrict__ b, const float* __restrict__ c, const float* __restrict__ dt,
+                 const float* __restrict__ dt_bias, int softplus, float* __restrict__ db,
+                 float* __restrict__ dc, float* __restrict__ pos, float* __restrict__ rneg,
                  int64_t rows, int H, int G) {
     constexpr int PL = DK / 32;
     const int lane = threadIdx.x & 31, rep = H / G;
@@ -363,8 +359,8 @@ ssm_group_kernel(const float* __restrict__ dch, const float* __restrict__ dbh,
         float bb[PL], cc[PL], sb[PL], sc[PL];
 #pragma unroll
         for (int j = 0; j < PL; j += 2) {
-            const float2 x = load2<IO>(b + u * DK + lane * PL + j);
-            const float2 y = load2<IO>(c + u * DK + lane * PL + j);
+            const float2 x = load2<float>(b + u * DK + lane * PL + j);
+            const float2 y = load2<float>(c + u * DK + lane * PL + j);
             bb[j] = x.x; bb[j + 1] = x.y;
             cc[j] = y.x; cc[j + 1] = y.y;
             sb[j] = sb[j + 1] = sc[j] = sc[j + 1] = 0.f;
@@ -393,8 +389,8 @@ ssm_group_kernel(const float* __restrict__ dch, const float* __restrict__ dbh,
         }
 #pragma unroll
         for (int j = 0; j < PL; j += 2) {
-            store2<IO>(db + u * DK + lane * PL + j, make_float2(sb[j], sb[j + 1]));
-            store2<IO>(dc + u * DK + lane * PL + j, make_float2(sc[j], sc[j + 1]));
+            store2<float>(db + u * DK + lane * PL + j, make_float2(sb[j], sb[j + 1]));
+            store2<float>(dc + u * DK + lane * PL + j, make_float2(sc[j], sc[j + 1]));
         }
     }
 }
