@@ -336,6 +336,10 @@ OSDN_API osdn_status_t osdn_conv_bwd(const void* x, const float* weight, const f
  *   S0, ST  [N,H,Dv,Dk] float32 (as for osdn_chunk_fwd); S0 NULL for zeros, ST NULL to skip.
  *   workspace  osdn_ssm_fwd_workspace_bytes(...) bytes, 256-byte aligned (NULL if that is 0).
  * Dk, Dv in {64, 128}; H <= 65535 and a multiple of G.  y and ST must not overlap anything else.
+ * Values that are not finite: those of other sequences never matter, nor do a later token's b, c or
+ * dt.  With bf16 tokens an x that is not finite makes its head and channel of y not finite for all of
+ * its chunk (128 tokens from the sequence's start on), tokens in front of it included; with float32
+ * tokens from it on.
  */
 OSDN_API size_t osdn_ssm_fwd_workspace_bytes(int32_t num_seqs, int32_t B, int32_t T, int32_t H,
                                              int32_t Dk, int32_t Dv, osdn_dtype_t io);

@@ -193,3 +193,29 @@ def test_scan_outputs_by_norm(osdn, case, forget):  # noqa: F811
     finish(osdn)
     assert relative_l2(y, want["y"]) <= (2.5e-3 if state or max(lens) > 128 else ROUNDED)
     near(ST, want["ST"], 2.0 ** -17 + 2.0 ** -20, "ST")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_scan_of_tokens_that_are_not_finite(osdn, io, bad):  # noqa: F811
+    """What a later token of the same sequence holds does not reach y: b, c and dt not at all, x (of
+    bf16 tokens) only its own head and value channel, within its chunk of 128 tokens."""
+    H, G, D, at, v = 2, 1, 64, 150, 5
+    a, _ = scan_inputs(io, [300], H, G, D, D, True, True, True, True, seed=51)
+    t = scan_dev(a, io, [300], False)
+    y0, _ = scan_fwd(osdn, t)
+    for name in ("b", "c", "dt"):
+        u = dict(t, **{name: t[name].clone()})
+        u[name][0, at, 0] = bad
+        y1, _ = scan_fwd(osdn, u)
+        assert torch.equal(y1[:, :at], y0[:, :at]), name
+        assert not torch.isfinite(y1[:, at, 0].float()).all(), name
+    u = dict(t, x=t["x"].clone())
+    u["x"][0, at, 1, v] = bad
+    y1, _ = scan_fwd(osdn, u)
+    finish(osdn)
+    clean = 128 if io == "bf16" else at
+    assert torch.equal(y1[:, :clean], y0[:, :clean])
+    assert not torch.isfinite(y1[:, at:, 1, v].float()).any()
+    y1[0, clean:, 1, v] = y0[0, clean:, 1, v]
+    assert torch.equal(y1, y0)
