@@ -259,7 +259,8 @@ bool make_chunk_map(CUtensorMap* m, const void* base, int D, int heads, int64_t 
 //   still gives 4 chunks to a segment: the first launch re-reads b and x and costs about half
 //   a chunk's time per chunk (16 heads, Dv=64: 65,536 tokens 252 us, 1321 uncut; 2048 tokens 36, 52
 //   uncut).
-//   Packed sequences, whose lengths the host does not know: twice the tokens that an even split
+//   Packed sequences (more than one: a single one has all T tokens, whether offsets say so or not),
+//   whose lengths the host does not know: twice the tokens that an even split
 //   of the whole would give a CTA, so only sequences far above the average are cut (16 heads,
 //   Dv=64: 300 + 9000 + 200 tokens 91 us, 195 uncut; six of up to 4096 tokens 77, 97 uncut; eight
 //   of 1024, none of them cut, 44, and 37 without the first launch).
@@ -609,7 +610,7 @@ osdn_status_t osdn_ssm_fwd(const void* x, const float* dt, const float* A, const
         t.S_in = S0; t.y = static_cast<__nv_bfloat16*>(y); t.S_out = ST; t.cu = cu_seqlens;
         t.rows = rows; t.N = (int)N; t.T = T; t.H = H; t.G = G; t.softplus = softplus;
         t.nvt = Dv / TCS_BV;
-        const SsmSegments sg = ssm_segments(cu_seqlens != nullptr, rows, N, T, H, Dk, Dv, 1);
+        const SsmSegments sg = ssm_segments(rows != N * T, rows, N, T, H, Dk, Dv, 1);
         t.seg = sg.seg;
         t.seg_state = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sg.state);
         t.seg_decay = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sg.decay);
@@ -631,7 +632,7 @@ size_t osdn_ssm_fwd_workspace_bytes(int32_t num_seqs, int32_t B, int32_t T, int3
         (Dv != 64 && Dv != 128) || (io != OSDN_BF16 && io != OSDN_F32) || (int64_t)B * T == 0)
         return 0;
     const int64_t rows = (int64_t)B * T, N = num_seqs > 0 ? num_seqs : B;
-    return io == OSDN_BF16 ? ssm_segments(num_seqs > 0, rows, N, T, H, Dk, Dv, 1).bytes
+    return io == OSDN_BF16 ? ssm_segments(rows != N * T, rows, N, T, H, Dk, Dv, 1).bytes
                            : ssm_f32_segments(rows, N, T, H, Dk, Dv).bytes;
 }
 

@@ -219,3 +219,16 @@ def test_scan_of_tokens_that_are_not_finite(osdn, io, bad):  # noqa: F811
     assert not torch.isfinite(y1[:, at:, 1, v].float()).any()
     y1[0, clean:, 1, v] = y0[0, clean:, 1, v]
     assert torch.equal(y1, y0)
+
+
+@pytest.mark.parametrize("T", [1100, 3200])
+def test_scan_of_one_sequence_with_offsets(osdn, T):  # noqa: F811
+    """Offsets that say what the shape says: the same segments, the same bits."""
+    a, rng = scan_inputs("bf16", [T], 2, 1, 64, 64, True, True, True, True, seed=52)
+    t, p = scan_dev(a, "bf16", [T], False), scan_dev(a, "bf16", [T], True)
+    dy = dev(rng.standard_normal(t["x"].shape), "bf16")
+    for x, y in zip(scan_fwd(osdn, t), scan_fwd(osdn, p)):
+        assert torch.equal(x, y)
+    g, h = scan_bwd(osdn, t, dy), scan_bwd(osdn, p, dy)
+    finish(osdn)
+    assert all(torch.equal(g[k], h[k]) for k in g)

@@ -61,3 +61,11 @@ def test_sizes_past_32_bits_are_refused(monkeypatch, name):
 def test_workspace_sizes_past_32_bits_are_refused():
     with pytest.raises(osdn.OsdnError):
         osdn.osdn_ssm_fwd_workspace_bytes(1, BIG + 8, 1, 64, 64)
+
+
+@pytest.mark.parametrize("T", [1100, 7112, 65536])
+def test_one_sequence_with_offsets_is_cut_like_one_without(T):
+    """The forward workspace holds the segments' states, so its size tells how a call is cut."""
+    for H in (1, 2, 16):
+        assert (osdn.osdn_ssm_fwd_workspace_bytes(1, T, H, 128, 64, num_seqs=1) ==
+                osdn.osdn_ssm_fwd_workspace_bytes(1, T, H, 128, 64))
