@@ -10,11 +10,16 @@ import torch
 
 from tests import layer_ref as R
 from tests.step_gradient_bounds import bounds, relative_error
-from tests.test_gpu_layer_ops import (E, SCANS, U, close, dev, finish, norm_inputs, osdn,  # noqa: F401
-                                      rounded, scan_bwd, scan_dev, scan_fwd, scan_inputs,
+from tests.test_gpu_layer_ops import (E, NORMS, SCANS, U, close, dev, finish, norm_inputs,  # noqa: F401
+                                      osdn, rounded, scan_bwd, scan_dev, scan_fwd, scan_inputs,
                                       scan_ref)
 
 pytestmark = pytest.mark.gpu
+
+
+def relative_l2(got, want):
+    want = np.asarray(want).reshape(got.shape)
+    return np.linalg.norm(got.detach().double().cpu().numpy() - want) / max(np.linalg.norm(want), 1e-300)
 
 
 # ====================================================================================== norm
@@ -54,6 +59,38 @@ def test_norm_gradients_at_small_scales(osdn, io, res, gate, scale):  # noqa: F8
               np.abs(a["f"]) * np.maximum(1.0, np.abs(a["gate"])), "dgate")
 
 
+@pytest.mark.parametrize("io,Rr,D,gate,first,act,post,res,nxt", NORMS)
+def test_norm_by_norm(osdn, io, Rr, D, gate, first, act, post, res, nxt):  # noqa: F811
+    """Every result in L2 norm: bf16 to its own rounding, fp32 to 2^-18 (gradients 2^-17).  A value passes
+    some 16 products (2^-24 each); a sigmoid is good to 2^-21 (e^-z and a quotient of 2^-22, and z's own
+    rounding, |z| < 5); a row's sum of squares adds 16 values a thread one after another and the threads
+    in a tree, 32 x 2^-24 at most, of which the root takes half: (16 + 8 + 16) 2^-24 < 2^-18.  Gradients
+    pass both a norm's products and its sum twice.  Rows of one value: df = dn (1 - n^2) / rms with
+    1 - n^2 = eps / (f^2 + eps), formed as dn - n (dn n) from products off by 2^-24 of dn each, four of them
+    at most: 4 x 2^-24 (f^2 + eps) / eps more.  Weight gradients sum the rows' terms in fp32, Rr of
+    them, with random signs: another sqrt(Rr) 2^-24."""
+    a, rng = norm_inputs(io, Rr, D, gate, post, res, nxt, seed=22)
+    dxo = rounded(rng.standard_normal((Rr, D)), io)
+    dh = rounded(rng.standard_normal((Rr, D)), io) if nxt else None
+    want = R.norm(a["f"], a["x"], a["gate"], a["w_post"], a["w_next"], act, first, 0.5, 1e-5, dxo, dh)
+    d = {k: dev(v, "f32" if k.startswith("w") else io) for k, v in a.items()}
+    kw = dict(gate_act=act, gate_first=first, scale=0.5, eps=1e-5)
+    xo, h = osdn.osdn_norm_fwd(d["f"], d["x"], d["gate"], d["w_post"], d["w_next"], **kw)
+    g = osdn.osdn_norm_bwd(d["f"], dev(dxo, io), dev(dh, io), d["x"], d["gate"], d["w_post"], d["w_next"], **kw)
+    finish(osdn)
+    half = 1.9e-3 if Rr * D > 500 else 2.0 ** -8
+    for name, got, lim in (("x_out", xo, 2.0 ** -18), ("h", h, 2.0 ** -18), ("df", g["df"], 2.0 ** -17),
+                           ("dx", g["dx"], 2.0 ** -17), ("dgate", g["dgate"], 2.0 ** -17)):
+        if got is not None:
+            lim = half if io == "bf16" else lim
+            if name == "df" and D == 1:
+                lim += 4 * E * (a["f"].max() ** 2 + 1e-5) / 1e-5
+            assert relative_l2(got, want[name]) <= lim, name
+    for name in ("dw_post", "dw_next"):
+        if g[name] is not None and D > 1:
+            assert relative_l2(g[name], want[name]) <= 2.0 ** -17 + Rr ** 0.5 * E, name
+
+
 # ====================================================================================== scan
 def near(got, want, tol, name):
     """Per head (the axis in front of the last two, the last of 1- and 2-d results): the L2 norm of the
@@ -65,11 +102,6 @@ def near(got, want, tol, name):
     lim = tol * norm(want) if np.ndim(tol) == 0 else tol
     assert np.all(np.isfinite(got)), name
     assert np.all(norm(got - want) <= lim + 1e-30), (name, norm(got - want), lim)
-
-
-def relative_l2(got, want):
-    want = np.asarray(want).reshape(got.shape)
-    return np.linalg.norm(got.detach().double().cpu().numpy() - want) / max(np.linalg.norm(want), 1e-300)
 
 
 def step_gradients(g, want, a, io, softplus, lens, dy, dST):
