@@ -8,9 +8,14 @@
 // exponential and a quotient).  A thread owns V neighbouring channels, as pairs per instruction,
 // and walks a strip of consecutive tokens with the last W - 1 inputs in registers, so x is read
 // once plus W - 1 rows per strip (which sit in L2), the next four tokens' loads in flight.
-// Bound by HBM up to two thirds, then by the issue of silu: 31 us at 4 x 4096 tokens of 2048 bf16
-// channels (134 MB: 20.5 us at copy speed).  The gradient costs 4 W + some 20 operations a value
-// and is bound by issue: 43 us at 8 x 2048 tokens of 1024 channels (101 MB: 15.4 us).
+// 31 us at 4 x 4096 tokens of 2048 bf16 channels (134 MB: 20.5 us at copy speed): too few warps wait,
+// no unit is full.  14 instructions issued a value take 46% of the schedulers' slots, and of the 11
+// cycles between two of a warp's instructions 2.3 are waits for loads, 1.9 for the queue of the special
+// functions (silu's exponential and quotient) and 1.9 for fixed latencies, with 5 warps a scheduler.
+// The gradient takes 43 us at 8 x 2048 tokens of 1024 channels (101 MB: 15.4 us), 37 of them in the
+// kernel: 27 instructions a value take 39% of the slots, and of a warp's 9.8 cycles 3.8 are waits for
+// loads.  Its 128 registers leave 16 warps an SM, and with W = 4 some are spilled (24 bytes with bf16
+// tokens, 48 with fp32 dy, 120 with fp32 tokens).  The sum of the partial rows takes the rest.
 #pragma once
 
 #include "mixer_common.cuh"

@@ -257,17 +257,18 @@ bool make_chunk_map(CUtensorMap* m, const void* base, int D, int heads, int64_t 
 // does not need a device) take one CTA each.
 //   Equal sequences: as many segments each as keep every CTA on an SM of its own, if a sequence
 //   still gives 4 chunks to a segment: the first launch re-reads b and x and costs about half
-//   a chunk's time per chunk (16 heads, Dv=64: 65,536 tokens 252 us, 1321 uncut; 2048 tokens 36, 52
+//   a chunk's time per chunk (16 heads, Dv=64: 65,536 tokens 267 us, 1403 uncut; 2048 tokens 35, 53
 //   uncut).
 //   Packed sequences (more than one: a single one has all T tokens, whether offsets say so or not),
 //   whose lengths the host does not know: twice the tokens that an even split
 //   of the whole would give a CTA, so only sequences far above the average are cut (16 heads,
-//   Dv=64: 300 + 9000 + 200 tokens 91 us, 195 uncut; six of up to 4096 tokens 77, 97 uncut; eight
-//   of 1024, none of them cut, 44, and 37 without the first launch).
+//   Dv=64: 300 + 9000 + 200 tokens 96 us, 205 uncut; six of up to 4096 tokens 78, 100 uncut; eight
+//   of 1024, none of them cut, 43, and 37 without the first launch).
 //   The backward pass's chains go both ways (dirs 2), a CTA each, and their first launch costs
-//   more (three terms of V'): three segments of 8 chunks at least (B=1, T=7112, H=16, Dv=64: 252
-//   us uncut, 216 in four; two segments at T=2048: 85 uncut, 96 cut), and packed sequences stay
-//   whole (six of up to 4096 tokens, H=16: 229, cut 263).
+//   more (three terms of V'): three segments of 8 chunks at least (B=1, T=7112, H=16, Dv=64: 266
+//   us uncut, 225 in four; two segments at T=2048: 96 uncut, 103 cut), and packed sequences stay
+//   whole (six of up to 4096 tokens, H=16: 242, cut 279; a few long ones with few heads lose by it: two
+//   of 16,384 tokens with H=2 317, cut 172).
 SsmSegments ssm_segments(bool packed, int64_t rows, int64_t N, int64_t T, int H, int Dk, int Dv,
                          int dirs) {
     const int64_t nvt = dirs * Dv / TCS_BV, chunks = ceil_div(packed ? rows : T, TCS_L), sms = 148;

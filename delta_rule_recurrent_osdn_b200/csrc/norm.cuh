@@ -11,9 +11,16 @@
 // Some 20 operations per element and two to four sums over the row: bound by HBM if those stay
 // cheap, so a row is held in the registers of TPR threads, sums go by shuffles (and through shared
 // memory when a row takes several warps), and the next row's loads are in flight while one is
-// worked on.  Forward: 57 us at 16384 bf16 rows of 2048 with residual, gate and both norms (336 MB:
-// 51 us at copy speed).  Backward: 47 us at 131,072 rows of 128 with a gate (168 MB: 26 us), bound
-// by issue: some 40 operations a value, and sums of weight gradients that cross rows.
+// worked on.  Forward: 59 us at 16384 bf16 rows of 2048 with residual, gate and both norms (336 MB:
+// 51 us at copy speed).  Backward: 47 us at 131,072 rows of 128 with a gate (168 MB: 26 us).  38 of
+// them are the kernel, at 66% of the schedulers' slots (47 instructions a value) and with the waits of 5
+// warps a scheduler for the rest; then 740 partial rows of weight gradients are added by 4 blocks, a
+// chain of 92 loads a warp (13 us with cold caches).  142 us at 16384 rows of 2048 with both norms (537 MB:
+// 82 us): 76 instructions a value at 57% of the slots, and four sums across the warps of a row.
+// Registers are the limit of the gradient: up to 128, and the forms with the second norm spill for
+// fp32 rows (44 bytes and more), wherever D is not a multiple of 8 (112 to 180 bytes) and above 4096
+// columns (224 to 344 bytes); without it the fp32 forms, those above 4096 columns and those of
+// other D spill 8 to 136 bytes.
 #pragma once
 
 #include "mixer_common.cuh"

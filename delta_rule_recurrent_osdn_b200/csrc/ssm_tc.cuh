@@ -34,10 +34,10 @@
 // Warp roles: 0 TMA loads (two tiles each of C, B and X), 1 MMA issue, 2-3 the gates (softplus,
 // sums of log decays), 4-7 the state, 8-15 V', 16-19 the output rows, 20-27 P.  (V' by one
 // warpgroup is on the chain from one state to the next: 99 against 96 us at B=4, T=4096, H=16,
-// Dk=Dv=128, 261 against 246 at T=65,536 with Dv=64.)
-// Bound by the chain: about 3 us a chunk at 4096 tokens (four products wait for one another
-// through shared and tensor memory, and the P and output warps issue some 2000 instructions a
-// scheduler), 96 us against 42 for its 274 MB at copy speed.
+// Dk=Dv=128, 261 against 246 at T=65,536 with Dv=64, both with P as one term.)
+// Bound by the chain: 3.4 us a chunk at 4096 tokens (four products wait for one another
+// through shared and tensor memory, with the element-wise work of P, V' and the output rows in
+// between), 115 us against 42 for its 274 MB at copy speed.
 // Hand-offs are mbarriers with bounded waits; a role that gives up leaves its loop, the others
 // run into their own bounds, and everything in flight is waited for before the CTA leaves.
 #pragma once

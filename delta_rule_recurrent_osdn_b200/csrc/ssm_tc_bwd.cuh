@@ -28,8 +28,8 @@
 // Warps 0-15: element-wise work, thread = row, the four warpgroups taking every fourth 16-column
 // sub-block of scores and a quarter of the outputs' columns; warp 16: loads and MMAs; 17: gates.
 // The images' terms pass through two slots of shared memory, each loaded again once used up.
-// 340M layer (B=8, T=2048, H=8, 128 x 128): 112 us for 364 MB read and 82 written, seven rounds
-// of CTAs at 16 us each.  A CTA's products, its element-wise work and its stores follow one
+// 340M layer (B=8, T=2048, H=8, 128 x 128): 131 us for 361 MB read and 81 written, seven rounds
+// of CTAs at 19 us each (16 with one term of the weighted scores and two in <R, S>).  A CTA's products, its element-wise work and its stores follow one
 // another, and shared memory (four tiles, two terms) leaves room for one CTA on an SM.
 #pragma once
 
@@ -173,8 +173,8 @@ ssm_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             load_term(1, imr + L::TERM);
             // What the CTA that follows here about a round later will load, into L2 meanwhile: its
             // first loads then do not wait for HBM.  Asked for once this CTA's own loads (all but
-            // one term) are under way, which would stand in line behind it: 121 us at the 340M
-            // shape, 135 when asked for at the start, 156 without.
+            // one term) are under way, which would stand in line behind it: 226 us at the 340M
+            // shape (the whole gradient), 243 when asked for at the start, 230 without.
             const int64_t ahead = (int64_t)blockIdx.x + p.round, aslot = ahead / p.H;
             const int ah = (int)(ahead - aslot * p.H), ag = ah / (p.H / p.G);
             int an, achunk;

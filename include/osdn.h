@@ -363,7 +363,8 @@ OSDN_API osdn_status_t osdn_ssm_step(const void* x, const float* dt, const float
  * Backward pass of osdn_ssm_fwd, given dy [B,T,H,Dv] io dtype and dST [N,H,Dv,Dk] float32 (NULL
  * for 0).  Written: dx [B,T,H,Dv], db, dc [B,T,G,Dk] io dtype; ddt [B,T,H], dA [H] float32;
  * dD, ddt_bias [H], dS0 [N,H,Dv,Dk] float32, each NULL to skip.
- *   workspace  osdn_ssm_bwd_workspace_bytes(...) bytes, 256-byte aligned.
+ *   workspace  osdn_ssm_bwd_workspace_bytes(...) bytes, 256-byte aligned.  (The size is enough for any
+ *   G; with G == H, 8 * B * T * H * Dk bytes of it are not touched with bf16 tokens.)
  */
 OSDN_API size_t osdn_ssm_bwd_workspace_bytes(int32_t num_seqs, int32_t B, int32_t T, int32_t H,
                                              int32_t Dk, int32_t Dv, osdn_dtype_t io);
